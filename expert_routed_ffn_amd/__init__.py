@@ -1,5 +1,6 @@
 """Python binding of libbeam_moe.so: one Beam-style MoE layer forward on
-MI355X (gfx950).
+MI355X (gfx950), and the attention sublayer beside it (per-head query/key
+norm with the position rotation, a paged key-value cache, one-token decode).
 
 The functions below carry the C entry points' names and do argument
 marshalling only: they check that the torch tensors are contiguous device
@@ -32,7 +33,8 @@ SYMBOLS = ("beam_moe_route", "beam_moe_permute", "beam_moe_quantize_fp8", "beam_
            "beam_moe_experts_static", "beam_moe_combine_norm", "beam_moe_norm_boundary",
            "beam_moe_permute_shard", "beam_moe_combine_partial", "beam_moe_dense_mlp",
            "beam_moe_dense_workspace_bytes", "beam_moe_pack_weights", "beam_moe_workspace_bytes",
-           "beam_moe_status_string")
+           "beam_moe_status_string", "beam_moe_qk_norm_rope", "beam_moe_qk_norm_rope_cache", "beam_moe_kv_write",
+           "beam_moe_kv_read", "beam_moe_attn_decode", "beam_moe_attn_workspace_bytes")
 STATIC_SCRATCH_BYTES = 64 << 20   # BEAM_MOE_STATIC_SCRATCH_BYTES
 
 
@@ -60,6 +62,45 @@ class LayerCfg:
     def c(self) -> BeamMoeCfg:
         return BeamMoeCfg(self.hidden, self.n_experts, self.n_groups, self.topk_groups, self.topk,
                           self.group_topn, self.d_ff, self.routed_scale, self.rms_eps)
+
+
+class BeamMoeAttnCfg(ctypes.Structure):
+    _fields_ = [("n_heads", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("rope_dim", ctypes.c_int32), ("rope_interleaved", ctypes.c_int32), ("window", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("ssmax_len", ctypes.c_float), ("ssmax_exp", ctypes.c_float),
+                ("softmax_scale", ctypes.c_float), ("rms_eps", ctypes.c_float)]
+
+
+class BeamMoeKvCache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("n_pages", ctypes.c_int32), ("dtype", ctypes.c_int32)]
+
+
+@dataclasses.dataclass(frozen=True)
+class AttnCfg:
+    """Shape of one attention sublayer.  Beam defaults: a rotary
+    sliding-window layer.  Its full-attention layers have rope_dim=0,
+    window=0 and ssmax_len=2048."""
+    n_heads: int = 48
+    n_kv_heads: int = 8
+    head_dim: int = 128
+    rope_dim: int = 128
+    rope_interleaved: bool = False
+    window: int = 512
+    page_size: int = 64
+    ssmax_len: float = 0.0
+    ssmax_exp: float = 0.1
+    softmax_scale: float = 128 ** -0.5
+    rms_eps: float = 1e-6
+
+    def __post_init__(self):
+        c = BeamMoeAttnCfg(self.n_heads, self.n_kv_heads, self.head_dim, self.rope_dim,
+                           int(self.rope_interleaved), self.window, self.page_size, self.ssmax_len,
+                           self.ssmax_exp, self.softmax_scale, self.rms_eps)
+        object.__setattr__(self, "_c", c)
+
+    def c(self) -> BeamMoeAttnCfg:
+        return self._c
 
 
 class BeamError(RuntimeError):
@@ -99,12 +140,22 @@ def lib() -> ctypes.CDLL:
     L.beam_moe_pack_weights.argtypes = [cfgp, i32, i32, vp, vp, vp, vp, vp]
     L.beam_moe_workspace_bytes.argtypes = [cfgp, i32, i32]
     L.beam_moe_workspace_bytes.restype = sz
+    acfgp, cachep, i64 = ctypes.POINTER(BeamMoeAttnCfg), ctypes.POINTER(BeamMoeKvCache), ctypes.c_int64
+    L.beam_moe_qk_norm_rope.argtypes = [acfgp, i32, vp, i64, vp, i64, i32, vp, vp, vp, vp, vp, vp, vp]
+    L.beam_moe_qk_norm_rope_cache.argtypes = [acfgp, i32, vp, i64, vp, i64, vp, i64, i32, vp, vp, vp, vp, vp, vp,
+                                              cachep, vp]
+    L.beam_moe_kv_write.argtypes = [acfgp, i32, vp, i64, vp, i64, i32, vp, cachep, vp]
+    L.beam_moe_kv_read.argtypes = [acfgp, i32, i32, cachep, vp, i32, vp, vp, vp, vp, i32, vp]
+    L.beam_moe_attn_decode.argtypes = [acfgp, i32, vp, i64, i32, cachep, vp, i32, vp, i32, vp, vp, vp, sz, vp]
+    L.beam_moe_attn_workspace_bytes.argtypes = [acfgp, i32, i32]
+    L.beam_moe_attn_workspace_bytes.restype = sz
     L.beam_moe_status_string.argtypes = [i32]
     L.beam_moe_status_string.restype = ctypes.c_char_p
     for f in ("beam_moe_route", "beam_moe_permute", "beam_moe_quantize_mx", "beam_moe_experts",
               "beam_moe_experts_static", "beam_moe_combine_norm", "beam_moe_norm_boundary",
               "beam_moe_permute_shard", "beam_moe_combine_partial", "beam_moe_dense_mlp",
-              "beam_moe_pack_weights"):
+              "beam_moe_pack_weights", "beam_moe_qk_norm_rope", "beam_moe_qk_norm_rope_cache", "beam_moe_kv_write",
+              "beam_moe_kv_read", "beam_moe_attn_decode"):
         getattr(L, f).restype = i32
     _lib = L
     return L
@@ -492,3 +543,233 @@ def moe_layer(cfg: LayerCfg, x, w_router, bias, w_gate_up, w_down, h, gamma_post
                      s_down=s_down, ws=bufs.ws, stream=stream)
     beam_moe_combine_norm(cfg, bufs.y, bufs.pair_row, bufs.topk_w, h, bufs.x_next, gamma_post,
                           gamma_pre, n, bufs.moe_out, stream)
+
+
+# ------------------------------------------------------------------ attention sublayer
+
+_ACTS = (torch.bfloat16, torch.float32)
+_CODES = (torch.uint8, torch.float8_e4m3fn)
+
+
+def _on(dev, t, shape, dtypes, name):
+    """Pointer of a dense tensor of this shape on `dev`."""
+    if t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)} != {tuple(shape)}")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name}: dtype {t.dtype} not in {dtypes}")
+    if t.device != dev:
+        raise ValueError(f"{name}: on {t.device}, not on {dev}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: must be contiguous")
+    return t.data_ptr()
+
+
+def _heads(dev, t, T, heads, dim, dtype, name):
+    """Pointer and row stride of [T, heads, dim] rows whose heads are adjacent
+    (a dense tensor or columns of a wider row-major matrix)."""
+    if t.shape != (T, heads, dim):
+        raise ValueError(f"{name}: shape {tuple(t.shape)} != {(T, heads, dim)}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name}: dtype {t.dtype} != {dtype}")
+    if t.device != dev:
+        raise ValueError(f"{name}: on {t.device}, not on {dev}")
+    row, head, one = t.stride()
+    if one != 1 or (head != dim and heads > 1):
+        raise ValueError(f"{name}: the heads of a token must be adjacent")
+    return t.data_ptr(), (row if T > 1 else heads * dim)
+
+
+def _gpu(t):
+    if not t.is_cuda:
+        raise ValueError("tensors must live on the GPU")
+    return t.device
+
+
+def _launch(fn, dev, stream, *args):
+    """Calls an entry point with the device of its tensors current, on
+    `stream` (default: that device's current stream)."""
+    if isinstance(stream, torch.cuda.Stream) and stream.device != dev:
+        raise ValueError(f"stream of {stream.device} for tensors on {dev}")
+    f = getattr(lib(), fn)
+    if dev.index == torch.cuda.current_device():
+        st = f(*args, _stream(stream))
+    else:
+        with torch.cuda.device(dev):
+            st = f(*args, _stream(stream))
+    _ok(fn, st)
+
+
+@dataclasses.dataclass(frozen=True)
+class KVCache:
+    """The paged key-value cache of one layer: k, v [n_pages, n_kv_heads,
+    page_size, head_dim] in bf16, fp32 or e4m3 codes (float8_e4m3fn or
+    uint8); the codes with fp32 scales [n_pages, n_kv_heads, page_size]."""
+    k: torch.Tensor
+    v: torch.Tensor
+    k_scale: torch.Tensor | None = None
+    v_scale: torch.Tensor | None = None
+
+    def __post_init__(self):
+        k, v = self.k, self.v
+        dev = _gpu(k)
+        if k.dim() != 4:
+            raise ValueError(f"k: {k.dim()} dims, not [n_pages, n_kv_heads, page_size, head_dim]")
+        kp = _on(dev, k, k.shape, _ACTS + _CODES, "k")
+        vp = _on(dev, v, k.shape, (k.dtype,), "v")
+        ks = vs = None
+        if k.dtype in _CODES:
+            if self.k_scale is None or self.v_scale is None:
+                raise ValueError("e4m3 codes need k_scale and v_scale")
+            ks = _on(dev, self.k_scale, k.shape[:3], (torch.float32,), "k_scale")
+            vs = _on(dev, self.v_scale, k.shape[:3], (torch.float32,), "v_scale")
+        elif self.k_scale is not None or self.v_scale is not None:
+            raise ValueError("scales go with e4m3 codes only")
+        object.__setattr__(self, "_c", BeamMoeKvCache(kp, vp, ks, vs, k.shape[0], _dt(k)))
+
+    def c(self, cfg: AttnCfg, dev) -> BeamMoeKvCache:
+        if self.k.shape[1:] != (cfg.n_kv_heads, cfg.page_size, cfg.head_dim):
+            raise ValueError(f"cache pages {tuple(self.k.shape[1:])} != "
+                             f"{(cfg.n_kv_heads, cfg.page_size, cfg.head_dim)}")
+        if self.k.device != dev:
+            raise ValueError(f"cache on {self.k.device}, not on {dev}")
+        return self._c
+
+
+def kv_cache(cfg: AttnCfg, n_pages: int, dtype: int, device="cuda") -> KVCache:
+    """An empty cache (its contents are undefined until written)."""
+    shape = (n_pages, cfg.n_kv_heads, cfg.page_size, cfg.head_dim)
+    t = {BEAM_F32: torch.float32, BEAM_BF16: torch.bfloat16, BEAM_FP8_E4M3: torch.float8_e4m3fn}[dtype]
+    k, v = torch.empty(shape, dtype=t, device=device), torch.empty(shape, dtype=t, device=device)
+    if dtype != BEAM_FP8_E4M3:
+        return KVCache(k, v)
+    return KVCache(k, v, torch.empty(shape[:3], dtype=torch.float32, device=device),
+                   torch.empty(shape[:3], dtype=torch.float32, device=device))
+
+
+def _prep(cfg, q, k, positions, inv_freq, gamma_q, gamma_k, q_out):
+    """Checks and arguments that both norm/rotation calls share."""
+    dev = _gpu(q)
+    T, dt, D = q.shape[0], q.dtype, cfg.head_dim
+    if dt not in _ACTS:
+        raise ValueError(f"q: dtype {dt} not in {_ACTS}")
+    qp, qs = _heads(dev, q, T, cfg.n_heads, D, dt, "q")
+    kp, ks = _heads(dev, k, T, cfg.n_kv_heads, D, dt, "k")
+    gq = None if gamma_q is None else _on(dev, gamma_q, (D,), (dt,), "gamma_q")
+    gk = None if gamma_k is None else _on(dev, gamma_k, (D,), (dt,), "gamma_k")
+    pp = _on(dev, positions, (T,), (torch.int32,), "positions")
+    fp = None
+    if cfg.rope_dim:
+        if inv_freq is None:
+            raise ValueError("inv_freq: needed for rope_dim > 0")
+        fp = _on(dev, inv_freq, (cfg.rope_dim // 2,), (torch.float32,), "inv_freq")
+    qo = _on(dev, q_out, q.shape, (dt,), "q_out")
+    return dev, T, dt, qp, qs, kp, ks, gq, gk, pp, fp, qo
+
+
+def beam_moe_qk_norm_rope(cfg: AttnCfg, q, k, positions, q_out, k_out, inv_freq=None, gamma_q=None, gamma_k=None,
+                          stream=None):
+    """Per-head RMSNorm of q [T,n_heads,D] and k [T,n_kv_heads,D], the
+    rotation by positions [T] and the queries' position factor, into dense
+    q_out and k_out.  q and k may be columns of a merged projection."""
+    dev, T, dt, qp, qs, kp, ks, gq, gk, pp, fp, qo = _prep(cfg, q, k, positions, inv_freq, gamma_q, gamma_k, q_out)
+    ko = _on(dev, k_out, k.shape, (dt,), "k_out")
+    _launch("beam_moe_qk_norm_rope", dev, stream, cfg.c(), T, qp, qs, kp, ks, _dt(q), gq, gk, pp, fp, qo, ko)
+
+
+def beam_moe_qk_norm_rope_cache(cfg: AttnCfg, q, k, v, positions, slots, q_out, cache: KVCache, inv_freq=None,
+                                gamma_q=None, gamma_k=None, stream=None):
+    """The same for q; k (normed and rotated) and v go into the cache at
+    slots [T] (page * page_size + place; -1: not stored)."""
+    dev, T, dt, qp, qs, kp, ks, gq, gk, pp, fp, qo = _prep(cfg, q, k, positions, inv_freq, gamma_q, gamma_k, q_out)
+    vp, vs = _heads(dev, v, T, cfg.n_kv_heads, cfg.head_dim, dt, "v")
+    sp = _on(dev, slots, (T,), (torch.int32,), "slots")
+    _launch("beam_moe_qk_norm_rope_cache", dev, stream, cfg.c(), T, qp, qs, kp, ks, vp, vs, _dt(q), gq, gk, pp, fp,
+            sp, qo, cache.c(cfg, dev))
+
+
+def beam_moe_kv_write(cfg: AttnCfg, k, v, slots, cache: KVCache, stream=None):
+    """Stores ready rows k, v [T,n_kv_heads,D] at slots [T]."""
+    dev = _gpu(k)
+    T, dt = k.shape[0], k.dtype
+    if dt not in _ACTS:
+        raise ValueError(f"k: dtype {dt} not in {_ACTS}")
+    kp, ks = _heads(dev, k, T, cfg.n_kv_heads, cfg.head_dim, dt, "k")
+    vp, vs = _heads(dev, v, T, cfg.n_kv_heads, cfg.head_dim, dt, "v")
+    sp = _on(dev, slots, (T,), (torch.int32,), "slots")
+    _launch("beam_moe_kv_write", dev, stream, cfg.c(), T, kp, ks, vp, vs, _dt(k), sp, cache.c(cfg, dev))
+
+
+def beam_moe_kv_read(cfg: AttnCfg, cache: KVCache, page_table, row_offsets, k_out, v_out, first=None, stream=None):
+    """Rows row_offsets[b] .. row_offsets[b+1]-1 of k_out, v_out
+    [N,n_kv_heads,D] get the tokens first[b] (default 0), first[b]+1, ... of
+    sequence b of page_table [B,max_pages]; rows behind row_offsets[B] stay."""
+    dev = _gpu(k_out)
+    N, dt, B = k_out.shape[0], k_out.dtype, page_table.shape[0]
+    shape = (N, cfg.n_kv_heads, cfg.head_dim)
+    ko = _on(dev, k_out, shape, _ACTS, "k_out")
+    vo = _on(dev, v_out, shape, (dt,), "v_out")
+    tp = _on(dev, page_table, (B, page_table.shape[1]), (torch.int32,), "page_table")
+    op = _on(dev, row_offsets, (B + 1,), (torch.int32,), "row_offsets")
+    fp = None if first is None else _on(dev, first, (B,), (torch.int32,), "first")
+    _launch("beam_moe_kv_read", dev, stream, cfg.c(), B, N, cache.c(cfg, dev), tp, page_table.shape[1], op, fp, ko,
+            vo, _dt(k_out))
+
+
+def attn_workspace(cfg: AttnCfg, B: int, max_len: int, device="cuda") -> torch.Tensor:
+    n = int(lib().beam_moe_attn_workspace_bytes(cfg.c(), B, max_len))
+    return torch.empty(max(n, 256), dtype=torch.uint8, device=device)
+
+
+def beam_moe_attn_decode(cfg: AttnCfg, q, cache: KVCache, page_table, seq_lens, max_len: int, out, ws, lse=None,
+                         stream=None):
+    """Attention of one new token per sequence: q [B,n_heads,D] over the
+    cached tokens of page_table [B,max_pages] and seq_lens [B], into out
+    [B,n_heads,D] (and lse [B,n_heads] fp32).  max_len: the longest length to
+    expect; ws from attn_workspace(cfg, B, max_len)."""
+    dev = _gpu(q)
+    B, dt = q.shape[0], q.dtype
+    if dt not in _ACTS:
+        raise ValueError(f"q: dtype {dt} not in {_ACTS}")
+    qp, qs = _heads(dev, q, B, cfg.n_heads, cfg.head_dim, dt, "q")
+    tp = _on(dev, page_table, (B, page_table.shape[1]), (torch.int32,), "page_table")
+    lp = _on(dev, seq_lens, (B,), (torch.int32,), "seq_lens")
+    op = _on(dev, out, q.shape, (dt,), "out")
+    ep = None if lse is None else _on(dev, lse, (B, cfg.n_heads), (torch.float32,), "lse")
+    wp = None if ws is None else _on(dev, ws, ws.shape, (torch.uint8,), "ws")
+    _launch("beam_moe_attn_decode", dev, stream, cfg.c(), B, qp, qs, _dt(q), cache.c(cfg, dev), tp,
+            page_table.shape[1], lp, max_len, op, ep, wp, 0 if ws is None else ws.numel())
+
+
+@dataclasses.dataclass
+class AttnBuffers:
+    """Device outputs and scratch of one decode attention for B sequences."""
+    q: torch.Tensor
+    out: torch.Tensor
+    lse: torch.Tensor | None
+    ws: torch.Tensor
+
+
+def attn_buffers(cfg: AttnCfg, B: int, max_len: int, act_dtype=torch.bfloat16, keep_lse=False,
+                 device="cuda") -> AttnBuffers:
+    shape = (B, cfg.n_heads, cfg.head_dim)
+    return AttnBuffers(q=torch.empty(shape, dtype=act_dtype, device=device),
+                       out=torch.empty(shape, dtype=act_dtype, device=device),
+                       lse=torch.empty(shape[:2], dtype=torch.float32, device=device) if keep_lse else None,
+                       ws=attn_workspace(cfg, B, max_len, device))
+
+
+def attn_layer(cfg: AttnCfg, qkv, positions, slots, cache: KVCache, page_table, seq_lens, max_len: int,
+               bufs: AttnBuffers, inv_freq=None, gamma_q=None, gamma_k=None, stream=None):
+    """The attention of one decode step between its two projections: qkv
+    [B, (n_heads + 2 n_kv_heads) * D] is the merged projection of the step's
+    tokens; their keys and values go into the cache at `slots`, then every
+    token attends to the seq_lens [B] tokens of its sequence, itself
+    included.  The result lands in bufs.out [B,n_heads,D]; its output
+    projection is the m of beam_moe_norm_boundary."""
+    B, hq, hkv, D = qkv.shape[0], cfg.n_heads, cfg.n_kv_heads, cfg.head_dim
+    if qkv.shape != (B, (hq + 2 * hkv) * D):
+        raise ValueError(f"qkv: shape {tuple(qkv.shape)} != {(B, (hq + 2 * hkv) * D)}")
+    rows = qkv.view(B, hq + 2 * hkv, D)
+    beam_moe_qk_norm_rope_cache(cfg, rows[:, :hq], rows[:, hq:hq + hkv], rows[:, hq + hkv:], positions, slots,
+                                bufs.q, cache, inv_freq, gamma_q, gamma_k, stream)
+    beam_moe_attn_decode(cfg, bufs.q, cache, page_table, seq_lens, max_len, bufs.out, bufs.ws, bufs.lse, stream)

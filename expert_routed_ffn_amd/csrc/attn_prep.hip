@@ -1,0 +1,312 @@
+// What goes into the attention: per-head RMSNorm of queries and keys, the
+// position rotation, the queries' position factor, and the paged key-value
+// cache (written in bf16, fp32 or e4m3, and read back).
+// (TokenSpeed x Reflection Beam blog, "Architecture", and vLLM Beam summary,
+//  kernel list: QK norm + rotation or position factor in one kernel with the
+//  cache write.)
+//
+// A head row is spread over D/8 lanes of 8 consecutive elements, so a wave
+// holds 512/D heads, a row's sums take log2(D/8) lane exchanges and every
+// access is 16 bytes of bf16 per lane.
+#include "common.h"
+#include "kernels.h"
+
+namespace beam {
+
+// ---------------------------------------------------------------- 8 elements
+
+template <bool BF> struct Raw8;
+template <> struct Raw8<true> { uint4 v; };
+template <> struct Raw8<false> { float4 a, b; };
+
+template <bool BF> BEAM_DEV Raw8<BF> ld8(const void* p, size_t i) {
+    Raw8<BF> r;
+    if constexpr (BF) {
+        r.v = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + i);
+    } else {
+        const float4* f = reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
+        r.a = f[0];
+        r.b = f[1];
+    }
+    return r;
+}
+BEAM_DEV void wid8(const Raw8<true>& r, float (&x)[8]) {
+    const uint32_t w[4] = {r.v.x, r.v.y, r.v.z, r.v.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        x[2 * j] = __uint_as_float(w[j] << 16);
+        x[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+    }
+}
+BEAM_DEV void wid8(const Raw8<false>& r, float (&x)[8]) {
+    x[0] = r.a.x; x[1] = r.a.y; x[2] = r.a.z; x[3] = r.a.w;
+    x[4] = r.b.x; x[5] = r.b.y; x[6] = r.b.z; x[7] = r.b.w;
+}
+template <bool BF> BEAM_DEV void st8(void* p, size_t i, const float (&x)[8]) {
+    if constexpr (BF) {
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + i) =
+            make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
+                       pack_bf16x2(x[6], x[7]));
+    } else {
+        float4* f = reinterpret_cast<float4*>(static_cast<float*>(p) + i);
+        f[0] = make_float4(x[0], x[1], x[2], x[3]);
+        f[1] = make_float4(x[4], x[5], x[6], x[7]);
+    }
+}
+
+// sum / maximum over the LPH lanes that hold one head row
+template <int LPH> BEAM_DEV float head_sum(float v) {
+#pragma unroll
+    for (int o = LPH / 2; o > 0; o >>= 1) v += __shfl_xor(v, o, kWave);
+    return v;
+}
+template <int LPH> BEAM_DEV float head_max(float v) {
+#pragma unroll
+    for (int o = LPH / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor(v, o, kWave));
+    return v;
+}
+
+// Stores a head row's 8 elements of this lane at row `row` of one cache
+// side.  e4m3: the scale and codes that quantize_row_e4m3_wave gives a row.
+template <int CK, int D>
+BEAM_DEV void store_cache(void* side, float* scales, size_t row, int e0, const float (&x)[8], bool live) {
+    if constexpr (CK == A_FP8) {
+        float amax = 0.f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(x[j]));
+        amax = head_max<D / 8>(amax);   // every lane takes part
+        const float s = amax > 0.f ? __fdiv_rn(amax, 448.0f) : 1.0f;
+        if (!live) return;
+        float y[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) y[j] = __fdiv_rn(x[j], s);
+        *reinterpret_cast<uint2*>(static_cast<uint8_t*>(side) + row * D + e0) =
+            make_uint2(e4m3x4(y[0], y[1], y[2], y[3]), e4m3x4(y[4], y[5], y[6], y[7]));
+        if (e0 == 0) scales[row] = s;
+    } else {
+        if (live) st8<CK == A_BF16>(side, row * D + e0, x);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Units of a token: its Hq query heads, Hkv key heads and (into the cache)
+// Hkv value heads.  A wave takes `gpw` consecutive groups of 512/D units of
+// one token; the rotation's cosines and sines depend on the lane's place in
+// the head only, so they are formed once per wave.
+// ---------------------------------------------------------------------------
+template <bool BF, int CK, int D>
+__global__ __launch_bounds__(256) void beam_attn_prep(AttnPrepArgs a, int units, int wpt, int gpw) {
+    constexpr int LPH = D / 8, HPW = kWave / LPH;
+    const int lane = threadIdx.x & 63;
+    const int wid = blockIdx.x * 4 + (threadIdx.x >> 6);
+    const int t = wid / wpt;
+    if (t >= a.T) return;   // whole wave
+    const int g0 = (wid - t * wpt) * gpw;
+    const int li = lane % LPH, e0 = li * 8;
+
+    // cos/sin of the angles of this lane's elements: half-split, element e0+j
+    // of the rotated dims has frequency (e0 + j) mod R/2; interleaved, the
+    // pair (e0 + 2j, e0 + 2j + 1) has frequency e0/2 + j
+    float cs[8], sn[8];
+    const int half = a.R / 2;
+    const bool turns = e0 < a.R;
+    if (a.R > 0) {
+        const double p = (double)a.pos[t];
+        const int f0 = a.inter ? e0 / 2 : (e0 < half ? e0 : e0 - half);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int f = f0 + j;
+            if (turns && f < half) {
+                // whole turns drop out in fp64, so far positions keep their angle
+                double rev = p * ((double)a.inv_freq[f] * 0.15915494309189533577);
+                rev -= rint(rev);
+                sincospif((float)(2.0 * rev), &sn[j], &cs[j]);
+            } else {
+                cs[j] = 1.f;
+                sn[j] = 0.f;
+            }
+        }
+    }
+    float qf = 1.f;
+    if (a.ssmax_len > 0.f) qf = powf(1.f + fmaxf((float)a.pos[t], 0.f) / a.ssmax_len, a.ssmax_exp);
+    int slot = -1;
+    if (CK >= 0) {
+        slot = a.slots[t];
+        if ((int64_t)slot >= ((int64_t)a.c.n_pages << a.c.pshift)) slot = -1;
+    }
+
+    for (int i = 0; i < gpw; ++i) {
+        const int ub = (g0 + i) * HPW;
+        if (ub >= units) break;
+        const int u = ub + lane / LPH;
+        const bool is_q = u < a.Hq;
+        const bool is_v = u >= a.Hq + a.Hkv;
+        const bool in = u < units;
+        const int h = is_q ? u : (is_v ? u - a.Hq - a.Hkv : u - a.Hq);
+        const void* src = is_q ? a.q : (is_v ? a.v : a.k);
+        const size_t rs = is_q ? a.qs : (is_v ? a.vs : a.ks);
+        float x[8];
+        if (in) {
+            wid8(ld8<BF>(src, (size_t)t * rs + (size_t)h * D + e0), x);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[j] = 0.f;
+        }
+        if (a.gq) {
+            float ss = 0.f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) ss = fmaf(x[j], x[j], ss);
+            ss = head_sum<LPH>(ss);
+            if (!is_v) {
+                const float rinv = 1.0f / sqrtf(ss * (1.0f / D) + a.eps);
+                float g[8];
+                wid8(ld8<BF>(is_q ? a.gq : a.gk, e0), g);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) x[j] = x[j] * rinv * g[j];
+            }
+        }
+        if (a.R > 0) {
+            if (a.inter) {
+                if (!is_v && turns) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float u0 = x[2 * j], w0 = x[2 * j + 1];
+                        x[2 * j] = u0 * cs[j] - w0 * sn[j];
+                        x[2 * j + 1] = w0 * cs[j] + u0 * sn[j];
+                    }
+                }
+            } else {
+                const int d = a.R / 16;   // lanes between the two halves of a pair
+                const int from = turns ? (e0 < half ? lane + d : lane - d) : lane;
+                const float sg = e0 < half ? -1.f : 1.f;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float o = __shfl(x[j], from, kWave);
+                    if (!is_v && turns) x[j] = x[j] * cs[j] + sg * (o * sn[j]);
+                }
+            }
+        }
+        if (is_q) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[j] *= qf;
+            st8<BF>(a.q_out, ((size_t)t * a.Hq + h) * D + e0, x);
+        }
+        if constexpr (CK < 0) {
+            if (in && !is_q) st8<BF>(a.k_out, ((size_t)t * a.Hkv + h) * D + e0, x);
+        } else {
+            const size_t page = slot >= 0 ? (size_t)(slot >> a.c.pshift) : 0;
+            const size_t row = ((page * a.Hkv + h) << a.c.pshift) + (slot & ((1 << a.c.pshift) - 1));
+            store_cache<CK, D>(is_v ? a.c.v : a.c.k, is_v ? a.c.vs : a.c.ks, row, e0, x,
+                               in && !is_q && slot >= 0);
+        }
+    }
+}
+
+template <bool BF, int CK, int D>
+static void launch_prep(const AttnPrepArgs& a, hipStream_t st) {
+    constexpr int HPW = 512 / D;
+    const int units = a.Hq + a.Hkv * (CK < 0 ? 1 : 2);
+    const int groups = (units + HPW - 1) / HPW;
+    const int gpw = 1;
+    const int wpt = (groups + gpw - 1) / gpw;
+    const unsigned grid = (unsigned)(((size_t)a.T * wpt + 3) / 4);
+    hipLaunchKernelGGL((beam_attn_prep<BF, CK, D>), dim3(grid), dim3(256), 0, st, a, units, wpt, gpw);
+}
+
+template <bool BF, int CK>
+static void launch_prep_d(const AttnPrepArgs& a, hipStream_t st) {
+    if (a.D == 64) launch_prep<BF, CK, 64>(a, st);
+    else if (a.D == 128) launch_prep<BF, CK, 128>(a, st);
+    else launch_prep<BF, CK, 256>(a, st);
+}
+
+template <bool BF>
+static void launch_prep_c(const AttnPrepArgs& a, hipStream_t st) {
+    if (a.k_out) launch_prep_d<BF, -1>(a, st);
+    else if (a.c.kind == A_F32) launch_prep_d<BF, A_F32>(a, st);
+    else if (a.c.kind == A_BF16) launch_prep_d<BF, A_BF16>(a, st);
+    else launch_prep_d<BF, A_FP8>(a, st);
+}
+
+hipError_t launch_attn_prep(const AttnPrepArgs& a, hipStream_t st) {
+    if (a.bf16) launch_prep_c<true>(a, st);
+    else launch_prep_c<false>(a, st);
+    return hipGetLastError();
+}
+
+// ---------------------------------------------------------------------------
+// Cache rows back to dense rows.  A workgroup takes kReadRows consecutive
+// output rows; thread group (row, head, side) of D/8 lanes copies one head
+// row.
+// ---------------------------------------------------------------------------
+template <int CK> BEAM_DEV void load_cache8(const void* side, const float* scales, size_t row, int D, int e0,
+                                            float (&x)[8]) {
+    if constexpr (CK == A_FP8) {
+        const uint2 c = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(side) + row * D + e0);
+        const float s = scales[row];
+        typedef float f32x2v __attribute__((ext_vector_type(2)));
+        const f32x2v p0 = __builtin_amdgcn_cvt_pk_f32_fp8((int)c.x, false), p1 = __builtin_amdgcn_cvt_pk_f32_fp8((int)c.x, true);
+        const f32x2v p2 = __builtin_amdgcn_cvt_pk_f32_fp8((int)c.y, false), p3 = __builtin_amdgcn_cvt_pk_f32_fp8((int)c.y, true);
+        x[0] = p0.x * s; x[1] = p0.y * s; x[2] = p1.x * s; x[3] = p1.y * s;
+        x[4] = p2.x * s; x[5] = p2.y * s; x[6] = p3.x * s; x[7] = p3.y * s;
+    } else {
+        wid8(ld8<CK == A_BF16>(side, row * D + e0), x);
+    }
+}
+
+template <bool BF, int CK, int D>
+__global__ __launch_bounds__(256) void beam_kv_read(KvReadArgs a) {
+    constexpr int LPH = D / 8, HPB = 256 / LPH;
+    const int row = blockIdx.x;
+    // last sequence whose first row is at or before this one
+    int lo = 0, hi = a.B;   // offsets[lo] <= row < offsets[hi], if there is one
+    if (row >= a.offsets[a.B]) return;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if (a.offsets[mid] <= row) lo = mid;
+        else hi = mid;
+    }
+    const int64_t tok = (int64_t)row - a.offsets[lo] + (a.first ? a.first[lo] : 0);
+    const int64_t pi = tok >> a.c.pshift;
+    int page = -1;
+    if (tok >= 0 && pi < a.max_pages) page = a.table[(size_t)lo * a.max_pages + pi];
+    const bool ok = page >= 0 && page < a.c.n_pages;
+    const int off = (int)(tok & ((1 << a.c.pshift) - 1));
+    const int e0 = (threadIdx.x % LPH) * 8;
+    for (int u = threadIdx.x / LPH; u < 2 * a.Hkv; u += HPB) {
+        const bool is_v = u >= a.Hkv;
+        const int h = is_v ? u - a.Hkv : u;
+        float x[8];
+        if (ok) {
+            load_cache8<CK>(is_v ? a.c.v : a.c.k, is_v ? a.c.vs : a.c.ks,
+                            (((size_t)page * a.Hkv + h) << a.c.pshift) + off, D, e0, x);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[j] = 0.f;
+        }
+        st8<BF>(is_v ? a.v_out : a.k_out, ((size_t)row * a.Hkv + h) * D + e0, x);
+    }
+}
+
+template <bool BF, int CK>
+static void launch_read_d(const KvReadArgs& a, hipStream_t st) {
+    const dim3 grid(a.N), block(256);
+    if (a.D == 64) hipLaunchKernelGGL((beam_kv_read<BF, CK, 64>), grid, block, 0, st, a);
+    else if (a.D == 128) hipLaunchKernelGGL((beam_kv_read<BF, CK, 128>), grid, block, 0, st, a);
+    else hipLaunchKernelGGL((beam_kv_read<BF, CK, 256>), grid, block, 0, st, a);
+}
+
+template <bool BF>
+static void launch_read_c(const KvReadArgs& a, hipStream_t st) {
+    if (a.c.kind == A_F32) launch_read_d<BF, A_F32>(a, st);
+    else if (a.c.kind == A_BF16) launch_read_d<BF, A_BF16>(a, st);
+    else launch_read_d<BF, A_FP8>(a, st);
+}
+
+hipError_t launch_kv_read(const KvReadArgs& a, hipStream_t st) {
+    if (a.bf16) launch_read_c<true>(a, st);
+    else launch_read_c<false>(a, st);
+    return hipGetLastError();
+}
+
+}  // namespace beam

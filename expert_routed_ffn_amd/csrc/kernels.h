@@ -110,4 +110,69 @@ struct CombineArgs {
 };
 hipError_t launch_combine_norm(const CombineArgs& a, hipStream_t st);
 
+// Element kinds of the attention sublayer's activations and cache.
+enum AKind { A_F32 = 0, A_BF16 = 1, A_FP8 = 2 };
+
+// A paged key-value cache: [n_pages, Hkv, 2^pshift, D] per side.
+struct KvCache {
+    void* k;
+    void* v;
+    float* ks;              // FP8: [n_pages, Hkv, 2^pshift]
+    float* vs;
+    int n_pages;
+    int pshift;             // log2 of the tokens per page
+    AKind kind;
+};
+
+struct AttnPrepArgs {
+    int T, Hq, Hkv, D;      // Hq = 0: no queries (kv_write)
+    int R;                  // rotated dims (0: none)
+    bool inter;
+    bool bf16;              // q, k, v, gammas and dense outputs
+    float ssmax_len, ssmax_exp, eps;
+    const void* q;
+    const void* k;
+    const void* v;          // null: no values (dense k_out)
+    size_t qs, ks, vs;      // row strides, elements
+    const void* gq;         // null: no norm
+    const void* gk;
+    const int32_t* pos;
+    const float* inv_freq;
+    void* q_out;
+    void* k_out;            // dense keys; null: keys and values go to the cache
+    const int32_t* slots;
+    KvCache c;
+};
+hipError_t launch_attn_prep(const AttnPrepArgs& a, hipStream_t st);
+
+struct KvReadArgs {
+    int B, N, Hkv, D, max_pages;
+    bool bf16;
+    const int32_t* table;
+    const int32_t* offsets;
+    const int32_t* first;
+    void* k_out;
+    void* v_out;
+    KvCache c;
+};
+hipError_t launch_kv_read(const KvReadArgs& a, hipStream_t st);
+
+struct AttnDecodeArgs {
+    int B, Hq, Hkv, D, max_pages, window;
+    int S, C;               // parts per sequence and least tokens per part (attn_decode_split)
+    float scale;
+    const void* q;
+    size_t qs;
+    const int32_t* table;
+    const int32_t* lens;
+    void* out;
+    float* lse;
+    float* parts;           // workspace, S > 1: [B, S, Hq, D] sums, then [B, S, Hq] (max, sum) pairs
+    KvCache c;
+};
+constexpr int kMaxLen = 1 << 30;   // longest sequence attn_decode counts
+void attn_decode_split(int B, int Hkv, int max_len, int window, int* S, int* C);
+size_t attn_decode_ws_bytes(int B, int Hq, int Hkv, int D, int max_len, int window);
+hipError_t launch_attn_decode(const AttnDecodeArgs& a, hipStream_t st);
+
 }  // namespace beam

@@ -373,6 +373,160 @@ beam_status beam_moe_pack_weights(const beam_moe_cfg* cfg, int32_t n_experts, be
  * experts of w_dtype (the maximum over the three).  0 for invalid input. */
 size_t beam_moe_workspace_bytes(const beam_moe_cfg* cfg, int32_t T, beam_dtype w_dtype);
 
+/* ---------------------------------------------------------------------------
+ * Attention sublayer: per-head query/key norms with the position rotation, a
+ * paged key-value cache, and the attention of one new token over it.
+ * (TokenSpeed x Reflection Beam blog, "Architecture"; vLLM Beam summary,
+ *  attention section: 48 query heads over 8 key-value heads of 128, a
+ *  per-head RMSNorm of queries and keys, sliding windows of 512 with rotary
+ *  positions or full attention without them and queries scaled by
+ *  (1 + p/2048)^0.1.)  Its output, projected, is the m of
+ *  beam_moe_norm_boundary; the boundary's x_next, projected, its input.
+ *
+ * The conventions at the top of this file hold.  In addition q, k and v of
+ * the first three calls may be columns of a wider row-major matrix: each
+ * has a row stride in elements (a multiple of 8, at least its heads times
+ * head_dim); the heads of one token are adjacent.
+ * ------------------------------------------------------------------------ */
+
+typedef struct beam_moe_attn_cfg {
+    int32_t n_heads;          /* query heads, at most 256; n_heads % n_kv_heads == 0    */
+    int32_t n_kv_heads;       /* key-value heads; n_heads / n_kv_heads at most 64       */
+    int32_t head_dim;         /* D: 64, 128 or 256                                      */
+    int32_t rope_dim;         /* R leading dims that rotate: 0 (none) .. D, R % 16 == 0 */
+    int32_t rope_interleaved; /* 0: pairs (i, i + R/2); 1: pairs (2i, 2i + 1)           */
+    int32_t window;           /* newest tokens a query sees; 0: all of them             */
+    int32_t page_size;        /* tokens per cache page: a power of two, 16 .. 1024      */
+    float ssmax_len;          /* > 0: rotated q times (1 + max(p, 0)/ssmax_len)^ssmax_exp */
+    float ssmax_exp;
+    float softmax_scale;      /* > 0, times q.k                                         */
+    float rms_eps;            /* RMSNorm epsilon                                        */
+} beam_moe_attn_cfg;
+
+/*
+ * A paged key-value cache (of one layer): slot = page * page_size + place in
+ * the page.  Read by the host during a call only; the arrays are device
+ * memory, 16-byte aligned:
+ *   k, v             [n_pages, n_kv_heads, page_size, D] of dtype
+ *                    (F32, BF16 or FP8_E4M3)
+ *   k_scale, v_scale [n_pages, n_kv_heads, page_size] fp32, FP8_E4M3 only:
+ *                    an element is code * scale, one scale per head row
+ * n_pages * page_size is at most 2^31 - 1.
+ */
+typedef struct beam_moe_kv_cache {
+    void* k;
+    void* v;
+    float* k_scale;
+    float* v_scale;
+    int32_t n_pages;
+    beam_dtype dtype;
+} beam_moe_kv_cache;
+
+/*
+ * beam_moe_qk_norm_rope -- per-head RMSNorm of queries and keys, the position
+ * rotation and the queries' position factor in one pass.  For a head row x
+ * of token t at position p = positions[t]:
+ *   x <- x / sqrt(mean(x^2) + rms_eps) * gamma          (with gamma)
+ *   (u, w) <- (u cos a - w sin a, w cos a + u sin a), a = p * inv_freq[i],
+ *             for pair i = 0 .. R/2 - 1                 (with R > 0)
+ *   q: x <- x * (1 + max(p, 0)/ssmax_len)^ssmax_exp     (with ssmax_len > 0)
+ * in fp32 (the angle in fp64, reduced to one turn), rounded once.
+ *   q [T, n_heads, D], k [T, n_kv_heads, D]  dtype BF16 or F32, strided rows
+ *   gamma_q, gamma_k  [D] of dtype; both null: no norm
+ *   positions [T] int32; inv_freq [R/2] fp32 (null allowed when R == 0)
+ *   q_out [T, n_heads, D], k_out [T, n_kv_heads, D] out, of dtype, dense;
+ *         each may be its input where that is dense, and must not overlap
+ *         any input otherwise.
+ */
+beam_status beam_moe_qk_norm_rope(const beam_moe_attn_cfg* cfg, int32_t T,
+                                  const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                                  beam_dtype dtype, const void* gamma_q, const void* gamma_k,
+                                  const int32_t* positions, const float* inv_freq,
+                                  void* q_out, void* k_out, void* stream);
+
+/*
+ * beam_moe_qk_norm_rope_cache -- the same for q, while k goes (normed and
+ * rotated) and v goes (as it is) into the cache at slots[t], in one launch.
+ * What is stored is the fp32 result rounded once to the cache's dtype; for
+ * FP8_E4M3, scale = amax/448 of the head row (1 for a row of zeros) and
+ * code = e4m3(value / scale), rounded to nearest even, as
+ * beam_moe_quantize_fp8 does per token.
+ *   slots [T] int32: a row whose slot is outside [0, n_pages * page_size)
+ *         (-1 for padding) is not stored; its q_out row is written all the
+ *         same.  The slots in range must differ: two rows for one slot
+ *         leave that slot's contents unspecified.
+ *   q_out as above; the cache must not overlap the inputs.
+ */
+beam_status beam_moe_qk_norm_rope_cache(const beam_moe_attn_cfg* cfg, int32_t T,
+                                        const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                                        const void* v, int64_t v_stride, beam_dtype dtype,
+                                        const void* gamma_q, const void* gamma_k,
+                                        const int32_t* positions, const float* inv_freq,
+                                        const int32_t* slots, void* q_out,
+                                        const beam_moe_kv_cache* cache, void* stream);
+
+/*
+ * beam_moe_kv_write -- stores ready key and value rows k, v
+ * [T, n_kv_heads, D] (dtype BF16 or F32, strided rows) at slots[t], rounded
+ * or quantised as above.
+ */
+beam_status beam_moe_kv_write(const beam_moe_attn_cfg* cfg, int32_t T, const void* k, int64_t k_stride,
+                              const void* v, int64_t v_stride, beam_dtype dtype, const int32_t* slots,
+                              const beam_moe_kv_cache* cache, void* stream);
+
+/*
+ * beam_moe_kv_read -- reads runs of B sequences' tokens back into dense rows:
+ * rows row_offsets[b] .. row_offsets[b+1] - 1 of k_out and v_out get the
+ * tokens first[b], first[b] + 1, ... of sequence b (code * scale in fp32,
+ * rounded once).
+ *   page_table  [B, max_pages] int32: page of the sequence's tokens
+ *               [i * page_size, (i+1) * page_size)
+ *   row_offsets [B+1] int32, ascending from 0;  first [B] int32, nullable (0)
+ *   k_out, v_out [N, n_kv_heads, D] out, dtype BF16 or F32, dense.  Rows at
+ *               and behind row_offsets[B] are left as they were.
+ * A token whose page is outside [0, n_pages) or outside the table reads as
+ * zeros; nothing outside the cache or the table is accessed.
+ */
+beam_status beam_moe_kv_read(const beam_moe_attn_cfg* cfg, int32_t B, int32_t N,
+                             const beam_moe_kv_cache* cache, const int32_t* page_table, int32_t max_pages,
+                             const int32_t* row_offsets, const int32_t* first,
+                             void* k_out, void* v_out, beam_dtype dtype, void* stream);
+
+/*
+ * beam_moe_attn_decode -- attention of one new token per sequence over its
+ * cached tokens (the new token's own key and value are in the cache
+ * already).  Query head h reads key-value head h / (n_heads / n_kv_heads):
+ *   z_j = softmax_scale * q . k_j for the tokens j in
+ *         [max(0, len - window), len) (window 0: [0, len)), len = seq_lens[b]
+ *   out = sum_j softmax(z)_j v_j,   lse = log sum_j exp(z_j)
+ * Sums, maxima and the join of the parts are fp32; with a BF16 or FP8_E4M3
+ * cache the probabilities (times the value row's scale) are rounded to bf16
+ * for the matrix cores.
+ *   q      [B, n_heads, D] dtype, rows q_stride apart; out [B, n_heads, D]
+ *          dtype, dense, must not overlap q.  dtype is BF16 for a BF16 or
+ *          FP8_E4M3 cache and F32 for an F32 one.
+ *   lse    [B, n_heads] fp32 out, nullable (natural logarithm)
+ *   page_table as in beam_moe_kv_read; seq_lens [B] int32.  A length below 0
+ *          counts as 0 and one beyond the table as the table's
+ *          max_pages * page_size (or 2^30).  A row with no token (or whose scores are all
+ *          -inf) gets out = 0 and lse = -inf.  Tokens on a page outside
+ *          [0, n_pages) are skipped.
+ *   max_len  the longest length to expect, 0 .. 2^30: it sizes the split
+ *          over the cache's length.  Results hold for longer ones too, more slowly.
+ *   ws     beam_moe_attn_workspace_bytes(cfg, B, max_len) bytes, 16-byte
+ *          aligned (may be null where that is 0); its contents need no
+ *          initialisation, and calls that overlap in time must not share it.
+ */
+beam_status beam_moe_attn_decode(const beam_moe_attn_cfg* cfg, int32_t B, const void* q, int64_t q_stride,
+                                 beam_dtype dtype, const beam_moe_kv_cache* cache,
+                                 const int32_t* page_table, int32_t max_pages, const int32_t* seq_lens,
+                                 int32_t max_len, void* out, float* lse,
+                                 void* ws, size_t ws_bytes, void* stream);
+
+/* Workspace bytes of beam_moe_attn_decode for B sequences of at most max_len
+ * tokens (0 for invalid input, and where none is needed). */
+size_t beam_moe_attn_workspace_bytes(const beam_moe_attn_cfg* cfg, int32_t B, int32_t max_len);
+
 /* Static, human-readable name of a status code. */
 const char* beam_moe_status_string(beam_status status);
 

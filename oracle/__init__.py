@@ -1,4 +1,5 @@
-"""CPU oracle for one Beam-style MoE layer forward.  TEST INFRASTRUCTURE ONLY.
+"""CPU oracle for one Beam-style MoE layer forward and the attention
+sublayer beside it.  TEST INFRASTRUCTURE ONLY.
 
 This package is the slow, plain reference that the HIP path is checked
 against.  Only the tests, the package smoke check and the bench's CPU
@@ -15,8 +16,10 @@ Sources (the three pages the method is described on):
        day-0 post: section "MoE and residual stream: FP32 router, sandwich
        norm, depth-scaled residual" and the list of seven kernel changes.
 
-Every function in oracle.moe cites the passage it follows.  Pins (checks of
-the oracle against something other than itself) live in tests/test_oracle_*.
+Every function in oracle.moe and the header of oracle.attn cite the passages
+followed.  Pins (checks of the oracle against something other than itself)
+live in tests/test_oracle_*.
 """
 
+from .attn import *  # noqa: F401,F403
 from .moe import *  # noqa: F401,F403

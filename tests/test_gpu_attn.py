@@ -1,0 +1,695 @@
+"""GPU parity of the attention sublayer's entry points against the fp64
+oracle (oracle/attn.py): head layouts, odd sizes, lengths from none to many
+parts, windows, bad pages, garbage in unwritten places, strides, streams,
+captured graphs, and the calls chained as a decode step uses them.
+
+Tolerances, from the arithmetic.  h(t) = finfo(t).eps / 2 is the relative
+error of one rounding to t, u = h(fp32) = 2^-24.
+
+Norm and rotation, per head row with largest magnitude M (after norm and
+factor): the sum of D <= 256 squares (8 in a lane, then log2 steps), the
+square root, the quotient and two products are each good to a few u (16 u in
+all), the reduced angle is off by at most pi * u + 2 ulp of sin and cos (8 u),
+a rotated element adds two such products of magnitude at most M and the
+position factor 4 u more: below 64 u M = 2^-18 M, plus h(dtype) |value|.
+
+Decode, with A = sum_j softmax_j |v_j| and Z = scale * max_j sum_d |q_d k_jd|:
+a score's products are exact (bf16, e4m3) or off by u each, and summed in at
+most D/4 + 8 steps, so it is off by e = (D/4 + 8) u Z, which moves a
+probability by the factor 1 + 2 e; exp2, the rescalings and the n-term sums in
+fp32 add (n/32 + 64) u; a probability is rounded to bf16 once (bf16 and e4m3
+caches: h(bf16), and the value's scale, where there is one, enters before that
+rounding, 2 u).  So out is off by
+(h(bf16) or 0 + 2 e + (n/32 + 64) u) A + h(dtype) |out|, and lse by
+e + (n/32 + 64) u + u |lse|.
+"""
+
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import oracle
+import synth
+from parity_util import say
+
+beam = pytest.importorskip("expert_routed_ffn_amd")
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+U = 2.0 ** -24
+HALF = {torch.float32: U, torch.bfloat16: 2.0 ** -8}
+KIND = {"f32": beam.BEAM_F32, "bf16": beam.BEAM_BF16, "fp8": beam.BEAM_FP8_E4M3}
+ACT = {"f32": torch.float32, "bf16": torch.bfloat16}
+
+
+def f64(t):
+    return synth.to_f64(t.float() if t.dtype == torch.float8_e4m3fn else t)
+
+
+def gen(seed):
+    g = torch.Generator(device=DEV)
+    g.manual_seed(seed)
+    return g
+
+
+def poisoned(cfg, n_pages, kind):
+    """A cache whose every element is NaN."""
+    c = beam.kv_cache(cfg, n_pages, KIND[kind], DEV)
+    for t in (c.k, c.v, c.k_scale, c.v_scale):
+        if t is not None:
+            (t.view(torch.uint8).fill_(0x7F) if t.dtype == torch.float8_e4m3fn else t.fill_(float("nan")))
+    return c
+
+
+def filled(cfg, n_pages, kind, seed):
+    """A cache of random rows, and its exact values k, v [n_pages, h, P, D]."""
+    c = beam.kv_cache(cfg, n_pages, KIND[kind], DEV)
+    g = gen(seed)
+    vals = []
+    for t, s in ((c.k, c.k_scale), (c.v, c.v_scale)):
+        x = torch.randn(t.shape, generator=g, device=DEV)
+        if kind == "fp8":
+            s.copy_(x.abs().amax(-1) / 448)
+            t.copy_((x / s[..., None]).to(torch.float8_e4m3fn))
+            vals.append(f64(t) * f64(s)[..., None])
+        else:
+            t.copy_(x)
+            vals.append(f64(t))
+    return c, vals
+
+
+# ------------------------------------------------------------------ norm, rotation, cache rows
+
+def rope_inputs(cfg, T, act, seed, gap=0):
+    """Columns of a merged projection (with `gap` columns before and between), positions, gammas, frequencies."""
+    g = gen(seed)
+    hq, hkv, D = cfg.n_heads, cfg.n_kv_heads, cfg.head_dim
+    w = (hq + 2 * hkv) * D + 3 * gap
+    m = torch.randn((T, w), generator=g, device=DEV).to(ACT[act])
+    at = [gap, 2 * gap + hq * D, 3 * gap + (hq + hkv) * D]
+    q, k, v = (m[:, a:a + h * D].unflatten(1, (h, D)) for a, h in zip(at, (hq, hkv, hkv)))
+    pos = torch.randint(0, 1 << 20, (T,), generator=g, device=DEV, dtype=torch.int32)
+    pos[0] = 0
+    if T > 2:
+        pos[1], pos[2] = (1 << 31) - 1, -7
+    gq, gk = ((1 + 0.1 * torch.randn(D, generator=g, device=DEV)).to(ACT[act]) for _ in range(2))
+    f = None
+    if cfg.rope_dim:
+        f = (10000.0 ** (-torch.arange(0, cfg.rope_dim, 2, dtype=torch.float64) / cfg.rope_dim)).float().to(DEV)
+    return q, k, v, pos, gq, gk, f
+
+
+def rope_ref(cfg, x, gamma, pos, f, is_q):
+    X, G, P = f64(x), None if gamma is None else f64(gamma), f64(pos)
+    F = None if f is None else f64(f)
+    return np.stack([np.stack([oracle.norm_rope_row(
+        X[t, h], G, cfg.rms_eps, P[t], F, cfg.rope_interleaved,
+        oracle.ssmax_factor(P[t], cfg.ssmax_len, cfg.ssmax_exp) if is_q else 1.0) for h in range(X.shape[1])])
+        for t in range(X.shape[0])])
+
+
+def check_rows(name, got, ref, half):
+    top = np.abs(ref).max(-1, keepdims=True)
+    err = np.abs(f64(got) - ref) - half * np.abs(ref) - 2.0 ** -18 * top
+    say(f"  {name}: over the bound by {err.max():.2e}")
+    assert (err <= 0).all(), name
+
+
+ROPE = [
+    # act, T, n_heads, n_kv_heads, D, R, interleaved, ssmax, gammas, gap
+    ("bf16", 1, 48, 8, 128, 128, False, 0.0, True, 0),
+    ("bf16", 37, 48, 8, 128, 128, False, 0.0, True, 8),
+    ("bf16", 5, 48, 8, 128, 0, False, 2048.0, True, 0),
+    ("f32", 9, 16, 4, 64, 32, True, 0.0, True, 16),
+    ("f32", 3, 5, 5, 256, 256, False, 100.0, True, 8),
+    ("bf16", 7, 3, 1, 64, 48, False, 0.0, False, 8),
+    ("bf16", 4, 7, 7, 256, 16, True, 0.0, True, 0),
+    ("f32", 130, 3, 1, 128, 64, False, 0.0, False, 0),
+]
+
+
+@pytest.mark.parametrize("act,T,hq,hkv,D,R,inter,ssmax,norm,gap", ROPE)
+def test_qk_norm_rope(act, T, hq, hkv, D, R, inter, ssmax, norm, gap):
+    say(f"qk_norm_rope {act} T={T} {hq}/{hkv} D={D} R={R}")
+    cfg = beam.AttnCfg(hq, hkv, D, R, inter, 0, 16, ssmax)
+    q, k, _, pos, gq, gk, f = rope_inputs(cfg, T, act, 3 + T, gap)
+    if not norm:
+        gq = gk = None
+    qo = torch.full((T + 1, hq, D), 5.0, dtype=ACT[act], device=DEV)
+    ko = torch.full((T + 1, hkv, D), 5.0, dtype=ACT[act], device=DEV)
+    beam.beam_moe_qk_norm_rope(cfg, q, k, pos, qo[:T], ko[:T], f, gq, gk)
+    torch.cuda.synchronize()
+    check_rows("q", qo[:T], rope_ref(cfg, q, gq, pos, f, True), HALF[ACT[act]])
+    check_rows("k", ko[:T], rope_ref(cfg, k, gk, pos, f, False), HALF[ACT[act]])
+    assert (qo[T] == 5).all() and (ko[T] == 5).all()       # rows behind the last stay
+
+
+def test_qk_norm_rope_in_place():
+    cfg = beam.AttnCfg(6, 2, 128, 64)
+    q, k, _, pos, gq, gk, f = rope_inputs(cfg, 19, "bf16", 5)
+    q, k = q.contiguous(), k.contiguous()
+    qo, ko = torch.empty_like(q), torch.empty_like(k)
+    beam.beam_moe_qk_norm_rope(cfg, q, k, pos, qo, ko, f, gq, gk)
+    beam.beam_moe_qk_norm_rope(cfg, q, k, pos, q, k, f, gq, gk)
+    torch.cuda.synchronize()
+    assert torch.equal(q, qo) and torch.equal(k, ko)
+
+
+def test_norm_of_zeros_and_non_finite_rows():
+    """A row of zeros stays zero; a non-finite element makes its own head row
+    NaN (with the norm) or only its own pair (without), and no other."""
+    cfg = beam.AttnCfg(4, 2, 64, 32)
+    q, k, _, pos, gq, gk, f = rope_inputs(cfg, 4, "bf16", 6)
+    q, k = q.contiguous(), k.contiguous()
+    q[0, 1] = 0
+    q[1, 2, 60] = float("inf")
+    k[2, 0, 3] = float("nan")
+    qo, ko = torch.empty_like(q), torch.empty_like(k)
+    beam.beam_moe_qk_norm_rope(cfg, q, k, pos, qo, ko, f, gq, gk)
+    torch.cuda.synchronize()
+    assert (qo[0, 1] == 0).all()
+    bad = torch.isnan(qo).any(-1)
+    assert bad.sum() == 1 and bad[1, 2]
+    bad = torch.isnan(ko).any(-1)
+    assert bad.sum() == 1 and bad[2, 0]
+    beam.beam_moe_qk_norm_rope(cfg, q, k, pos, qo, ko, f)
+    torch.cuda.synchronize()
+    assert torch.isinf(qo[1, 2, 60]) and torch.isfinite(qo).sum() == qo.numel() - 1
+    bad = torch.nonzero(~torch.isfinite(ko[2, 0]))[:, 0].tolist()
+    assert bad == [3, 19] and torch.isfinite(ko).sum() == ko.numel() - 2
+
+
+def stored(c, slots, cfg):
+    """fp64 values, and scales, of the cache rows [len(slots), h, D] at slots."""
+    s = torch.as_tensor(slots, device=DEV).long()
+    at = s // cfg.page_size, slice(None), s % cfg.page_size
+    out = []
+    for t, sc in ((c.k, c.k_scale), (c.v, c.v_scale)):
+        out.append((f64(t[at]), None if sc is None else f64(sc[at])))
+    return out
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32", "fp8"])
+@pytest.mark.parametrize("act,T,hq,hkv,D,R,inter,ssmax,norm,gap", ROPE)
+def test_qk_norm_rope_cache(kind, act, T, hq, hkv, D, R, inter, ssmax, norm, gap):
+    say(f"qk_norm_rope_cache {act} -> {kind} T={T} {hq}/{hkv} D={D} R={R}")
+    cfg = beam.AttnCfg(hq, hkv, D, R, inter, 0, 16, ssmax)
+    q, k, v, pos, gq, gk, f = rope_inputs(cfg, T, act, 3 + T, gap)
+    if not norm:
+        gq = gk = None
+    n_pages = T // 16 + 3
+    slots = torch.randperm(n_pages * 16, generator=gen(T), device=DEV)[:T].to(torch.int32)
+    if T > 4:                                   # rows that go nowhere
+        slots[1], slots[3], slots[4] = -1, n_pages * 16, (1 << 31) - 1
+    keep = ((slots >= 0) & (slots < n_pages * 16)).cpu().numpy()
+    c = poisoned(cfg, n_pages, kind)
+    qo = torch.empty((T, hq, D), dtype=ACT[act], device=DEV)
+    beam.beam_moe_qk_norm_rope_cache(cfg, q, k, v, pos, slots, qo, c, f, gq, gk)
+    torch.cuda.synchronize()
+    check_rows("q", qo, rope_ref(cfg, q, gq, pos, f, True), HALF[ACT[act]])
+    (gotk, ks), (gotv, vs) = stored(c, slots.cpu().numpy()[keep], cfg)
+    refk, refv = rope_ref(cfg, k, gk, pos, f, False)[keep], f64(v)[keep]
+    if kind == "fp8":
+        # the scale follows the row's maximum; a code is off by half a step of
+        # its binade (2^-4 relative) or of the smallest one (2^-10 scales)
+        top = np.abs(refk).max(-1)
+        assert (np.abs(ks - top / 448) <= 2.0 ** -17 * top / 448).all()
+        err = np.abs(gotk * ks[..., None] - refk)
+        assert (err <= 2.0 ** -4 * np.abs(refk) + 2.0 ** -10 * ks[..., None] + 2.0 ** -17 * top[..., None]).all()
+        for t in range(len(refv)):              # values: the oracle's codes, bit for bit
+            for h in range(hkv):
+                sc, codes = oracle.quantize_row_e4m3(refv[t, h])
+                assert sc == vs[t, h] and np.array_equal(codes, gotv[t, h])
+    else:
+        half = HALF[ACT[kind]]
+        top = np.abs(refk).max(-1, keepdims=True)
+        assert (np.abs(gotk - refk) <= half * np.abs(refk) + 2.0 ** -18 * top).all()
+        assert np.array_equal(gotv, refv if act == "bf16" or kind == "f32" else oracle.round_bf16(refv))
+    # nothing else in the cache was touched
+    untouched = np.setdiff1d(np.arange(n_pages * 16), slots.cpu().numpy()[keep])
+    for got, sc in stored(c, untouched, cfg):
+        assert np.isnan(got).all() and (sc is None or np.isnan(sc).all())
+
+
+@pytest.mark.parametrize("act,kind,T,hkv,D,P", [
+    ("bf16", "bf16", 33, 8, 128, 64), ("bf16", "fp8", 33, 8, 128, 16), ("f32", "fp8", 5, 3, 64, 32),
+    ("f32", "f32", 1, 1, 256, 1024), ("bf16", "f32", 4, 2, 64, 128), ("f32", "bf16", 300, 1, 128, 16),
+    ("bf16", "fp8", 1000, 5, 256, 64),
+])
+def test_kv_write_then_read(act, kind, T, hkv, D, P):
+    """Written rows come back, bit for bit where the formats allow it; other
+    slots stay; the rows are read in runs that begin and end inside pages."""
+    say(f"kv write/read {act} {kind} T={T} hkv={hkv} D={D} P={P}")
+    cfg = beam.AttnCfg(hkv, hkv, D, 0, False, 0, P)
+    g = gen(T)
+    m = torch.randn((T, 2 * hkv * D + 8), generator=g, device=DEV).to(ACT[act])
+    k, v = m[:, :hkv * D].unflatten(1, (hkv, D)), m[:, hkv * D + 8:].unflatten(1, (hkv, D))
+    k[0, 0] = 0                                            # an all-zero row: scale 1, codes 0
+    # two sequences that share nothing, tokens in order, pages in any order
+    n1 = T // 3
+    lens = [n1, T - n1]
+    width = -(-max(lens) // P) + 1
+    n_pages = 2 * width + 1
+    perm = torch.randperm(n_pages, generator=g, device=DEV).tolist()
+    table = np.full((3, width), -1, np.int32)
+    slots = []
+    for b, n in enumerate(lens):
+        for j in range(-(-n // P)):
+            table[b, j] = perm.pop()
+        slots += [table[b, t // P] * P + t % P for t in range(n)]
+    c = poisoned(cfg, n_pages, kind)
+    beam.beam_moe_kv_write(cfg, k, v, torch.tensor(slots, dtype=torch.int32, device=DEV), c)
+    torch.cuda.synchronize()
+    ref = []
+    for x, (got, sc) in zip((f64(k), f64(v)), stored(c, slots, cfg)):
+        if kind == "fp8":
+            want = np.zeros_like(x)
+            for t in range(T):
+                for h in range(hkv):
+                    s, codes = oracle.quantize_row_e4m3(x[t, h])
+                    assert s == sc[t, h] and np.array_equal(codes, got[t, h])
+                    want[t, h] = codes * s
+        else:
+            want = oracle.round_bf16(x) if kind == "bf16" else x
+            assert np.array_equal(got, want)
+        ref.append(want)
+    free = np.setdiff1d(np.arange(n_pages * P), slots)
+    for got, sc in stored(c, free, cfg):
+        assert np.isnan(got).all() and (sc is None or np.isnan(sc).all())
+
+    # runs: from inside the first sequence, all of the second, none of the third
+    first = [n1 // 2, 0, 0]
+    off = np.cumsum([0, n1 - n1 // 2, T - n1, 0]).astype(np.int32)
+    rows = [t for t in range(n1 // 2, n1)] + [t for t in range(n1, T)]
+    table = torch.tensor(table, device=DEV)
+    for out in ("bf16", "f32"):
+        ko, vo = (torch.full((len(rows) + 3, hkv, D), 7.0, dtype=ACT[out], device=DEV) for _ in range(2))
+        beam.beam_moe_kv_read(cfg, c, table, torch.tensor(off, device=DEV), ko, vo,
+                              first=torch.tensor(first, dtype=torch.int32, device=DEV))
+        torch.cuda.synchronize()
+        for got, want in ((ko, ref[0]), (vo, ref[1])):
+            want = want[rows].astype(np.float32).astype(np.float64)     # code * scale in fp32
+            assert np.array_equal(f64(got[:len(rows)]), want if out == "f32" else oracle.round_bf16(want))
+            assert (got[len(rows):] == 7).all()
+
+
+def test_kv_read_outside_the_cache():
+    """Bad pages, tokens before the first and behind the table read as zeros."""
+    cfg = beam.AttnCfg(2, 2, 64, 0, False, 0, 16)
+    c, (k, _) = filled(cfg, 3, "fp8", 1)
+    table = torch.tensor([[0, -1, 3], [1 << 30, 2, -(1 << 31)], [1, 1, 1]], dtype=torch.int32, device=DEV)
+    off = torch.tensor([0, 60, 80, 90], dtype=torch.int32, device=DEV)
+    first = torch.tensor([0, 10, -5], dtype=torch.int32, device=DEV)
+    ko, vo = (torch.full((90, 2, 64), 3.0, device=DEV) for _ in range(2))
+    beam.beam_moe_kv_read(cfg, c, table, off, ko, vo, first=first)
+    torch.cuda.synchronize()
+    want = np.zeros((90, 2, 64))
+    for i in range(90):
+        b, t = (0, i) if i < 60 else (1, 10 + i - 60) if i < 80 else (2, i - 80 - 5)
+        p = table[b, t // 16].item() if 0 <= t < 48 else -1
+        if 0 <= p < 3:
+            want[i] = k[p, :, t % 16]
+    assert np.array_equal(f64(ko), want.astype(np.float32).astype(np.float64))
+
+
+# ------------------------------------------------------------------ decode
+
+def tables(lens, P, n_pages, seed, width=None):
+    """A page table of distinct random pages, -1 behind each sequence."""
+    width = width or max(1, -(-max(lens) // P))
+    perm = np.random.default_rng(seed).permutation(n_pages).tolist()
+    t = np.full((len(lens), width), -1, np.int32)
+    for b, n in enumerate(lens):
+        for j in range(min(width, -(-n // P))):
+            t[b, j] = perm.pop()
+    return t
+
+
+def decode_ref(cfg, q, k, v, table, lens, n_pages):
+    """(out, lse, bound on out, bound on lse) of every sequence."""
+    B, hq, D = q.shape
+    hkv = cfg.n_kv_heads
+    P, act = cfg.page_size, q.dtype
+    out, lse = np.zeros((B, hq, D)), np.zeros((B, hq))
+    eo, el = np.zeros((B, hq, D)), np.zeros((B, hq))
+    for b, n in enumerate(lens):
+        n = min(max(n, 0), table.shape[1] * P)
+        toks = range(max(0, n - cfg.window) if cfg.window else 0, n)
+        kr, there = oracle.cached_rows(k, table[b], toks, n_pages)
+        vr, _ = oracle.cached_rows(v, table[b], toks, n_pages)
+        kr, vr = kr[there], vr[there]
+        qb = f64(q[b]).reshape(hkv, hq // hkv, D)
+        o, z, mag = oracle.decode_attention(qb, kr, vr, cfg.softmax_scale)
+        Z = 0.0
+        if len(kr):
+            Z = cfg.softmax_scale * max((np.abs(qb[h]) @ np.abs(kr[:, h]).T).max() for h in range(hkv))
+        e = (D / 4 + 8) * U * Z
+        c = len(kr) / 32 + 64
+        half_p = 0.0 if act == torch.float32 else 2.0 ** -8 + 2 * U
+        out[b], lse[b] = o.reshape(hq, D), z.reshape(hq)
+        eo[b] = (half_p + 2 * e + c * U) * mag.reshape(hq, D) + HALF[act] * np.abs(out[b])
+        el[b] = e + c * U + U * np.abs(np.where(np.isinf(lse[b]), 0, lse[b]))
+    return out, lse, eo, el
+
+
+def check_decode(cfg, q, c, vals, table, lens, max_len, name, n_pages=None, stream=None):
+    n_pages = n_pages or c.k.shape[0]
+    B = len(lens)
+    dt = torch.tensor(table, device=DEV)
+    dl = torch.tensor(lens, dtype=torch.int32, device=DEV)
+    out = torch.full(q.shape, 9.0, dtype=q.dtype, device=DEV)
+    lse = torch.full((B, cfg.n_heads), 9.0, device=DEV)
+    ws = beam.attn_workspace(cfg, B, max_len)
+    ws.view(torch.uint8).fill_(0xFF)                       # its contents do not matter
+    beam.beam_moe_attn_decode(cfg, q, c, dt, dl, max_len, out, ws, lse)
+    torch.cuda.synchronize()
+    ro, rl, eo, el = decode_ref(cfg, q, *vals, table, lens, n_pages)
+    got, gl = f64(out), f64(lse)
+    d = np.abs(got - ro) - eo
+    inf = np.isinf(rl)
+    say(f"  {name}: out over the bound by {d.max():.2e}, lse max err {np.abs(np.where(inf, 0, gl - np.where(inf, 0, rl))).max():.2e}")
+    assert (d <= 0).all(), name
+    assert (got[np.broadcast_to(inf[..., None], got.shape)] == 0).all()
+    assert np.array_equal(np.isneginf(gl), inf) and (np.abs(gl[~inf] - rl[~inf]) <= el[~inf]).all(), name
+    return out
+
+
+LENS = [0, 1, 15, 16, 17, 31, 32, 33, 100, 127, 128, 129, 300, 513]
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp8", "f32"])
+@pytest.mark.parametrize("hq,hkv,D", [(48, 8, 128), (4, 4, 64), (16, 1, 256), (17, 1, 128), (48, 1, 64), (64, 1, 128),
+                                      (40, 2, 256), (6, 2, 64)])
+@pytest.mark.parametrize("window,P", [(0, 16), (100, 64)])
+def test_decode(kind, hq, hkv, D, window, P):
+    say(f"decode {kind} {hq}/{hkv} D={D} window={window} P={P}")
+    cfg = beam.AttnCfg(hq, hkv, D, 0, False, window, P, softmax_scale=D ** -0.5)
+    n_pages = sum(-(-n // P) for n in LENS) + 2
+    c, vals = filled(cfg, n_pages, kind, 7)
+    table = tables(LENS, P, n_pages, 1)
+    q = torch.randn((len(LENS), hq, D), generator=gen(2), device=DEV) * 2
+    check_decode(cfg, q.to(ACT["f32" if kind == "f32" else "bf16"]), c, vals, table, LENS, max(LENS), "decode")
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp8", "f32"])
+@pytest.mark.parametrize("window", [1, 2, 16, 33, 512, 5000])
+def test_decode_windows_and_garbage(kind, window):
+    """Windows that begin anywhere in a page, NaN in every place that no
+    query may see: behind the length, before the window, in free pages."""
+    say(f"decode window {window} {kind}")
+    lens = [1, 16, 47, 64, 65, 515, 640, 700]
+    P = 64
+    cfg = beam.AttnCfg(8, 2, 128, 0, False, window, P)
+    n_pages = sum(-(-n // P) for n in lens) + 3
+    c, vals = filled(cfg, n_pages, kind, 11)
+    table = tables(lens, P, n_pages, 3)
+    seen = np.zeros((n_pages, P), bool)
+    for b, n in enumerate(lens):
+        for t in range(max(0, n - window), n):
+            seen[table[b, t // P], t % P] = True
+    hide = torch.tensor(~seen, device=DEV)[:, None, :].expand(n_pages, 2, P)
+    for t in (c.k, c.v):
+        if kind == "fp8":
+            t.view(torch.uint8)[hide] = 0x7F
+        else:
+            t[hide] = float("nan")
+    for s in (c.k_scale, c.v_scale):
+        if s is not None:
+            s[hide] = float("nan")
+    q = torch.randn((len(lens), 8, 128), generator=gen(4), device=DEV)
+    check_decode(cfg, q.to(ACT["f32" if kind == "f32" else "bf16"]), c, vals, table, lens, max(lens), "window")
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp8", "f32"])
+def test_decode_bad_pages_and_lengths(kind):
+    """Pages outside the cache are skipped (also all of them), lengths below
+    zero count as zero and beyond the table as the table's."""
+    P, n_pages = 16, 12
+    cfg = beam.AttnCfg(6, 2, 64, 0, False, 0, P)
+    c, vals = filled(cfg, n_pages, kind, 5)
+    table = np.array([[0, -1, 2, 3], [n_pages, 4, 1 << 30, 5], [-1, -1, -1, -1], [6, 7, 8, 9], [10, 11, 0, 1],
+                      [-(1 << 31), 3, n_pages + 1, n_pages]], np.int32)
+    lens = [60, 64, 33, -5, 1000, 49]
+    q = torch.randn((6, 6, 64), generator=gen(4), device=DEV).to(ACT["f32" if kind == "f32" else "bf16"])
+    check_decode(cfg, q, c, vals, table, lens, 64, "bad pages")
+
+
+def test_decode_no_pages_at_all():
+    cfg = beam.AttnCfg(6, 2, 64, 0, False, 0, 16)
+    c, vals = filled(cfg, 1, "bf16", 5)
+    q = torch.randn((3, 6, 64), generator=gen(4), device=DEV).bfloat16()
+    check_decode(cfg, q, c, vals, np.zeros((3, 0), np.int32), [5, 0, 9], 100, "empty table")
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp8", "f32"])
+@pytest.mark.parametrize("B,lens,max_len,window", [
+    (1, [5000], 5000, 0),              # many parts
+    (1, [5000], 100, 0),               # longer than expected
+    (1, [40], 100000, 0),              # far shorter than expected
+    (3, [4097, 0, 130], 4097, 0),
+    (2, [3000, 2999], 4000, 1025),
+    (5, [2048, 1, 700, 128, 1500], 2048, 0),
+])
+def test_decode_parts(kind, B, lens, max_len, window):
+    say(f"decode parts {kind} {lens} expected {max_len} window {window}")
+    P = 32
+    cfg = beam.AttnCfg(6, 2, 128, 0, False, window, P)
+    n_pages = sum(-(-n // P) for n in lens) + 1
+    c, vals = filled(cfg, n_pages, kind, 9)
+    q = torch.randn((B, 6, 128), generator=gen(6), device=DEV) * 3
+    check_decode(cfg, q.to(ACT["f32" if kind == "f32" else "bf16"]), c, vals, tables(lens, P, n_pages, 2), lens,
+                 max_len, "parts")
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp8", "f32"])
+def test_decode_scores_far_apart(kind):
+    """Scores that grow and fall by hundreds along the sequence: late maxima
+    rescale what came before, early ones leave what follows at nothing."""
+    P, lens = 16, [900, 900, 260]
+    cfg = beam.AttnCfg(6, 2, 64, 0, False, 0, P, softmax_scale=1.0)
+    n_pages = 140
+    c = beam.kv_cache(cfg, n_pages, KIND[kind], DEV)
+    table = tables(lens, P, n_pages, 8)
+    g = gen(3)
+    kk = torch.randn((n_pages, 2, P, 64), generator=g, device=DEV) * 0.1
+    vv = torch.randn((n_pages, 2, P, 64), generator=g, device=DEV)
+    for b, n in enumerate(lens):
+        for t in range(n):
+            up = t if b == 0 else n - t if b == 1 else (t * 37) % n
+            kk[table[b, t // P], :, t % P, 0] = 0.5 * up
+    vals = []
+    for t, s, x in ((c.k, c.k_scale, kk), (c.v, c.v_scale, vv)):
+        if kind == "fp8":
+            s.copy_(x.abs().amax(-1) / 448)
+            t.copy_((x / s[..., None]).to(torch.float8_e4m3fn))
+            vals.append(f64(t) * f64(s)[..., None])
+        else:
+            t.copy_(x)
+            vals.append(f64(t))
+    q = torch.zeros((3, 6, 64), device=DEV)
+    q[..., 0] = torch.tensor([1.0, -1.0, 0.25, 0.01, 2.0, -0.5], device=DEV)
+    check_decode(cfg, q.to(ACT["f32" if kind == "f32" else "bf16"]), c, vals, table, lens, 900, "far apart")
+
+
+def test_decode_non_finite():
+    """A NaN or +inf key that is seen makes its heads NaN and no others; -inf
+    scores count as nothing, all of them give an empty row."""
+    P = 16
+    cfg = beam.AttnCfg(4, 2, 64, 0, False, 0, P, softmax_scale=1.0)
+    c, _ = filled(cfg, 9, "bf16", 5)
+    table = torch.arange(9, dtype=torch.int32, device=DEV).view(3, 3)
+    q = torch.zeros((3, 4, 64), dtype=torch.bfloat16, device=DEV)
+    q[..., 0] = 1.0
+    c.k[0, 0, 5, 7] = float("nan")          # sequence 0, kv head 0
+    c.k[3:6, 1, :, 0] = float("-inf")       # sequence 1, kv head 1: every score -inf
+    c.k[6, 0, 2, 0] = float("-inf")         # sequence 2, kv head 0: one of them
+    out, lse = torch.empty_like(q), torch.empty((3, 4), device=DEV)
+    for ml in (48, 4000):
+        beam.beam_moe_attn_decode(cfg, q, c, table, torch.tensor([40, 48, 33], dtype=torch.int32, device=DEV), ml, out,
+                                  beam.attn_workspace(cfg, 3, ml), lse)
+        torch.cuda.synchronize()
+        assert torch.isnan(out[0, :2]).all() and torch.isfinite(out[0, 2:]).all()
+        assert (out[1, 2:] == 0).all() and torch.isneginf(lse[1, 2:]).all() and torch.isfinite(out[1, :2]).all()
+        assert torch.isfinite(out[2]).all() and torch.isfinite(lse[2]).all()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp8"])
+def test_offsets_beyond_32_bits(kind):
+    """Pages whose elements lie past 2^31 (and bytes past 2^32) in the cache."""
+    cfg = beam.AttnCfg(16, 8, 128, 128, False, 0, 64)
+    n_pages = 40000                           # 64 * 1024 elements a page
+    c = beam.kv_cache(cfg, n_pages, KIND[kind], DEV)
+    T = 100
+    pages = [39999, 33000]
+    q, k, v, pos, gq, gk, f = rope_inputs(cfg, T, "bf16", 21)
+    slots = torch.tensor([pages[t // 64] * 64 + t % 64 for t in range(T)], dtype=torch.int32, device=DEV)
+    qo = torch.empty((T, 16, 128), dtype=torch.bfloat16, device=DEV)
+    beam.beam_moe_qk_norm_rope_cache(cfg, q, k, v, pos, slots, qo, c, f, gq, gk)
+    small = beam.kv_cache(cfg, 2, KIND[kind], DEV)
+    near = torch.arange(T, dtype=torch.int32, device=DEV)
+    q2 = torch.empty_like(qo)
+    beam.beam_moe_qk_norm_rope_cache(cfg, q, k, v, pos, near, q2, small, f, gq, gk)
+    res = []
+    for cache, tab in ((c, pages), (small, [0, 1])):
+        table = torch.tensor([tab], dtype=torch.int32, device=DEV)
+        ko, vo = (torch.empty((T, 8, 128), dtype=torch.bfloat16, device=DEV) for _ in range(2))
+        beam.beam_moe_kv_read(cfg, cache, table, torch.tensor([0, T], dtype=torch.int32, device=DEV), ko, vo)
+        out = torch.empty((1, 16, 128), dtype=torch.bfloat16, device=DEV)
+        beam.beam_moe_attn_decode(cfg, qo[-1:], cache, table, torch.tensor([T], dtype=torch.int32, device=DEV), T, out,
+                                  beam.attn_workspace(cfg, 1, T))
+        res.append((ko, vo, out))
+    torch.cuda.synchronize()
+    for a, b in zip(*res):
+        assert torch.isfinite(a).all() and torch.equal(a, b)
+
+
+# ------------------------------------------------------------------ as it is used
+
+def step_state(kind, B=6, P=16, seed=0):
+    cfg = beam.AttnCfg(8, 2, 128, 128, False, 0, P)
+    lens0 = [3, 0, 15, 16, 200, 640][:B]
+    width, steps = 64, 4
+    n_pages = sum(-(-(n + steps) // P) for n in lens0) + 1
+    table = tables([n + steps for n in lens0], P, n_pages, seed, width)
+    c, _ = filled(cfg, n_pages, kind, seed + 1)
+    g = gen(seed + 2)
+    qkv = torch.randn((steps, B, 12 * 128), generator=g, device=DEV).bfloat16()
+    gq, gk = ((1 + 0.1 * torch.randn(128, generator=g, device=DEV)).bfloat16() for _ in range(2))
+    f = (10000.0 ** (-torch.arange(0, 128, 2, dtype=torch.float64) / 128)).float().to(DEV)
+    pos = torch.tensor([[n + s for n in lens0] for s in range(steps)], dtype=torch.int32, device=DEV)
+    slots = torch.tensor([[table[b, (n + s) // P] * P + (n + s) % P for b, n in enumerate(lens0)]
+                          for s in range(steps)], dtype=torch.int32, device=DEV)
+    return cfg, table, c, qkv, gq, gk, f, pos, slots
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp8"])
+def test_decode_steps(kind):
+    """Steps of a decode loop, each attending to what the steps before it
+    wrote; also as one captured graph replayed per step, and on another
+    stream, with the same results."""
+    cfg, table, c, qkv, gq, gk, f, pos, slots = step_state(kind)
+    steps, B = qkv.shape[:2]
+    bufs = beam.attn_buffers(cfg, B, 1024, keep_lse=True)
+    t = torch.tensor(table, device=DEV)
+    before = [x.clone() for x in (c.k, c.v, c.k_scale, c.v_scale) if x is not None]
+    eager = []
+    for s in range(steps):
+        beam.attn_layer(cfg, qkv[s], pos[s], slots[s], c, t, pos[s] + 1, 1024, bufs, f, gq, gk)
+        torch.cuda.synchronize()
+        vals = []
+        for x, sc in ((c.k, c.k_scale), (c.v, c.v_scale)):
+            vals.append(f64(x) if sc is None else f64(x) * f64(sc)[..., None])
+        lens = (pos[s] + 1).tolist()
+        ro, rl, eo, el = decode_ref(cfg, bufs.q, *vals, table, lens, c.k.shape[0])
+        assert (np.abs(f64(bufs.out) - ro) <= eo).all() and (np.abs(f64(bufs.lse) - rl) <= el).all()
+        eager.append((bufs.out.clone(), bufs.lse.clone()))
+    after = [x.clone() for x in (c.k, c.v, c.k_scale, c.v_scale) if x is not None]
+
+    def rewind():
+        for x, y in zip((x for x in (c.k, c.v, c.k_scale, c.v_scale) if x is not None), before):
+            x.copy_(y)
+
+    inp, p, sl, ln = qkv[0].clone(), pos[0].clone(), slots[0].clone(), pos[0] + 1
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        rewind()
+        for s in range(steps):
+            beam.attn_layer(cfg, qkv[s], pos[s], slots[s], c, t, pos[s] + 1, 1024, bufs, f, gq, gk)
+            assert bufs.out is not None
+            got = bufs.out.clone()
+            side.synchronize()
+            assert torch.equal(got, eager[s][0])
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        beam.attn_layer(cfg, inp, p, sl, c, t, ln, 1024, bufs, f, gq, gk)
+    for again in range(2):
+        rewind()
+        for s in range(steps):
+            inp.copy_(qkv[s])
+            p.copy_(pos[s])
+            sl.copy_(slots[s])
+            ln.copy_(pos[s] + 1)
+            graph.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(bufs.out, eager[s][0]) and torch.equal(bufs.lse, eager[s][1])
+        for x, y in zip((x for x in (c.k, c.v, c.k_scale, c.v_scale) if x is not None), after):
+            assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
+
+
+def test_two_decodes_at_once():
+    """Two calls on two streams with a workspace each."""
+    cfg = beam.AttnCfg(6, 2, 128, 0, False, 0, 32)
+    lens = [3000, 1700]
+    c, _ = filled(cfg, 160, "bf16", 9)
+    t = torch.tensor(tables(lens, 32, 160, 2), device=DEV)
+    n = torch.tensor(lens, dtype=torch.int32, device=DEV)
+    qs = [torch.randn((2, 6, 128), generator=gen(i), device=DEV).bfloat16() for i in range(2)]
+    alone = []
+    for q in qs:
+        o = torch.empty_like(q)
+        beam.beam_moe_attn_decode(cfg, q, c, t, n, 3000, o, beam.attn_workspace(cfg, 2, 3000))
+        alone.append(o)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in qs]
+    ws = [beam.attn_workspace(cfg, 2, 3000) for _ in qs]
+    outs = [torch.empty_like(q) for q in qs]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for q, o, w, st in zip(qs, outs, ws, streams):
+            beam.beam_moe_attn_decode(cfg, q, c, t, n, 3000, o, w, stream=st)
+    torch.cuda.synchronize()
+    for a, o in zip(alone, outs):
+        assert torch.equal(a, o)
+
+
+def test_attention_between_two_boundaries():
+    """One decode step of a small decoder layer: projection, attention,
+    output projection, norm boundary, then the MoE layer on its x_next."""
+    H, hq, hkv, D = 512, 4, 2, 128
+    acfg = beam.AttnCfg(hq, hkv, D, 128, False, 512, 16)
+    cfg = beam.LayerCfg(hidden=H, n_experts=16, n_groups=4, topk_groups=2, topk=4, group_topn=2, d_ff=256)
+    g = gen(1)
+    rnd = lambda *s: torch.randn(s, generator=g, device=DEV)
+    lens = [1, 40, 600]
+    B, P = 3, 16
+    n_pages = sum(-(-n // P) for n in lens) + 1
+    table = tables(lens, P, n_pages, 4)
+    c, _ = filled(acfg, n_pages, "fp8", 2)
+    x, h = rnd(B, H).bfloat16(), rnd(B, H).bfloat16()
+    wqkv, wo = rnd(8 * D, H) / math.sqrt(H), rnd(H, hq * D) / math.sqrt(hq * D)
+    one = torch.ones(H, dtype=torch.bfloat16, device=DEV)
+    gq = torch.ones(D, dtype=torch.bfloat16, device=DEV)
+    f = (10000.0 ** (-torch.arange(0, D, 2, dtype=torch.float64) / D)).float().to(DEV)
+    pos = torch.tensor([n - 1 for n in lens], dtype=torch.int32, device=DEV)
+    slots = torch.tensor([table[b, (n - 1) // P] * P + (n - 1) % P for b, n in enumerate(lens)], dtype=torch.int32,
+                         device=DEV)
+    qkv = (x.float() @ wqkv.T).bfloat16()
+    bufs = beam.attn_buffers(acfg, B, 1024)
+    beam.attn_layer(acfg, qkv, pos, slots, c, torch.tensor(table, device=DEV), pos + 1, 1024, bufs, f, gq, gq)
+    m = (bufs.out.float().view(B, -1) @ wo.T).contiguous()
+    h0 = h.clone()
+    xn = torch.empty_like(h)
+    beam.beam_moe_norm_boundary(cfg, m, h, xn, one, one, 2)
+    torch.cuda.synchronize()
+    vals = [f64(t) * f64(s)[..., None] for t, s in ((c.k, c.k_scale), (c.v, c.v_scale))]
+    ro, _, eo, _ = decode_ref(acfg, bufs.q, *vals, table, lens, n_pages)
+    assert (np.abs(f64(bufs.out) - ro) <= eo).all()
+    # p, h' and x_next are rounded to bf16 one after the other: each may land one
+    # step (2^-7 relative) off the oracle's, and carries the step before it on
+    for b in range(B):
+        rp, rh, rx = oracle.norm_boundary(f64(m)[b], f64(h0)[b], f64(one), f64(one), 2, cfg.rms_eps)
+        size = np.abs(rp) + np.abs(f64(h0)[b])
+        assert (np.abs(f64(h)[b] - rh) <= 2.0 ** -6 * (size + np.abs(rh))).all()
+        assert (np.abs(f64(xn)[b] - rx) <= 2.0 ** -6 * (2 * size + np.abs(rx))).all()
+    # the MoE layer takes x_next
+    wr, bias = rnd(16, H) / math.sqrt(H), 28 + 0.02 * rnd(16)
+    wgu, wd = (rnd(16, 512, H) / math.sqrt(H)).bfloat16(), (rnd(16, H, 256) / 16).bfloat16()
+    pgu, pd = torch.empty_like(wgu), torch.empty_like(wd)
+    beam.beam_moe_pack_weights(cfg, wgu, wd, pgu, pd)
+    mb = beam.alloc_buffers(cfg, B, torch.bfloat16, beam.BEAM_BF16)
+    beam.moe_layer(cfg, xn, wr, bias, pgu, pd, h, one, one, 3, mb)
+    torch.cuda.synchronize()
+    assert torch.isfinite(mb.x_next).all()
