@@ -54,16 +54,32 @@ template <bool BF> BEAM_DEV void st8(void* p, size_t i, const float (&x)[8]) {
     }
 }
 
-// sum / maximum over the LPH lanes that hold one head row
-template <int LPH> BEAM_DEV float head_sum(float v) {
-#pragma unroll
-    for (int o = LPH / 2; o > 0; o >>= 1) v += __shfl_xor(v, o, kWave);
+// value of the lane that the DPP control CTRL gives inside rows of 16 lanes
+template <int CTRL> BEAM_DEV float dpp(float v) {
+    return __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(v), CTRL, 0xF, 0xF, true));
+}
+constexpr int kXor1 = 0xB1, kXor2 = 0x4E, kHalfMirror = 0x141, kMirror = 0x140, kRor8 = 0x128;
+
+// Combines over the LPH lanes that hold one head row, every lane getting the
+// result: pairs, quads, then the mirror image of 8 and of 16 lanes (whose
+// other half already agrees among itself) by DPP, and 16 lanes further by the
+// row swap.
+template <int LPH, typename F> BEAM_DEV float head_reduce(float v, F f) {
+    v = f(v, dpp<kXor1>(v));
+    v = f(v, dpp<kXor2>(v));
+    v = f(v, dpp<kHalfMirror>(v));
+    if constexpr (LPH >= 16) v = f(v, dpp<kMirror>(v));
+    if constexpr (LPH >= 32) {
+        const auto p = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+        v = f(__uint_as_float(p[0]), __uint_as_float(p[1]));
+    }
     return v;
 }
+template <int LPH> BEAM_DEV float head_sum(float v) {
+    return head_reduce<LPH>(v, [](float a, float b) { return a + b; });
+}
 template <int LPH> BEAM_DEV float head_max(float v) {
-#pragma unroll
-    for (int o = LPH / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor(v, o, kWave));
-    return v;
+    return head_reduce<LPH>(v, [](float a, float b) { return fmaxf(a, b); });
 }
 
 // Stores a head row's 8 elements of this lane at row `row` of one cache
@@ -116,7 +132,7 @@ __global__ __launch_bounds__(256) void beam_attn_prep(AttnPrepArgs a, int units,
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             const int f = f0 + j;
-            if (turns && f < half) {
+            if (turns && f < half && !(a.inter && j >= 4)) {
                 // whole turns drop out in fp64, so far positions keep their angle
                 double rev = p * ((double)a.inv_freq[f] * 0.15915494309189533577);
                 rev -= rint(rev);
@@ -135,23 +151,31 @@ __global__ __launch_bounds__(256) void beam_attn_prep(AttnPrepArgs a, int units,
         if ((int64_t)slot >= ((int64_t)a.c.n_pages << a.c.pshift)) slot = -1;
     }
 
-    for (int i = 0; i < gpw; ++i) {
-        const int ub = (g0 + i) * HPW;
-        if (ub >= units) break;
-        const int u = ub + lane / LPH;
-        const bool is_q = u < a.Hq;
-        const bool is_v = u >= a.Hq + a.Hkv;
-        const bool in = u < units;
-        const int h = is_q ? u : (is_v ? u - a.Hq - a.Hkv : u - a.Hq);
+    // the next group's loads are in flight while a group is worked on
+    const int gend = min(g0 + gpw, (units + HPW - 1) / HPW);
+    auto load = [&](int gi) {
+        const int u = min(gi * HPW + lane / LPH, units - 1);
+        const bool is_q = u < a.Hq, is_v = u >= a.Hq + a.Hkv;
         const void* src = is_q ? a.q : (is_v ? a.v : a.k);
         const size_t rs = is_q ? a.qs : (is_v ? a.vs : a.ks);
+        const int h = is_q ? u : (is_v ? u - a.Hq - a.Hkv : u - a.Hq);
+        return ld8<BF>(src, (size_t)t * rs + (size_t)h * D + e0);
+    };
+    float gq[8], gk[8];
+    if (a.gq) {
+        wid8(ld8<BF>(a.gq, e0), gq);
+        wid8(ld8<BF>(a.gk, e0), gk);
+    }
+    Raw8<BF> next = load(g0);
+    for (int gi = g0; gi < gend; ++gi) {
+        const int u = gi * HPW + lane / LPH;
+        const bool is_q = u < a.Hq;
+        const bool is_v = u >= a.Hq + a.Hkv;
+        const bool in = u < units;   // lanes past the last unit go along with it and store nothing
+        const int h = is_q ? u : (is_v ? u - a.Hq - a.Hkv : u - a.Hq);
         float x[8];
-        if (in) {
-            wid8(ld8<BF>(src, (size_t)t * rs + (size_t)h * D + e0), x);
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) x[j] = 0.f;
-        }
+        wid8(next, x);
+        if (gi + 1 < gend) next = load(gi + 1);
         if (a.gq) {
             float ss = 0.f;
 #pragma unroll
@@ -159,10 +183,8 @@ __global__ __launch_bounds__(256) void beam_attn_prep(AttnPrepArgs a, int units,
             ss = head_sum<LPH>(ss);
             if (!is_v) {
                 const float rinv = 1.0f / sqrtf(ss * (1.0f / D) + a.eps);
-                float g[8];
-                wid8(ld8<BF>(is_q ? a.gq : a.gk, e0), g);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) x[j] = x[j] * rinv * g[j];
+                for (int j = 0; j < 8; ++j) x[j] = x[j] * rinv * (is_q ? gq[j] : gk[j]);
             }
         }
         if (a.R > 0) {
@@ -176,13 +198,20 @@ __global__ __launch_bounds__(256) void beam_attn_prep(AttnPrepArgs a, int units,
                     }
                 }
             } else {
-                const int d = a.R / 16;   // lanes between the two halves of a pair
-                const int from = turns ? (e0 < half ? lane + d : lane - d) : lane;
+                const int d = a.R / 16;   // lanes between the two elements of a pair
                 const float sg = e0 < half ? -1.f : 1.f;
+                float o[8];
+                if (d == 8) {             // the other half of a row of 16 lanes
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float o = __shfl(x[j], from, kWave);
-                    if (!is_v && turns) x[j] = x[j] * cs[j] + sg * (o * sn[j]);
+                    for (int j = 0; j < 8; ++j) o[j] = dpp<kRor8>(x[j]);
+                } else {
+                    const int from = turns ? (e0 < half ? lane + d : lane - d) : lane;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) o[j] = __shfl(x[j], from, kWave);
+                }
+                if (!is_v && turns) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) x[j] = x[j] * cs[j] + sg * (o[j] * sn[j]);
                 }
             }
         }
@@ -193,7 +222,7 @@ __global__ __launch_bounds__(256) void beam_attn_prep(AttnPrepArgs a, int units,
         }
         if constexpr (CK < 0) {
             if (in && !is_q) st8<BF>(a.k_out, ((size_t)t * a.Hkv + h) * D + e0, x);
-        } else {
+        } else if (gi * HPW + HPW > a.Hq) {   // a group with keys or values
             const size_t page = slot >= 0 ? (size_t)(slot >> a.c.pshift) : 0;
             const size_t row = ((page * a.Hkv + h) << a.c.pshift) + (slot & ((1 << a.c.pshift) - 1));
             store_cache<CK, D>(is_v ? a.c.v : a.c.k, is_v ? a.c.vs : a.c.ks, row, e0, x,
@@ -202,12 +231,16 @@ __global__ __launch_bounds__(256) void beam_attn_prep(AttnPrepArgs a, int units,
     }
 }
 
+constexpr int kPrepWaves = 8192;   // 8 per SIMD
+
 template <bool BF, int CK, int D>
 static void launch_prep(const AttnPrepArgs& a, hipStream_t st) {
     constexpr int HPW = 512 / D;
     const int units = a.Hq + a.Hkv * (CK < 0 ? 1 : 2);
     const int groups = (units + HPW - 1) / HPW;
-    const int gpw = 1;
+    // groups per wave: one while that leaves the chip with few waves, more
+    // once the waves suffice, which forms a token's cosines fewer times
+    const int gpw = (int)min((int64_t)groups, max((int64_t)1, (int64_t)a.T * groups / kPrepWaves));
     const int wpt = (groups + gpw - 1) / gpw;
     const unsigned grid = (unsigned)(((size_t)a.T * wpt + 3) / 4);
     hipLaunchKernelGGL((beam_attn_prep<BF, CK, D>), dim3(grid), dim3(256), 0, st, a, units, wpt, gpw);
