@@ -21,24 +21,25 @@
 
 namespace beam {
 
-constexpr int kTile = 32;            // tokens per wave step
-constexpr int kStep = 4 * kTile;     // tokens per workgroup step
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
-// Parts of a sequence: about kWantWG workgroups in all, each of whole steps.
-constexpr int kWantWG = 1024;
-void attn_decode_split(int B, int Hkv, int max_len, int window, int* S, int* C) {
-    // a window's tokens start inside a tile
-    const int64_t span = window > 0 && window < max_len ? (int64_t)window + kTile - 1 : max_len;
+// Tokens per wave step, by cache element: 16 KiB of keys and values at D = 128.
+template <int KIND> constexpr int tile_tokens() { return KIND == A_F32 ? 16 : (KIND == A_BF16 ? 32 : 64); }
+constexpr int kMaxTile = 64;
+
+// Parts of a sequence: kMinPart to kMaxPart tokens (a power of two), as many
+// as give the chip about kWantWG workgroups.
+constexpr int kWantWG = 1024, kMinPart = 256, kMaxPart = 1024;
+void attn_decode_split(int B, int Hkv, int max_len, int window, int* S, int* cshift) {
+    // a window's tokens begin inside a tile
+    const int64_t span = window > 0 && window < max_len ? (int64_t)window + kMaxTile - 1 : max_len;
     const int64_t heads = (int64_t)B * Hkv;
-    const int64_t want = (kWantWG + heads - 1) / heads;
-    int64_t c = (span + want - 1) / want;
-    c = (c + kStep - 1) / kStep * kStep;
-    if (c < kStep) c = kStep;
-    int64_t s = (span + c - 1) / c;
-    if (s < 1) s = 1;
-    *S = (int)s;
-    *C = (int)c;
+    int sh = 0;
+    while ((1 << sh) < kMinPart) ++sh;
+    while ((1 << sh) < kMaxPart && heads * ((span + (1 << sh) - 1) >> sh) > kWantWG) ++sh;
+    const int64_t s = (span + (1 << sh) - 1) >> sh;
+    *S = s < 1 ? 1 : (int)s;
+    *cshift = sh;
 }
 
 size_t attn_decode_ws_bytes(int B, int Hq, int Hkv, int D, int max_len, int window) {
@@ -47,33 +48,31 @@ size_t attn_decode_ws_bytes(int B, int Hq, int Hkv, int D, int max_len, int wind
     return S > 1 ? (size_t)B * S * Hq * (D + 2) * sizeof(float) : 0;
 }
 
-// Tokens [t0, t1) of part s of a sequence.  Every part has at least C tokens
-// and together they cover the sequence whatever its length.
+// The tokens that a sequence's query sees, [start, len), cut into n parts of
+// 2^shift tokens from `base` on.  Parts double until S of them cover a
+// sequence that is longer than expected.
 struct Span {
-    int start, t0, t1, n;   // first token seen; the part's range; parts that have tokens
+    int start, len, base, shift, n;
 };
-BEAM_DEV Span span_of(const AttnDecodeArgs& a, int b, int s) {
+BEAM_DEV Span span_of(const AttnDecodeArgs& a, int b, int tile) {
     const int64_t cap = min((int64_t)a.max_pages << a.c.pshift, (int64_t)kMaxLen);
-    const int len = (int)min((int64_t)max(a.lens[b], 0), cap);
     Span p;
-    p.start = a.window > 0 ? max(0, len - a.window) : 0;
-    const int base = p.start & ~(kTile - 1);
-    const int all = len - base;
-    const int64_t per = ((int64_t)all + a.S - 1) / a.S;
-    const int64_t chunk = max((int64_t)a.C, (per + kStep - 1) & ~(int64_t)(kStep - 1));
-    p.n = (int)((all + chunk - 1) / chunk);
-    p.t0 = (int)min((int64_t)len, base + min(s, p.n) * chunk);
-    p.t1 = (int)min((int64_t)len, p.t0 + chunk);
+    p.len = (int)min((int64_t)max(a.lens[b], 0), cap);
+    p.start = a.window > 0 ? max(0, p.len - a.window) : 0;
+    p.base = p.start & ~(tile - 1);
+    const uint32_t all = (uint32_t)(p.len - p.base);
+    p.shift = a.cshift;
+    while (((uint64_t)a.S << p.shift) < all) ++p.shift;
+    p.n = (int)((all + (1u << p.shift) - 1) >> p.shift);
     return p;
 }
 
-typedef float f32x2 __attribute__((ext_vector_type(2)));
-
-// eight e4m3 codes to bf16 (exact)
-BEAM_DEV void e4m3_to_bf16(uint32_t c, uint32_t& lo, uint32_t& hi) {
-    const f32x2 p = __builtin_amdgcn_cvt_pk_f32_fp8((int)c, false), q = __builtin_amdgcn_cvt_pk_f32_fp8((int)c, true);
-    lo = pack_bf16x2(p.x, p.y);
-    hi = pack_bf16x2(q.x, q.y);
+// four e4m3 codes to bf16 (exact): codes 0, 1 and codes 2, 3
+BEAM_DEV uint32_t e4m3_lo(uint32_t c) {
+    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c, 1.0f, false));
+}
+BEAM_DEV uint32_t e4m3_hi(uint32_t c) {
+    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c, 1.0f, true));
 }
 
 // NW 32-bit words from global memory (16-, 8- or 4-byte pieces)
@@ -93,293 +92,444 @@ template <int NW> BEAM_DEV void ldw(const void* p, uint32_t (&w)[NW]) {
     }
 }
 
-template <int KIND, int D>
-__global__ __launch_bounds__(256) void beam_attn_decode(AttnDecodeArgs a, int qtiles) {
+BEAM_DEV f32x4 mfma_bf16(uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint4 b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, make_uint4(a0, a1, a2, a3)),
+                                                   __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+}
+
+// maximum over the four lanes (r, 0..3) that hold a query's tokens
+BEAM_DEV float max_over_g(float v) {
+    const auto p = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = fmaxf(__uint_as_float(p[0]), __uint_as_float(p[1]));
+    const auto q = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return fmaxf(__uint_as_float(q[0]), __uint_as_float(q[1]));
+}
+BEAM_DEV float sum_over_g(float v) {
+    const auto p = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = __uint_as_float(p[0]) + __uint_as_float(p[1]);
+    const auto q = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return __uint_as_float(q[0]) + __uint_as_float(q[1]);
+}
+
+// A wave's state over the tokens it has seen: 16 * QT queries.
+//   m   reference that the probabilities are relative to (2^(z - m)); -inf
+//       before the first score
+//   l   this lane's share of the sum of probabilities
+//   o   weighted sum of values
+template <int D, int QT> struct Acc {
+    float m[QT], l[QT];
+    f32x4 o[QT][D / 16];
+};
+
+template <int KIND, int D, int QT>
+__global__ __launch_bounds__(256) void beam_attn_decode(AttnDecodeArgs a, int qgroups) {
+    constexpr int TILE = tile_tokens<KIND>(), NU = TILE / 16;   // 16-token blocks per step
+    constexpr int STEP = 4 * TILE;                              // tokens per workgroup step
     constexpr int ES = KIND == A_F32 ? 4 : (KIND == A_BF16 ? 2 : 1);   // bytes per cache element
-    constexpr int DL = D / 16;                    // value elements per lane and token
-    constexpr int NQ = KIND == A_F32 ? D / 16 : D / 32;   // K fragments per token row
-    constexpr int QW = 4;                         // words per query fragment
+    constexpr int DL = D / 16;                                  // value elements per lane and token
+    constexpr int NK = KIND == A_F32 ? D / 16 : D / 32;         // key fragments per token
+    constexpr int KW = KIND == A_FP8 ? 2 : 4;                   // words per key fragment
+    constexpr int VW = DL * ES / 4;                             // words per lane and value row
     __shared__ float sO[4][16][D + 4];
     __shared__ float sM[4][16], sL[4][16];
 
+    // Workgroups of one (sequence, part, head) differ in their query rows
+    // only: they follow each other on one XCD, so that its L2 serves the
+    // keys and values of all but the first.
+    const int x = blockIdx.x;
+    const int work = (x >> 3) / qgroups * 8 + (x & 7), qg = (x >> 3) % qgroups;
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int r = lane & 15, g = lane >> 4;
-    int id = blockIdx.x;
-    const int h = id % a.Hkv;
-    id /= a.Hkv;
-    const int qt = id % qtiles;
-    id /= qtiles;
-    const int s = id % a.S, b = id / a.S;
+    const int h = work % a.Hkv, bs = work / a.Hkv;
+    const int s = bs % a.S, b = bs / a.S;
+    if (b >= a.B) return;
     const int G = a.Hq / a.Hkv;
-    const int P = 1 << a.c.pshift;
-    const Span sp = span_of(a, b, s);
+    const Span sp = span_of(a, b, TILE);
     if (s > 0 && s >= sp.n) return;               // no tokens; part 0 of an empty row goes on
+    const int t0 = sp.base + (int)((uint32_t)s << sp.shift);
+    const int t1 = (int)min((int64_t)sp.len, (int64_t)t0 + ((int64_t)1 << sp.shift));
 
-    // query fragments: lane (r, g) holds column r (head h*G + 16 qt + r)
-    const int qrow = qt * 16 + r;
-    const size_t qoff = (size_t)b * a.qs + (size_t)(h * G + qrow) * D;
-    uint32_t qf[NQ][QW];
+    // query fragments: lane (r, g) holds column r of each 16-query block
+    uint32_t qf[QT][NK][4];
 #pragma unroll
-    for (int c = 0; c < NQ; ++c) {
-        if (qrow < G) {
-            if constexpr (KIND == A_F32) ldw<4>(static_cast<const float*>(a.q) + qoff + 16 * c + 4 * g, qf[c]);
-            else ldw<4>(static_cast<const uint16_t*>(a.q) + qoff + 32 * c + 8 * g, qf[c]);
-        } else {
+    for (int j = 0; j < QT; ++j) {
+        const int qrow = (qg * QT + j) * 16 + r;
+        const size_t qoff = (size_t)b * a.qs + (size_t)(h * G + min(qrow, G - 1)) * D;
 #pragma unroll
-            for (int j = 0; j < QW; ++j) qf[c][j] = 0u;
+        for (int c = 0; c < NK; ++c) {
+            if constexpr (KIND == A_F32) ldw<4>(static_cast<const float*>(a.q) + qoff + 16 * c + 4 * g, qf[j][c]);
+            else ldw<4>(static_cast<const uint16_t*>(a.q) + qoff + 32 * c + 8 * g, qf[j][c]);
         }
     }
 
-    f32x4 o[DL];
+    Acc<D, QT> acc;
 #pragma unroll
-    for (int t = 0; t < DL; ++t) o[t] = f32x4{0.f, 0.f, 0.f, 0.f};
-    float m = -INFINITY, l = 0.f;
+    for (int j = 0; j < QT; ++j) {
+        acc.m[j] = -INFINITY;
+        acc.l[j] = 0.f;
+#pragma unroll
+        for (int t = 0; t < DL; ++t) acc.o[j][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
     const float zs = a.scale * kLog2e;
+    const int pmask = (1 << a.c.pshift) - 1;
     const int32_t* table = a.table + (size_t)b * a.max_pages;
     const uint8_t* kc = static_cast<const uint8_t*>(a.c.k);
     const uint8_t* vc = static_cast<const uint8_t*>(a.c.v);
 
-    for (int tile = sp.t0 + wave * kTile; tile < sp.t1; tile += kStep) {
-        // the two 16-token blocks' first cache rows; a block past the end or
-        // on a bad page reads page 0 and is masked
-        size_t row[2];
-        bool ok[2];
+    // pages of a step's 16-token blocks (-1 past the end); they are read one
+    // step ahead of the keys and values
+    auto pages_of = [&](int tile, int (&pg)[NU]) {
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
+        for (int u = 0; u < NU; ++u) {
             const int tok = tile + 16 * u;
-            int page = -1;
-            if (tok < sp.t1) page = table[tok >> a.c.pshift];
-            ok[u] = page >= 0 && page < a.c.n_pages;
-            row[u] = (((size_t)(ok[u] ? page : 0) * a.Hkv + h) << a.c.pshift) + (tok & (P - 1));
+            pg[u] = tok < t1 ? table[tok >> a.c.pshift] : -1;
         }
-        f32x4 z[2];
+    };
+    int pg[NU];
+    int tile = t0 + wave * TILE;
+    pages_of(tile, pg);
+
+    for (; tile < t1; tile += STEP) {
+        // all of the step's loads, before any use: a block past the end or
+        // on a bad page reads page 0 and is masked below
+        size_t row[NU];
+        bool ok[NU];
+        bool full = tile >= sp.start && tile + TILE <= t1;
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            z[u] = f32x4{0.f, 0.f, 0.f, 0.f};
-            const uint8_t* kr = kc + (row[u] + r) * (D * ES);
+        for (int u = 0; u < NU; ++u) {
+            ok[u] = (uint32_t)pg[u] < (uint32_t)a.c.n_pages;
+            full = full && ok[u];
+            row[u] = (((size_t)(ok[u] ? pg[u] : 0) * a.Hkv + h) << a.c.pshift) + ((tile + 16 * u) & pmask);
+        }
+        uint32_t kw[NU][NK][KW], vw[NU][4][VW];
+        float4 ks[NU], vs[NU];
 #pragma unroll
-            for (int c = 0; c < NQ; ++c) {
+        for (int u = 0; u < NU; ++u) {
+            const uint8_t* kr = kc + (row[u] + r) * (D * ES) + g * (KW * 4);
+#pragma unroll
+            for (int c = 0; c < NK; ++c) ldw<KW>(kr + c * (16 * KW), kw[u][c]);
+            if constexpr (KIND == A_FP8) ks[u] = *reinterpret_cast<const float4*>(a.c.ks + row[u] + 4 * g);
+        }
+#pragma unroll
+        for (int u = 0; u < NU; ++u) {
+            const uint8_t* vr = vc + (row[u] + 4 * g) * (D * ES) + r * (VW * 4);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) ldw<VW>(vr + i * (D * ES), vw[u][i]);
+            if constexpr (KIND == A_FP8) vs[u] = *reinterpret_cast<const float4*>(a.c.vs + row[u] + 4 * g);
+        }
+        pages_of(tile + STEP, pg);
+        __builtin_amdgcn_sched_barrier(0);
+
+        // scores in powers of two; lane (r, g): query r, tokens 16u + 4g + i
+        float p[QT][NU][4];
+#pragma unroll
+        for (int u = 0; u < NU; ++u) {
+            f32x4 z[QT];
+#pragma unroll
+            for (int j = 0; j < QT; ++j) z[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int c = 0; c < NK; ++c) {
                 if constexpr (KIND == A_F32) {
-                    uint32_t w[4];
-                    ldw<4>(kr + (16 * c + 4 * g) * 4, w);
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        z[u] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(w[e]), __uint_as_float(qf[c][e]),
-                                                                    z[u], 0, 0, 0);
+#pragma unroll
+                        for (int j = 0; j < QT; ++j)
+                            z[j] = __builtin_amdgcn_mfma_f32_16x16x4f32(
+                                __uint_as_float(kw[u][c][e]), __uint_as_float(qf[j][c][e]), z[j], 0, 0, 0);
                 } else {
-                    uint4 w;
+                    uint32_t w[4];
                     if constexpr (KIND == A_BF16) {
-                        w = *reinterpret_cast<const uint4*>(kr + (32 * c + 8 * g) * 2);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) w[e] = kw[u][c][e];
                     } else {
-                        uint32_t f[2];
-                        ldw<2>(kr + 32 * c + 8 * g, f);
-                        e4m3_to_bf16(f[0], w.x, w.y);
-                        e4m3_to_bf16(f[1], w.z, w.w);
+                        w[0] = e4m3_lo(kw[u][c][0]);
+                        w[1] = e4m3_hi(kw[u][c][0]);
+                        w[2] = e4m3_lo(kw[u][c][1]);
+                        w[3] = e4m3_hi(kw[u][c][1]);
                     }
-                    const uint4 qv = make_uint4(qf[c][0], qf[c][1], qf[c][2], qf[c][3]);
-                    z[u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, w),
-                                                                   __builtin_bit_cast(bf16x8, qv), z[u], 0, 0, 0);
+#pragma unroll
+                    for (int j = 0; j < QT; ++j)
+                        z[j] = mfma_bf16(w[0], w[1], w[2], w[3],
+                                         make_uint4(qf[j][c][0], qf[j][c][1], qf[j][c][2], qf[j][c][3]), z[j]);
                 }
             }
-        }
-        // scores in powers of two; lane: query r, tokens 16u + 4g + i
-        float zz[2][4];
-        bool live[2][4];
-        float4 vs[2];
-        float top = -INFINITY;
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            float4 ks = make_float4(1.f, 1.f, 1.f, 1.f);
-            vs[u] = ks;
+            float f[4] = {zs, zs, zs, zs};
             if constexpr (KIND == A_FP8) {
-                ks = *reinterpret_cast<const float4*>(a.c.ks + row[u] + 4 * g);
-                vs[u] = *reinterpret_cast<const float4*>(a.c.vs + row[u] + 4 * g);
+                f[0] *= ks[u].x; f[1] *= ks[u].y; f[2] *= ks[u].z; f[3] *= ks[u].w;
             }
-            const float kss[4] = {ks.x, ks.y, ks.z, ks.w};
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int tok = tile + 16 * u + 4 * g + i;
-                live[u][i] = ok[u] && tok >= sp.start && tok < sp.t1;
-                zz[u][i] = live[u][i] ? z[u][i] * kss[i] * zs : -INFINITY;
-                top = fmaxf(top, zz[u][i]);
-            }
+            for (int j = 0; j < QT; ++j)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) p[j][u][i] = z[j][i] * f[i];
         }
-        top = fmaxf(top, __shfl_xor(top, 16, kWave));
-        top = fmaxf(top, __shfl_xor(top, 32, kWave));
-        const float mn = fmaxf(m, top);
-        const float ms = mn == -INFINITY ? 0.f : mn;
-        const float alpha = __builtin_amdgcn_exp2f(m - ms);
-        m = mn;
-        float p[2][4];
-        float ps = 0.f;
+        if (!full) {
+            // scores of tokens that are not seen leave nothing, and their
+            // values, which may be anything, count as zeros
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
+            for (int u = 0; u < NU; ++u)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                p[u][i] = __builtin_amdgcn_exp2f(zz[u][i] - ms);   // masked: exp2(-inf) = 0
-                ps += p[u][i];
+                for (int i = 0; i < 4; ++i) {
+                    const int tok = tile + 16 * u + 4 * g + i;
+                    const bool live = ok[u] && tok >= sp.start && tok < t1;
+#pragma unroll
+                    for (int j = 0; j < QT; ++j) p[j][u][i] = live ? p[j][u][i] : -INFINITY;
+#pragma unroll
+                    for (int w = 0; w < VW; ++w) vw[u][i][w] = live ? vw[u][i][w] : 0u;
+                    if constexpr (KIND == A_FP8) {
+                        float* v4 = reinterpret_cast<float*>(&vs[u]);
+                        v4[i] = live ? v4[i] : 0.f;
+                    }
+                }
+        }
+#pragma unroll
+        for (int j = 0; j < QT; ++j) {
+            float top = -INFINITY;
+#pragma unroll
+            for (int u = 0; u < NU; ++u)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) top = fmaxf(top, p[j][u][i]);
+            // the reference moves (and what was summed is rescaled) only
+            // when a score exceeds it by kSlack powers of two: probabilities
+            // up to 2^kSlack lose nothing in fp32 sums or bf16 operands
+            constexpr float kSlack = 8.f;
+            if (__any(top > acc.m[j] + kSlack)) {
+                const float mn = fmaxf(acc.m[j], max_over_g(top));
+                const float alpha = __builtin_amdgcn_exp2f(acc.m[j] - (mn == -INFINITY ? 0.f : mn));
+                acc.m[j] = mn;
+                acc.l[j] *= alpha;
+#pragma unroll
+                for (int t = 0; t < DL; ++t) acc.o[j][t] *= alpha;
             }
-        l = l * alpha + ps;
+            const float ms = acc.m[j] == -INFINITY ? 0.f : acc.m[j];
+            float ps = 0.f;
 #pragma unroll
-        for (int t = 0; t < DL; ++t) o[t] *= alpha;
+            for (int u = 0; u < NU; ++u)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    p[j][u][i] = __builtin_amdgcn_exp2f(p[j][u][i] - ms);   // unseen: exp2(-inf) = 0
+                    ps += p[j][u][i];
+                }
+            acc.l[j] += ps;
+        }
 
-        // values of this lane's tokens; a masked token's row may hold anything
         if constexpr (KIND == A_F32) {
 #pragma unroll
-            for (int u = 0; u < 2; ++u)
+            for (int u = 0; u < NU; ++u)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    uint32_t w[DL];
-                    ldw<DL>(vc + ((row[u] + 4 * g + i) * D + r * DL) * 4, w);
+                for (int i = 0; i < 4; ++i)
 #pragma unroll
                     for (int t = 0; t < DL; ++t)
-                        o[t] = __builtin_amdgcn_mfma_f32_16x16x4f32(live[u][i] ? __uint_as_float(w[t]) : 0.f, p[u][i],
-                                                                    o[t], 0, 0, 0);
-                }
+#pragma unroll
+                        for (int j = 0; j < QT; ++j)
+                            acc.o[j][t] = __builtin_amdgcn_mfma_f32_16x16x4f32(
+                                __uint_as_float(vw[u][i][t]), p[j][u][i], acc.o[j][t], 0, 0, 0);
         } else {
-            uint32_t v[8][DL / 2];
+            // 32 tokens at a time: blocks u and u + 1
 #pragma unroll
-            for (int u = 0; u < 2; ++u)
+            for (int u = 0; u < NU; u += 2) {
+                uint4 pw[QT];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const uint8_t* vr = vc + ((row[u] + 4 * g + i) * D + r * DL) * ES;
-                    if constexpr (KIND == A_BF16) {
-                        ldw<DL / 2>(vr, v[4 * u + i]);
-                    } else {
-                        uint32_t f[DL / 4];
-                        ldw<DL / 4>(vr, f);
+                for (int j = 0; j < QT; ++j) {
+                    float y[8];
 #pragma unroll
-                        for (int j = 0; j < DL / 4; ++j) e4m3_to_bf16(f[j], v[4 * u + i][2 * j], v[4 * u + i][2 * j + 1]);
+                    for (int i = 0; i < 4; ++i) {
+                        y[i] = p[j][u][i];
+                        y[4 + i] = p[j][u + 1][i];
                     }
-#pragma unroll
-                    for (int j = 0; j < DL / 2; ++j) v[4 * u + i][j] = live[u][i] ? v[4 * u + i][j] : 0u;
-                    // the value scale joins the probability (one rounding to bf16)
-                    if constexpr (KIND == A_FP8) {
-                        const float vss[4] = {vs[u].x, vs[u].y, vs[u].z, vs[u].w};
-                        p[u][i] *= live[u][i] ? vss[i] : 0.f;
+                    if constexpr (KIND == A_FP8) {   // the value row's scale, before the one rounding to bf16
+                        y[0] *= vs[u].x; y[1] *= vs[u].y; y[2] *= vs[u].z; y[3] *= vs[u].w;
+                        y[4] *= vs[u + 1].x; y[5] *= vs[u + 1].y; y[6] *= vs[u + 1].z; y[7] *= vs[u + 1].w;
                     }
+                    pw[j] = make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]),
+                                       pack_bf16x2(y[6], y[7]));
                 }
-            const uint4 pw = make_uint4(pack_bf16x2(p[0][0], p[0][1]), pack_bf16x2(p[0][2], p[0][3]),
-                                        pack_bf16x2(p[1][0], p[1][1]), pack_bf16x2(p[1][2], p[1][3]));
 #pragma unroll
-            for (int t = 0; t < DL; ++t) {
-                const uint32_t sel = t % 2 ? 0x07060302u : 0x05040100u;
-                uint4 w;
-                w.x = __builtin_amdgcn_perm(v[1][t / 2], v[0][t / 2], sel);
-                w.y = __builtin_amdgcn_perm(v[3][t / 2], v[2][t / 2], sel);
-                w.z = __builtin_amdgcn_perm(v[5][t / 2], v[4][t / 2], sel);
-                w.w = __builtin_amdgcn_perm(v[7][t / 2], v[6][t / 2], sel);
-                o[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, w),
-                                                               __builtin_bit_cast(bf16x8, pw), o[t], 0, 0, 0);
+                for (int w = 0; w < VW; ++w) {
+                    // tokens 2n, 2n + 1 of element t side by side
+                    constexpr int TW = 4 / ES;   // elements per word
+                    uint32_t av[TW][4];
+#pragma unroll
+                    for (int n = 0; n < 4; ++n) {
+                        const uint32_t x0 = vw[u + n / 2][2 * (n % 2)][w], x1 = vw[u + n / 2][2 * (n % 2) + 1][w];
+                        if constexpr (KIND == A_BF16) {
+                            av[0][n] = __builtin_amdgcn_perm(x1, x0, 0x05040100u);
+                            av[1][n] = __builtin_amdgcn_perm(x1, x0, 0x07060302u);
+                        } else {
+                            const uint32_t y0 = __builtin_amdgcn_perm(x1, x0, 0x05010400u);
+                            const uint32_t y1 = __builtin_amdgcn_perm(x1, x0, 0x07030602u);
+                            av[0][n] = e4m3_lo(y0);
+                            av[1][n] = e4m3_hi(y0);
+                            av[TW - 2][n] = e4m3_lo(y1);
+                            av[TW - 1][n] = e4m3_hi(y1);
+                        }
+                    }
+#pragma unroll
+                    for (int e = 0; e < TW; ++e)
+#pragma unroll
+                        for (int j = 0; j < QT; ++j)
+                            acc.o[j][w * TW + e] =
+                                mfma_bf16(av[e][0], av[e][1], av[e][2], av[e][3], pw[j], acc.o[j][w * TW + e]);
+                }
             }
         }
     }
 
-    // join the four waves: o[t][i] of lane (r, g) is query r, d = (4g + i) * DL + t
-    l += __shfl_xor(l, 16, kWave);
-    l += __shfl_xor(l, 32, kWave);
-    if (g == 0) {
-        sM[wave][r] = m;
-        sL[wave][r] = l;
-    }
+    // join the four waves, 16 queries at a time: o[t][i] of lane (r, g) is
+    // query r, d = (4g + i) * DL + t
+    const bool whole = sp.n <= 1;                 // the only part: no join to come
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int t = 0; t < DL; ++t) sO[wave][r][(4 * g + i) * DL + t] = o[t][i];
-    __syncthreads();
-    const int rows = min(16, G - qt * 16);
-    for (int x = threadIdx.x; x < rows * (D / 4); x += 256) {
-        const int q = x / (D / 4), d = x % (D / 4) * 4;
-        float M = sM[0][q];
-#pragma unroll
-        for (int w = 1; w < 4; ++w) M = fmaxf(M, sM[w][q]);
-        const float Ms = M == -INFINITY ? 0.f : M;
-        float L = 0.f;
-        float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
-            const float e = __builtin_amdgcn_exp2f(sM[w][q] - Ms);
-            const float4 v = *reinterpret_cast<const float4*>(&sO[w][q][d]);
-            L = fmaf(e, sL[w][q], L);
-            O.x = fmaf(e, v.x, O.x);
-            O.y = fmaf(e, v.y, O.y);
-            O.z = fmaf(e, v.z, O.z);
-            O.w = fmaf(e, v.w, O.w);
+    for (int j = 0; j < QT; ++j) {
+        const int q0 = (qg * QT + j) * 16;
+        if (q0 >= G) break;
+        if (j > 0) __syncthreads();
+        const float l = sum_over_g(acc.l[j]);
+        if (g == 0) {
+            sM[wave][r] = acc.m[j];
+            sL[wave][r] = l;
         }
-        const int head = h * G + qt * 16 + q;
-        if (a.S == 1) {
-            const float inv = L == 0.f ? 0.f : 1.0f / L;
-            const size_t at = ((size_t)b * a.Hq + head) * D + d;
-            if constexpr (KIND == A_F32)
-                *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at) =
-                    make_float4(O.x * inv, O.y * inv, O.z * inv, O.w * inv);
-            else
-                *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at) =
-                    make_uint2(pack_bf16x2(O.x * inv, O.y * inv), pack_bf16x2(O.z * inv, O.w * inv));
-            if (a.lse && d == 0) a.lse[(size_t)b * a.Hq + head] = L == 0.f ? -INFINITY : M * kLn2 + logf(L);
-        } else {
-            const size_t pr = ((size_t)b * a.S + s) * a.Hq + head;
-            *reinterpret_cast<float4*>(a.parts + pr * D + d) = O;
-            if (d == 0)
-                *reinterpret_cast<float2*>(a.parts + (size_t)a.B * a.S * a.Hq * D + pr * 2) = make_float2(M, L);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int t = 0; t < DL; ++t) sO[wave][r][(4 * g + i) * DL + t] = acc.o[j][t][i];
+        __syncthreads();
+        const int rows = min(16, G - q0);
+        for (int y = threadIdx.x; y < rows * (D / 4); y += 256) {
+            const int q = y / (D / 4), d = y % (D / 4) * 4;
+            float M = sM[0][q];
+#pragma unroll
+            for (int w = 1; w < 4; ++w) M = fmaxf(M, sM[w][q]);
+            const float Ms = M == -INFINITY ? 0.f : M;
+            float L = 0.f;
+            float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                const float e = __builtin_amdgcn_exp2f(sM[w][q] - Ms);
+                const float4 v = *reinterpret_cast<const float4*>(&sO[w][q][d]);
+                L = fmaf(e, sL[w][q], L);
+                O.x = fmaf(e, v.x, O.x);
+                O.y = fmaf(e, v.y, O.y);
+                O.z = fmaf(e, v.z, O.z);
+                O.w = fmaf(e, v.w, O.w);
+            }
+            const int head = h * G + q0 + q;
+            if (whole) {
+                const float inv = L == 0.f ? 0.f : 1.0f / L;
+                const size_t at = ((size_t)b * a.Hq + head) * D + d;
+                if constexpr (KIND == A_F32)
+                    *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at) =
+                        make_float4(O.x * inv, O.y * inv, O.z * inv, O.w * inv);
+                else
+                    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at) =
+                        make_uint2(pack_bf16x2(O.x * inv, O.y * inv), pack_bf16x2(O.z * inv, O.w * inv));
+                if (a.lse && d == 0) a.lse[(size_t)b * a.Hq + head] = L == 0.f ? -INFINITY : M * kLn2 + logf(L);
+            } else {
+                const size_t pr = ((size_t)b * a.S + s) * a.Hq + head;
+                *reinterpret_cast<float4*>(a.parts + pr * D + d) = O;
+                if (d == 0)
+                    *reinterpret_cast<float2*>(a.parts + (size_t)a.B * a.S * a.Hq * D + pr * 2) = make_float2(M, L);
+            }
         }
     }
 }
 
-// Join of a sequence's parts: one wave per (sequence, query head), D/64
-// elements per lane, parts in order.
-template <bool BF, int D>
+// Join of a sequence's parts: a workgroup per (sequence, query head).  Groups
+// of D/4 lanes take the parts in turn, kBatch at a time with all their loads
+// in flight (the first batch's before the number of parts is known: they lie
+// in the workspace whether written or not), each group with its own running
+// maximum; the groups are joined through LDS in a fixed order.
+template <int KIND, int D>
 __global__ __launch_bounds__(256) void beam_attn_join(AttnDecodeArgs a) {
-    constexpr int N = D / 64;
-    const int lane = threadIdx.x & 63;
-    const int wid = blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    if (wid >= a.B * a.Hq) return;
-    const int b = wid / a.Hq, head = wid - b * a.Hq;
-    const int n = max(span_of(a, b, 0).n, 1);
+    constexpr int LPR = D / 4, NG = 256 / LPR, kBatch = 4;
+    __shared__ float sO[NG][D];
+    __shared__ float sM[NG], sL[NG];
+    const int head = blockIdx.x % a.Hq, b = blockIdx.x / a.Hq;
+    const int grp = threadIdx.x / LPR, d = threadIdx.x % LPR * 4;
     const float2* ml = reinterpret_cast<const float2*>(a.parts + (size_t)a.B * a.S * a.Hq * D);
     const size_t first = (size_t)b * a.S * a.Hq + head;
-    float M = -INFINITY;
-    for (int s = 0; s < n; ++s) M = fmaxf(M, ml[first + (size_t)s * a.Hq].x);
-    const float Ms = M == -INFINITY ? 0.f : M;
-    float L = 0.f, O[N];
+    float2 v[kBatch];
+    float4 o[kBatch];
+    auto load = [&](int s0) {
 #pragma unroll
-    for (int j = 0; j < N; ++j) O[j] = 0.f;
-    for (int s = 0; s < n; ++s) {
-        const size_t pr = first + (size_t)s * a.Hq;
-        const float2 v = ml[pr];
-        const float e = __builtin_amdgcn_exp2f(v.x - Ms);
-        L = fmaf(e, v.y, L);
+        for (int k = 0; k < kBatch; ++k) {
+            const size_t pr = first + (size_t)min(s0 + k * NG, a.S - 1) * a.Hq;
+            v[k] = ml[pr];
+            o[k] = *reinterpret_cast<const float4*>(a.parts + pr * D + d);
+        }
+    };
+    load(grp);
+    const int n = span_of(a, b, tile_tokens<KIND>()).n;
+    if (n <= 1) return;                           // its only part wrote the result
+    float M = -INFINITY, L = 0.f;
+    float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int s0 = grp; s0 < n; s0 += kBatch * NG) {
+        if (s0 != grp) load(s0);
+        float top = M;
 #pragma unroll
-        for (int j = 0; j < N; ++j) O[j] = fmaf(e, a.parts[pr * D + j * 64 + lane], O[j]);
+        for (int k = 0; k < kBatch; ++k)
+            if (s0 + k * NG < n) top = fmaxf(top, v[k].x);
+        const float ts = top == -INFINITY ? 0.f : top;
+        const float alpha = __builtin_amdgcn_exp2f(M - ts);
+        M = top;
+        L *= alpha;
+        O.x *= alpha; O.y *= alpha; O.z *= alpha; O.w *= alpha;
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k)
+            if (s0 + k * NG < n) {
+                const float e = __builtin_amdgcn_exp2f(v[k].x - ts);
+                L = fmaf(e, v[k].y, L);
+                O.x = fmaf(e, o[k].x, O.x);
+                O.y = fmaf(e, o[k].y, O.y);
+                O.z = fmaf(e, o[k].z, O.z);
+                O.w = fmaf(e, o[k].w, O.w);
+            }
     }
-    const float inv = L == 0.f ? 0.f : 1.0f / L;
-#pragma unroll
-    for (int j = 0; j < N; ++j) {
-        const size_t at = (size_t)wid * D + j * 64 + lane;
-        if constexpr (BF) static_cast<uint16_t*>(a.out)[at] = f32_to_bf16(O[j] * inv);
-        else static_cast<float*>(a.out)[at] = O[j] * inv;
+    *reinterpret_cast<float4*>(&sO[grp][d]) = O;
+    if (d == 0) {
+        sM[grp] = M;
+        sL[grp] = L;
     }
-    if (a.lse && lane == 0) a.lse[wid] = L == 0.f ? -INFINITY : M * kLn2 + logf(L);
+    __syncthreads();
+    const int t = threadIdx.x;
+    if (t >= D) return;
+    float top = sM[0];
+#pragma unroll
+    for (int k = 1; k < NG; ++k) top = fmaxf(top, sM[k]);
+    const float ts = top == -INFINITY ? 0.f : top;
+    float Lt = 0.f, Ot = 0.f;
+#pragma unroll
+    for (int k = 0; k < NG; ++k) {
+        const float e = __builtin_amdgcn_exp2f(sM[k] - ts);
+        Lt = fmaf(e, sL[k], Lt);
+        Ot = fmaf(e, sO[k][t], Ot);
+    }
+    const float res = Lt == 0.f ? 0.f : Ot / Lt;
+    const size_t at = (size_t)blockIdx.x * D + t;
+    if constexpr (KIND == A_F32) static_cast<float*>(a.out)[at] = res;
+    else static_cast<uint16_t*>(a.out)[at] = f32_to_bf16(res);
+    if (a.lse && t == 0) a.lse[blockIdx.x] = Lt == 0.f ? -INFINITY : top * kLn2 + logf(Lt);
 }
 
-template <int KIND, int D>
+template <int KIND, int D, int QT>
 static hipError_t launch_decode(const AttnDecodeArgs& a, hipStream_t st) {
-    const int qtiles = (a.Hq / a.Hkv + 15) / 16;
-    const unsigned grid = (unsigned)((size_t)a.B * a.S * qtiles * a.Hkv);
-    hipLaunchKernelGGL((beam_attn_decode<KIND, D>), dim3(grid), dim3(256), 0, st, a, qtiles);
+    const int qgroups = (a.Hq / a.Hkv + 16 * QT - 1) / (16 * QT);
+    const size_t work = (size_t)a.B * a.S * a.Hkv;
+    const unsigned grid = (unsigned)((work + 7) / 8 * 8 * qgroups);
+    hipLaunchKernelGGL((beam_attn_decode<KIND, D, QT>), dim3(grid), dim3(256), 0, st, a, qgroups);
     hipError_t err = hipGetLastError();
     if (err != hipSuccess || a.S == 1) return err;
-    const dim3 jgrid((a.B * a.Hq + 3) / 4);
-    hipLaunchKernelGGL((beam_attn_join<KIND != A_F32, D>), jgrid, dim3(256), 0, st, a);
+    hipLaunchKernelGGL((beam_attn_join<KIND, D>), dim3((unsigned)((size_t)a.B * a.Hq)), dim3(256), 0, st, a);
     return hipGetLastError();
 }
 
+// Above 16 queries per key-value head a wave takes 32 at once, so the cache
+// is read half as often; at D = 256 their sums would not fit the registers.
 template <int KIND>
 static hipError_t launch_decode_d(const AttnDecodeArgs& a, hipStream_t st) {
-    if (a.D == 64) return launch_decode<KIND, 64>(a, st);
-    if (a.D == 128) return launch_decode<KIND, 128>(a, st);
-    return launch_decode<KIND, 256>(a, st);
+    const bool wide = a.Hq / a.Hkv > 16;
+    if (a.D == 64) return wide ? launch_decode<KIND, 64, 2>(a, st) : launch_decode<KIND, 64, 1>(a, st);
+    if (a.D == 128) return wide ? launch_decode<KIND, 128, 2>(a, st) : launch_decode<KIND, 128, 1>(a, st);
+    return launch_decode<KIND, 256, 1>(a, st);
 }
 
 hipError_t launch_attn_decode(const AttnDecodeArgs& a, hipStream_t st) {
