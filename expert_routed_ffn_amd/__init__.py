@@ -547,56 +547,71 @@ def moe_layer(cfg: LayerCfg, x, w_router, bias, w_gate_up, w_down, h, gamma_post
 
 # ------------------------------------------------------------------ attention sublayer
 
-_ACTS = (torch.bfloat16, torch.float32)
+_ACTS = {torch.float32: BEAM_F32, torch.bfloat16: BEAM_BF16}
 _CODES = (torch.uint8, torch.float8_e4m3fn)
 
+# A decode step calls these entry points with a handful of small tensors, so
+# the checks are one expression per tensor and the message is made only for a
+# tensor that fails (on an idle host 9 us a call instead of 12).  `dev` is a
+# device index.
 
-def _on(dev, t, shape, dtypes, name):
-    """Pointer of a dense tensor of this shape on `dev`."""
-    if t.shape != shape:
+
+def _refuse(dev, t, shape, dtype, name):
+    if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name}: shape {tuple(t.shape)} != {tuple(shape)}")
-    if t.dtype not in dtypes:
-        raise ValueError(f"{name}: dtype {t.dtype} not in {dtypes}")
-    if t.device != dev:
-        raise ValueError(f"{name}: on {t.device}, not on {dev}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name}: must be contiguous")
-    return t.data_ptr()
+    if t.dtype != dtype:
+        raise ValueError(f"{name}: dtype {t.dtype} != {dtype}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: on {t.device}, not on cuda:{dev}")
+    raise ValueError(f"{name}: must be contiguous")
+
+
+def _on(dev, t, shape, dtype, name):
+    """Pointer of a dense tensor of this shape and dtype on device `dev`."""
+    if t.shape == shape and t.dtype is dtype and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
+    _refuse(dev, t, shape, dtype, name)
 
 
 def _heads(dev, t, T, heads, dim, dtype, name):
     """Pointer and row stride of [T, heads, dim] rows whose heads are adjacent
     (a dense tensor or columns of a wider row-major matrix)."""
-    if t.shape != (T, heads, dim):
-        raise ValueError(f"{name}: shape {tuple(t.shape)} != {(T, heads, dim)}")
-    if t.dtype != dtype:
-        raise ValueError(f"{name}: dtype {t.dtype} != {dtype}")
-    if t.device != dev:
-        raise ValueError(f"{name}: on {t.device}, not on {dev}")
+    if t.shape != (T, heads, dim) or t.dtype is not dtype or t.get_device() != dev:
+        _refuse(dev, t, (T, heads, dim), dtype, name)
     row, head, one = t.stride()
     if one != 1 or (head != dim and heads > 1):
         raise ValueError(f"{name}: the heads of a token must be adjacent")
     return t.data_ptr(), (row if T > 1 else heads * dim)
 
 
-def _gpu(t):
-    if not t.is_cuda:
+def _rows(q, name):
+    """Device index, rows, dtype and its code of an activation tensor."""
+    dev, dt = q.get_device(), q.dtype
+    if dev < 0:
         raise ValueError("tensors must live on the GPU")
-    return t.device
+    code = _ACTS.get(dt)
+    if code is None:
+        raise ValueError(f"{name}: dtype {dt} not in {tuple(_ACTS)}")
+    return dev, len(q), dt, code
 
 
 def _launch(fn, dev, stream, *args):
     """Calls an entry point with the device of its tensors current, on
     `stream` (default: that device's current stream)."""
-    if isinstance(stream, torch.cuda.Stream) and stream.device != dev:
-        raise ValueError(f"stream of {stream.device} for tensors on {dev}")
-    f = getattr(lib(), fn)
-    if dev.index == torch.cuda.current_device():
-        st = f(*args, _stream(stream))
+    if stream is None:
+        stream = torch._C._cuda_getCurrentRawStream(dev)
+    elif isinstance(stream, torch.cuda.Stream):
+        if stream.device_index != dev:
+            raise ValueError(f"stream of {stream.device} for tensors on cuda:{dev}")
+        stream = stream.cuda_stream
+    f = getattr(_lib or lib(), fn)
+    if dev == torch._C._cuda_getDevice():
+        st = f(*args, stream)
     else:
         with torch.cuda.device(dev):
-            st = f(*args, _stream(stream))
-    _ok(fn, st)
+            st = f(*args, stream)
+    if st:
+        raise BeamError(fn, st)
 
 
 @dataclasses.dataclass(frozen=True)
@@ -611,27 +626,32 @@ class KVCache:
 
     def __post_init__(self):
         k, v = self.k, self.v
-        dev = _gpu(k)
+        dev = k.get_device()
+        if dev < 0:
+            raise ValueError("tensors must live on the GPU")
         if k.dim() != 4:
             raise ValueError(f"k: {k.dim()} dims, not [n_pages, n_kv_heads, page_size, head_dim]")
-        kp = _on(dev, k, k.shape, _ACTS + _CODES, "k")
-        vp = _on(dev, v, k.shape, (k.dtype,), "v")
+        if k.dtype not in _ACTS and k.dtype not in _CODES:
+            raise ValueError(f"k: dtype {k.dtype} not in {tuple(_ACTS) + _CODES}")
+        kp = _on(dev, k, k.shape, k.dtype, "k")
+        vp = _on(dev, v, k.shape, k.dtype, "v")
         ks = vs = None
         if k.dtype in _CODES:
             if self.k_scale is None or self.v_scale is None:
                 raise ValueError("e4m3 codes need k_scale and v_scale")
-            ks = _on(dev, self.k_scale, k.shape[:3], (torch.float32,), "k_scale")
-            vs = _on(dev, self.v_scale, k.shape[:3], (torch.float32,), "v_scale")
+            ks = _on(dev, self.k_scale, k.shape[:3], torch.float32, "k_scale")
+            vs = _on(dev, self.v_scale, k.shape[:3], torch.float32, "v_scale")
         elif self.k_scale is not None or self.v_scale is not None:
             raise ValueError("scales go with e4m3 codes only")
         object.__setattr__(self, "_c", BeamMoeKvCache(kp, vp, ks, vs, k.shape[0], _dt(k)))
+        object.__setattr__(self, "_page", tuple(k.shape[1:]))
+        object.__setattr__(self, "_dev", dev)
 
-    def c(self, cfg: AttnCfg, dev) -> BeamMoeKvCache:
-        if self.k.shape[1:] != (cfg.n_kv_heads, cfg.page_size, cfg.head_dim):
-            raise ValueError(f"cache pages {tuple(self.k.shape[1:])} != "
-                             f"{(cfg.n_kv_heads, cfg.page_size, cfg.head_dim)}")
-        if self.k.device != dev:
-            raise ValueError(f"cache on {self.k.device}, not on {dev}")
+    def c(self, cfg: AttnCfg, dev: int) -> BeamMoeKvCache:
+        if self._page != (cfg.n_kv_heads, cfg.page_size, cfg.head_dim):
+            raise ValueError(f"cache pages {self._page} != {(cfg.n_kv_heads, cfg.page_size, cfg.head_dim)}")
+        if self._dev != dev:
+            raise ValueError(f"cache on cuda:{self._dev}, not on cuda:{dev}")
         return self._c
 
 
@@ -648,22 +668,20 @@ def kv_cache(cfg: AttnCfg, n_pages: int, dtype: int, device="cuda") -> KVCache:
 
 def _prep(cfg, q, k, positions, inv_freq, gamma_q, gamma_k, q_out):
     """Checks and arguments that both norm/rotation calls share."""
-    dev = _gpu(q)
-    T, dt, D = q.shape[0], q.dtype, cfg.head_dim
-    if dt not in _ACTS:
-        raise ValueError(f"q: dtype {dt} not in {_ACTS}")
-    qp, qs = _heads(dev, q, T, cfg.n_heads, D, dt, "q")
+    dev, T, dt, code = _rows(q, "q")
+    hq, D = cfg.n_heads, cfg.head_dim
+    qp, qs = _heads(dev, q, T, hq, D, dt, "q")
     kp, ks = _heads(dev, k, T, cfg.n_kv_heads, D, dt, "k")
-    gq = None if gamma_q is None else _on(dev, gamma_q, (D,), (dt,), "gamma_q")
-    gk = None if gamma_k is None else _on(dev, gamma_k, (D,), (dt,), "gamma_k")
-    pp = _on(dev, positions, (T,), (torch.int32,), "positions")
+    gq = None if gamma_q is None else _on(dev, gamma_q, (D,), dt, "gamma_q")
+    gk = None if gamma_k is None else _on(dev, gamma_k, (D,), dt, "gamma_k")
+    pp = _on(dev, positions, (T,), torch.int32, "positions")
     fp = None
     if cfg.rope_dim:
         if inv_freq is None:
             raise ValueError("inv_freq: needed for rope_dim > 0")
-        fp = _on(dev, inv_freq, (cfg.rope_dim // 2,), (torch.float32,), "inv_freq")
-    qo = _on(dev, q_out, q.shape, (dt,), "q_out")
-    return dev, T, dt, qp, qs, kp, ks, gq, gk, pp, fp, qo
+        fp = _on(dev, inv_freq, (cfg.rope_dim // 2,), torch.float32, "inv_freq")
+    qo = _on(dev, q_out, (T, hq, D), dt, "q_out")
+    return dev, T, dt, code, qp, qs, kp, ks, gq, gk, pp, fp, qo
 
 
 def beam_moe_qk_norm_rope(cfg: AttnCfg, q, k, positions, q_out, k_out, inv_freq=None, gamma_q=None, gamma_k=None,
@@ -671,48 +689,46 @@ def beam_moe_qk_norm_rope(cfg: AttnCfg, q, k, positions, q_out, k_out, inv_freq=
     """Per-head RMSNorm of q [T,n_heads,D] and k [T,n_kv_heads,D], the
     rotation by positions [T] and the queries' position factor, into dense
     q_out and k_out.  q and k may be columns of a merged projection."""
-    dev, T, dt, qp, qs, kp, ks, gq, gk, pp, fp, qo = _prep(cfg, q, k, positions, inv_freq, gamma_q, gamma_k, q_out)
-    ko = _on(dev, k_out, k.shape, (dt,), "k_out")
-    _launch("beam_moe_qk_norm_rope", dev, stream, cfg.c(), T, qp, qs, kp, ks, _dt(q), gq, gk, pp, fp, qo, ko)
+    dev, T, dt, code, qp, qs, kp, ks, gq, gk, pp, fp, qo = _prep(cfg, q, k, positions, inv_freq, gamma_q, gamma_k,
+                                                                 q_out)
+    ko = _on(dev, k_out, (T, cfg.n_kv_heads, cfg.head_dim), dt, "k_out")
+    _launch("beam_moe_qk_norm_rope", dev, stream, cfg._c, T, qp, qs, kp, ks, code, gq, gk, pp, fp, qo, ko)
 
 
 def beam_moe_qk_norm_rope_cache(cfg: AttnCfg, q, k, v, positions, slots, q_out, cache: KVCache, inv_freq=None,
                                 gamma_q=None, gamma_k=None, stream=None):
     """The same for q; k (normed and rotated) and v go into the cache at
     slots [T] (page * page_size + place; -1: not stored)."""
-    dev, T, dt, qp, qs, kp, ks, gq, gk, pp, fp, qo = _prep(cfg, q, k, positions, inv_freq, gamma_q, gamma_k, q_out)
+    dev, T, dt, code, qp, qs, kp, ks, gq, gk, pp, fp, qo = _prep(cfg, q, k, positions, inv_freq, gamma_q, gamma_k,
+                                                                 q_out)
     vp, vs = _heads(dev, v, T, cfg.n_kv_heads, cfg.head_dim, dt, "v")
-    sp = _on(dev, slots, (T,), (torch.int32,), "slots")
-    _launch("beam_moe_qk_norm_rope_cache", dev, stream, cfg.c(), T, qp, qs, kp, ks, vp, vs, _dt(q), gq, gk, pp, fp,
-            sp, qo, cache.c(cfg, dev))
+    sp = _on(dev, slots, (T,), torch.int32, "slots")
+    _launch("beam_moe_qk_norm_rope_cache", dev, stream, cfg._c, T, qp, qs, kp, ks, vp, vs, code, gq, gk, pp, fp, sp,
+            qo, cache.c(cfg, dev))
 
 
 def beam_moe_kv_write(cfg: AttnCfg, k, v, slots, cache: KVCache, stream=None):
     """Stores ready rows k, v [T,n_kv_heads,D] at slots [T]."""
-    dev = _gpu(k)
-    T, dt = k.shape[0], k.dtype
-    if dt not in _ACTS:
-        raise ValueError(f"k: dtype {dt} not in {_ACTS}")
+    dev, T, dt, code = _rows(k, "k")
     kp, ks = _heads(dev, k, T, cfg.n_kv_heads, cfg.head_dim, dt, "k")
     vp, vs = _heads(dev, v, T, cfg.n_kv_heads, cfg.head_dim, dt, "v")
-    sp = _on(dev, slots, (T,), (torch.int32,), "slots")
-    _launch("beam_moe_kv_write", dev, stream, cfg.c(), T, kp, ks, vp, vs, _dt(k), sp, cache.c(cfg, dev))
+    sp = _on(dev, slots, (T,), torch.int32, "slots")
+    _launch("beam_moe_kv_write", dev, stream, cfg._c, T, kp, ks, vp, vs, code, sp, cache.c(cfg, dev))
 
 
 def beam_moe_kv_read(cfg: AttnCfg, cache: KVCache, page_table, row_offsets, k_out, v_out, first=None, stream=None):
     """Rows row_offsets[b] .. row_offsets[b+1]-1 of k_out, v_out
     [N,n_kv_heads,D] get the tokens first[b] (default 0), first[b]+1, ... of
     sequence b of page_table [B,max_pages]; rows behind row_offsets[B] stay."""
-    dev = _gpu(k_out)
-    N, dt, B = k_out.shape[0], k_out.dtype, page_table.shape[0]
+    dev, N, dt, code = _rows(k_out, "k_out")
+    B, width = page_table.shape
     shape = (N, cfg.n_kv_heads, cfg.head_dim)
-    ko = _on(dev, k_out, shape, _ACTS, "k_out")
-    vo = _on(dev, v_out, shape, (dt,), "v_out")
-    tp = _on(dev, page_table, (B, page_table.shape[1]), (torch.int32,), "page_table")
-    op = _on(dev, row_offsets, (B + 1,), (torch.int32,), "row_offsets")
-    fp = None if first is None else _on(dev, first, (B,), (torch.int32,), "first")
-    _launch("beam_moe_kv_read", dev, stream, cfg.c(), B, N, cache.c(cfg, dev), tp, page_table.shape[1], op, fp, ko,
-            vo, _dt(k_out))
+    ko = _on(dev, k_out, shape, dt, "k_out")
+    vo = _on(dev, v_out, shape, dt, "v_out")
+    tp = _on(dev, page_table, (B, width), torch.int32, "page_table")
+    op = _on(dev, row_offsets, (B + 1,), torch.int32, "row_offsets")
+    fp = None if first is None else _on(dev, first, (B,), torch.int32, "first")
+    _launch("beam_moe_kv_read", dev, stream, cfg._c, B, N, cache.c(cfg, dev), tp, width, op, fp, ko, vo, code)
 
 
 def attn_workspace(cfg: AttnCfg, B: int, max_len: int, device="cuda") -> torch.Tensor:
@@ -726,18 +742,19 @@ def beam_moe_attn_decode(cfg: AttnCfg, q, cache: KVCache, page_table, seq_lens, 
     cached tokens of page_table [B,max_pages] and seq_lens [B], into out
     [B,n_heads,D] (and lse [B,n_heads] fp32).  max_len: the longest length to
     expect; ws from attn_workspace(cfg, B, max_len)."""
-    dev = _gpu(q)
-    B, dt = q.shape[0], q.dtype
-    if dt not in _ACTS:
-        raise ValueError(f"q: dtype {dt} not in {_ACTS}")
-    qp, qs = _heads(dev, q, B, cfg.n_heads, cfg.head_dim, dt, "q")
-    tp = _on(dev, page_table, (B, page_table.shape[1]), (torch.int32,), "page_table")
-    lp = _on(dev, seq_lens, (B,), (torch.int32,), "seq_lens")
-    op = _on(dev, out, q.shape, (dt,), "out")
-    ep = None if lse is None else _on(dev, lse, (B, cfg.n_heads), (torch.float32,), "lse")
-    wp = None if ws is None else _on(dev, ws, ws.shape, (torch.uint8,), "ws")
-    _launch("beam_moe_attn_decode", dev, stream, cfg.c(), B, qp, qs, _dt(q), cache.c(cfg, dev), tp,
-            page_table.shape[1], lp, max_len, op, ep, wp, 0 if ws is None else ws.numel())
+    dev, B, dt, code = _rows(q, "q")
+    hq, D, width = cfg.n_heads, cfg.head_dim, page_table.shape[1]
+    qp, qs = _heads(dev, q, B, hq, D, dt, "q")
+    tp = _on(dev, page_table, (B, width), torch.int32, "page_table")
+    lp = _on(dev, seq_lens, (B,), torch.int32, "seq_lens")
+    op = _on(dev, out, (B, hq, D), dt, "out")
+    ep = None if lse is None else _on(dev, lse, (B, hq), torch.float32, "lse")
+    wp, wn = None, 0
+    if ws is not None:
+        wn = ws.numel()
+        wp = _on(dev, ws, (wn,), torch.uint8, "ws")
+    _launch("beam_moe_attn_decode", dev, stream, cfg._c, B, qp, qs, code, cache.c(cfg, dev), tp, width, lp, max_len,
+            op, ep, wp, wn)
 
 
 @dataclasses.dataclass

@@ -23,22 +23,26 @@ namespace beam {
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
-// Tokens per wave step, by cache element: 16 KiB of keys and values at D = 128.
-template <int KIND> constexpr int tile_tokens() { return KIND == A_F32 ? 16 : (KIND == A_BF16 ? 32 : 64); }
-constexpr int kMaxTile = 64;
+// Tokens per wave step, by cache element.
+template <int KIND> constexpr int tile_tokens() { return KIND == A_F32 ? 16 : 32; }
 
-// Parts of a sequence: kMinPart to kMaxPart tokens (a power of two), as many
-// as give the chip about kWantWG workgroups.
-constexpr int kWantWG = 1024, kMinPart = 256, kMaxPart = 1024;
+// Parts of a sequence: kMinPart to kMaxPart tokens (a power of two), no more
+// of them than kWantWG workgroups need while kMaxPart allows.  Two workgroups
+// per CU keep the memory busy, and a sequence in one part needs no join (64
+// sequences, window 512, e4m3: 13.8 us in one part, 24.2 in two); parts are
+// bounded so that a batch of very different lengths still spreads over the
+// chip (1 .. 32768 tokens: 285 us at 2048, 289 at 1024, 302 at 512), until the
+// sequences alone are enough for that (kMostWG, which also bounds the workspace).
+constexpr int kWantWG = 512, kMostWG = 16384, kMinPart = 256, kMaxPart = 2048;
 void attn_decode_split(int B, int Hkv, int max_len, int window, int* S, int* cshift) {
-    // a window's tokens begin inside a tile
-    const int64_t span = window > 0 && window < max_len ? (int64_t)window + kMaxTile - 1 : max_len;
+    // a window's tokens begin inside a 16-token block
+    const int64_t span = window > 0 && window < max_len ? (int64_t)window + 15 : max_len;
     const int64_t heads = (int64_t)B * Hkv;
     int sh = 0;
     while ((1 << sh) < kMinPart) ++sh;
-    while ((1 << sh) < kMaxPart && heads * ((span + (1 << sh) - 1) >> sh) > kWantWG) ++sh;
-    const int64_t s = (span + (1 << sh) - 1) >> sh;
-    *S = s < 1 ? 1 : (int)s;
+    const auto parts = [&] { return span <= (int64_t)1 << sh ? 1 : (span + ((int64_t)1 << sh) - 1) >> sh; };
+    while (parts() > 1 && heads * parts() > ((1 << sh) < kMaxPart ? kWantWG : kMostWG)) ++sh;
+    *S = (int)parts();
     *cshift = sh;
 }
 
@@ -54,12 +58,12 @@ size_t attn_decode_ws_bytes(int B, int Hq, int Hkv, int D, int max_len, int wind
 struct Span {
     int start, len, base, shift, n;
 };
-BEAM_DEV Span span_of(const AttnDecodeArgs& a, int b, int tile) {
+BEAM_DEV Span span_of(const AttnDecodeArgs& a, int b) {
     const int64_t cap = min((int64_t)a.max_pages << a.c.pshift, (int64_t)kMaxLen);
     Span p;
     p.len = (int)min((int64_t)max(a.lens[b], 0), cap);
     p.start = a.window > 0 ? max(0, p.len - a.window) : 0;
-    p.base = p.start & ~(tile - 1);
+    p.base = p.start & ~15;
     const uint32_t all = (uint32_t)(p.len - p.base);
     p.shift = a.cshift;
     while (((uint64_t)a.S << p.shift) < all) ++p.shift;
@@ -75,26 +79,58 @@ BEAM_DEV uint32_t e4m3_hi(uint32_t c) {
     return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c, 1.0f, true));
 }
 
-// NW 32-bit words from global memory (16-, 8- or 4-byte pieces)
-template <int NW> BEAM_DEV void ldw(const void* p, uint32_t (&w)[NW]) {
-    if constexpr (NW % 4 == 0) {
+// NW 32-bit words from global memory (16-, 8- or 4-byte pieces).  STREAM: as
+// non-temporal loads.
+template <int NW, bool STREAM = false> BEAM_DEV void ldw(const void* p, uint32_t (&w)[NW]) {
+    constexpr int PW = NW % 4 == 0 ? 4 : NW;   // words per load
+    typedef uint32_t piece __attribute__((ext_vector_type(PW)));
+    static_assert(NW % PW == 0 && (PW == 4 || PW == 2 || PW == 1), "");
 #pragma unroll
-        for (int i = 0; i < NW / 4; ++i) {
-            const uint4 v = static_cast<const uint4*>(p)[i];
-            w[4 * i] = v.x; w[4 * i + 1] = v.y; w[4 * i + 2] = v.z; w[4 * i + 3] = v.w;
-        }
-    } else if constexpr (NW == 2) {
-        const uint2 v = *static_cast<const uint2*>(p);
-        w[0] = v.x; w[1] = v.y;
-    } else {
-        static_assert(NW == 1, "");
-        w[0] = *static_cast<const uint32_t*>(p);
+    for (int i = 0; i < NW / PW; ++i) {
+        const piece* q = static_cast<const piece*>(p) + i;
+        piece v;
+        if constexpr (STREAM) v = __builtin_nontemporal_load(q);
+        else v = *q;
+#pragma unroll
+        for (int j = 0; j < PW; ++j) w[PW * i + j] = v[j];
     }
 }
 
 BEAM_DEV f32x4 mfma_bf16(uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint4 b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, make_uint4(a0, a1, a2, a3)),
                                                    __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+}
+
+// Transposes 16-byte pieces among groups of N = 2 or 4 neighbouring lanes:
+// lane n's piece i becomes lane i's piece n.
+template <int CTRL> BEAM_DEV uint32_t dpp(uint32_t v) {
+    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, true);
+}
+template <int N> BEAM_DEV void lane_transpose(uint32_t (*w)[4]) {
+    constexpr int kXor1 = 0xB1, kXor2 = 0x4E;   // exchange with the lane 1 or 2 away
+    const bool odd = threadIdx.x & 1, upper = threadIdx.x & 2;
+    if constexpr (N >= 2) {
+#pragma unroll
+        for (int i = 0; i < N; i += 2)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const uint32_t a = w[i][e], b = w[i + 1][e];
+                const uint32_t xa = dpp<kXor1>(a), xb = dpp<kXor1>(b);   // every lane takes part
+                w[i][e] = odd ? xb : a;
+                w[i + 1][e] = odd ? b : xa;
+            }
+    }
+    if constexpr (N == 4) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const uint32_t a = w[i][e], b = w[i + 2][e];
+                const uint32_t xa = dpp<kXor2>(a), xb = dpp<kXor2>(b);
+                w[i][e] = upper ? xb : a;
+                w[i + 2][e] = upper ? b : xa;
+            }
+    }
 }
 
 // maximum over the four lanes (r, 0..3) that hold a query's tokens
@@ -129,6 +165,10 @@ __global__ __launch_bounds__(256) void beam_attn_decode(AttnDecodeArgs a, int qg
     constexpr int DL = D / 16;                                  // value elements per lane and token
     constexpr int NK = KIND == A_F32 ? D / 16 : D / 32;         // key fragments per token
     constexpr int KW = KIND == A_FP8 ? 2 : 4;                   // words per key fragment
+    constexpr int NC = NK * KW / 4;                             // 16-byte key pieces per lane and token
+    constexpr int NT = KIND != A_FP8 ? 1 : (NC < 4 ? NC : 4);   // pieces exchanged among NT lanes
+    constexpr int PF = 4 / KW;                                  // fragments per piece
+    constexpr int KE = 4 * KW / ES;                             // elements per key fragment
     constexpr int VW = DL * ES / 4;                             // words per lane and value row
     __shared__ float sO[4][16][D + 4];
     __shared__ float sM[4][16], sL[4][16];
@@ -145,12 +185,15 @@ __global__ __launch_bounds__(256) void beam_attn_decode(AttnDecodeArgs a, int qg
     const int s = bs % a.S, b = bs / a.S;
     if (b >= a.B) return;
     const int G = a.Hq / a.Hkv;
-    const Span sp = span_of(a, b, TILE);
+    const Span sp = span_of(a, b);
     if (s > 0 && s >= sp.n) return;               // no tokens; part 0 of an empty row goes on
     const int t0 = sp.base + (int)((uint32_t)s << sp.shift);
     const int t1 = (int)min((int64_t)sp.len, (int64_t)t0 + ((int64_t)1 << sp.shift));
 
-    // query fragments: lane (r, g) holds column r of each 16-query block
+    // query fragments: lane (r, g) holds column r of each 16-query block; the
+    // reduction index (g, c, j) stands for the key element that lane g's
+    // fragment c holds in place j: its quarter of the row in order (NT > 1), or
+    // every fourth piece
     uint32_t qf[QT][NK][4];
 #pragma unroll
     for (int j = 0; j < QT; ++j) {
@@ -158,8 +201,8 @@ __global__ __launch_bounds__(256) void beam_attn_decode(AttnDecodeArgs a, int qg
         const size_t qoff = (size_t)b * a.qs + (size_t)(h * G + min(qrow, G - 1)) * D;
 #pragma unroll
         for (int c = 0; c < NK; ++c) {
-            if constexpr (KIND == A_F32) ldw<4>(static_cast<const float*>(a.q) + qoff + 16 * c + 4 * g, qf[j][c]);
-            else ldw<4>(static_cast<const uint16_t*>(a.q) + qoff + 32 * c + 8 * g, qf[j][c]);
+            if constexpr (KIND == A_F32) ldw<4>(static_cast<const float*>(a.q) + qoff + KE * (4 * c + g), qf[j][c]);
+            else ldw<4>(static_cast<const uint16_t*>(a.q) + qoff + KE * (NT > 1 ? NK * g + c : (c / PF * 4 + g) * PF + c % PF), qf[j][c]);
         }
     }
 
@@ -202,20 +245,31 @@ __global__ __launch_bounds__(256) void beam_attn_decode(AttnDecodeArgs a, int qg
             full = full && ok[u];
             row[u] = (((size_t)(ok[u] ? pg[u] : 0) * a.Hkv + h) << a.c.pshift) + ((tile + 16 * u) & pmask);
         }
-        uint32_t kw[NU][NK][KW], vw[NU][4][VW];
+        uint32_t kw[NU][NC][4], vw[NU][4][VW];
         float4 ks[NU], vs[NU];
 #pragma unroll
         for (int u = 0; u < NU; ++u) {
-            const uint8_t* kr = kc + (row[u] + r) * (D * ES) + g * (KW * 4);
+            // bf16, fp32: the four lanes of a row read 64 bytes of it at a time.
+            // e4m3: NT neighbouring lanes read one row's pieces side by side,
+            // the lowest lane's row, then the next one's, and exchange them
+            // below: the cache unit takes four lanes at a time, in pieces that
+            // adjoin, and at one byte an element those accesses bound the kernel
+            const uint8_t* kr = kc + (row[u] + (r & ~(NT - 1))) * (D * ES) +
+                                (NT > 1 ? g * (D * ES / 4) + (r & (NT - 1)) * 16 : g * 16);
 #pragma unroll
-            for (int c = 0; c < NK; ++c) ldw<KW>(kr + c * (16 * KW), kw[u][c]);
+            for (int c = 0; c < NC; ++c)
+                ldw<4>(kr + (NT > 1 ? (c % NT) * (D * ES) + (c / NT) * (NT * 16) : c * 64), kw[u][c]);
             if constexpr (KIND == A_FP8) ks[u] = *reinterpret_cast<const float4*>(a.c.ks + row[u] + 4 * g);
         }
 #pragma unroll
         for (int u = 0; u < NU; ++u) {
+            // streamed: whole cache lines of a wave's load, read by no one else
+            // while they matter (64 sequences of 8192 tokens: bf16 391 -> 356 us,
+            // e4m3 217 -> 203 us; the keys too: 358 and 197 us, but a quarter
+            // slower where two waves read the same keys or the lines are split)
             const uint8_t* vr = vc + (row[u] + 4 * g) * (D * ES) + r * (VW * 4);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) ldw<VW>(vr + i * (D * ES), vw[u][i]);
+            for (int i = 0; i < 4; ++i) ldw<VW, true>(vr + i * (D * ES), vw[u][i]);
             if constexpr (KIND == A_FP8) vs[u] = *reinterpret_cast<const float4*>(a.c.vs + row[u] + 4 * g);
         }
         pages_of(tile + STEP, pg);
@@ -225,6 +279,11 @@ __global__ __launch_bounds__(256) void beam_attn_decode(AttnDecodeArgs a, int qg
         float p[QT][NU][4];
 #pragma unroll
         for (int u = 0; u < NU; ++u) {
+            if constexpr (NT > 1) {
+#pragma unroll
+                for (int c = 0; c < NC; c += NT) lane_transpose<NT>(&kw[u][c]);   // to each lane its own row
+            }
+            const auto key = [&](int c, int e) { return kw[u][(c * KW + e) / 4][(c * KW + e) % 4]; };
             f32x4 z[QT];
 #pragma unroll
             for (int j = 0; j < QT; ++j) z[j] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -236,17 +295,17 @@ __global__ __launch_bounds__(256) void beam_attn_decode(AttnDecodeArgs a, int qg
 #pragma unroll
                         for (int j = 0; j < QT; ++j)
                             z[j] = __builtin_amdgcn_mfma_f32_16x16x4f32(
-                                __uint_as_float(kw[u][c][e]), __uint_as_float(qf[j][c][e]), z[j], 0, 0, 0);
+                                __uint_as_float(key(c, e)), __uint_as_float(qf[j][c][e]), z[j], 0, 0, 0);
                 } else {
                     uint32_t w[4];
                     if constexpr (KIND == A_BF16) {
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) w[e] = kw[u][c][e];
+                        for (int e = 0; e < 4; ++e) w[e] = key(c, e);
                     } else {
-                        w[0] = e4m3_lo(kw[u][c][0]);
-                        w[1] = e4m3_hi(kw[u][c][0]);
-                        w[2] = e4m3_lo(kw[u][c][1]);
-                        w[3] = e4m3_hi(kw[u][c][1]);
+                        w[0] = e4m3_lo(key(c, 0));
+                        w[1] = e4m3_hi(key(c, 0));
+                        w[2] = e4m3_lo(key(c, 1));
+                        w[3] = e4m3_hi(key(c, 1));
                     }
 #pragma unroll
                     for (int j = 0; j < QT; ++j)
@@ -458,7 +517,7 @@ __global__ __launch_bounds__(256) void beam_attn_join(AttnDecodeArgs a) {
         }
     };
     load(grp);
-    const int n = span_of(a, b, tile_tokens<KIND>()).n;
+    const int n = span_of(a, b).n;
     if (n <= 1) return;                           // its only part wrote the result
     float M = -INFINITY, L = 0.f;
     float4 O = make_float4(0.f, 0.f, 0.f, 0.f);

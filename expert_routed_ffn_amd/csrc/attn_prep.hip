@@ -82,22 +82,40 @@ template <int LPH> BEAM_DEV float head_max(float v) {
     return head_reduce<LPH>(v, [](float a, float b) { return fmaxf(a, b); });
 }
 
+// The 8 quotients x / s, correctly rounded.  They share s, so its reciprocal
+// is formed once, to the last bit but for rare cases, and each quotient takes a
+// product, its exact remainder and a correction by it (Markstein 1990), where
+// no step can leave the range of normal numbers; __fdiv_rn elsewhere.
+BEAM_DEV void divide8(float (&x)[8], float s) {
+    if (__any(!(s > 1e-25f && s < 1e25f))) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] = __fdiv_rn(x[j], s);
+        return;
+    }
+    const float y0 = __builtin_amdgcn_rcpf(s);
+    const float y1 = fmaf(fmaf(-s, y0, 1.0f), y0, y0);
+    const float y = fmaf(fmaf(-s, y1, 1.0f), y1, y1);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const float q = x[j] * y;
+        x[j] = fmaf(fmaf(-q, s, x[j]), y, q);
+    }
+}
+
 // Stores a head row's 8 elements of this lane at row `row` of one cache
 // side.  e4m3: the scale and codes that quantize_row_e4m3_wave gives a row.
 template <int CK, int D>
-BEAM_DEV void store_cache(void* side, float* scales, size_t row, int e0, const float (&x)[8], bool live) {
+BEAM_DEV void store_cache(void* side, float* scales, size_t row, int e0, float (&x)[8], bool live) {
     if constexpr (CK == A_FP8) {
         float amax = 0.f;
 #pragma unroll
         for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(x[j]));
         amax = head_max<D / 8>(amax);   // every lane takes part
         const float s = amax > 0.f ? __fdiv_rn(amax, 448.0f) : 1.0f;
+        divide8(x, s);
         if (!live) return;
-        float y[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) y[j] = __fdiv_rn(x[j], s);
         *reinterpret_cast<uint2*>(static_cast<uint8_t*>(side) + row * D + e0) =
-            make_uint2(e4m3x4(y[0], y[1], y[2], y[3]), e4m3x4(y[4], y[5], y[6], y[7]));
+            make_uint2(e4m3x4(x[0], x[1], x[2], x[3]), e4m3x4(x[4], x[5], x[6], x[7]));
         if (e0 == 0) scales[row] = s;
     } else {
         if (live) st8<CK == A_BF16>(side, row * D + e0, x);
@@ -106,41 +124,69 @@ BEAM_DEV void store_cache(void* side, float* scales, size_t row, int e0, const f
 
 // ---------------------------------------------------------------------------
 // Units of a token: its Hq query heads, Hkv key heads and (into the cache)
-// Hkv value heads.  A wave takes `gpw` consecutive groups of 512/D units of
-// one token; the rotation's cosines and sines depend on the lane's place in
-// the head only, so they are formed once per wave.
+// Hkv value heads, in that order.  A wave takes `gpw` consecutive groups of
+// 512/D units of one token; the rotation's cosines and sines depend on the
+// lane's place in the head only, so they are formed once per wave, one or two
+// frequencies per lane, and handed round.
 // ---------------------------------------------------------------------------
 template <bool BF, int CK, int D>
 __global__ __launch_bounds__(256) void beam_attn_prep(AttnPrepArgs a, int units, int wpt, int gpw) {
     constexpr int LPH = D / 8, HPW = kWave / LPH;
     const int lane = threadIdx.x & 63;
-    const int wid = blockIdx.x * 4 + (threadIdx.x >> 6);
+    const int wid = blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int t = wid / wpt;
     if (t >= a.T) return;   // whole wave
     const int g0 = (wid - t * wpt) * gpw;
+    const int gend = min(g0 + gpw, (units + HPW - 1) / HPW);
     const int li = lane % LPH, e0 = li * 8;
 
-    // cos/sin of the angles of this lane's elements: half-split, element e0+j
-    // of the rotated dims has frequency (e0 + j) mod R/2; interleaved, the
-    // pair (e0 + 2j, e0 + 2j + 1) has frequency e0/2 + j
+    // this lane's place in each matrix's row of the token
+    const size_t esz = BF ? 2 : 4;
+    const char* qrow = static_cast<const char*>(a.q) + ((size_t)t * a.qs + e0) * esz;
+    const char* krow = static_cast<const char*>(a.k) + ((size_t)t * a.ks + e0) * esz;
+    const char* vrow = static_cast<const char*>(a.v) + ((size_t)t * a.vs + e0) * esz;
+    auto load = [&](int gi) {   // lanes past the last unit load it again
+        const int u = min(gi * HPW + lane / LPH, units - 1);
+        const char* p = qrow + (size_t)u * (D * esz);
+        if ((gi + 1) * HPW > a.Hq) {
+            const int k = u - a.Hq, v = k - a.Hkv;
+            p = k < 0 ? p : (v < 0 ? krow + (size_t)k * (D * esz) : vrow + (size_t)v * (D * esz));
+        }
+        return ld8<BF>(p, 0);
+    };
+    Raw8<BF> next = load(g0);   // a group's loads are in flight while the group before it is worked on
+
+    // The angles' cosines and sines for this lane's elements: half-split,
+    // element e0 + j of the rotated dims has frequency (e0 + j) mod R/2, and
+    // the sine enters the lower half with a minus; interleaved, the pair
+    // (e0 + 2j, e0 + 2j + 1) has frequency e0/2 + j.
     float cs[8], sn[8];
     const int half = a.R / 2;
     const bool turns = e0 < a.R;
     if (a.R > 0) {
         const double p = (double)a.pos[t];
+        float c[2], s[2];
+        auto angle = [&](int k) {
+            // whole turns drop out in fp64, so far positions keep their angle
+            double rev = p * ((double)a.inv_freq[min(lane + 64 * k, half - 1)] * 0.15915494309189533577);
+            rev -= rint(rev);
+            sincospif((float)(2.0 * rev), &s[k], &c[k]);
+        };
+        angle(0);
+        if (D > 128 && half > 64) angle(1);
         const int f0 = a.inter ? e0 / 2 : (e0 < half ? e0 : e0 - half);
+        const float sg = !a.inter && e0 < half ? -1.f : 1.f;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             const int f = f0 + j;
-            if (turns && f < half && !(a.inter && j >= 4)) {
-                // whole turns drop out in fp64, so far positions keep their angle
-                double rev = p * ((double)a.inv_freq[f] * 0.15915494309189533577);
-                rev -= rint(rev);
-                sincospif((float)(2.0 * rev), &sn[j], &cs[j]);
-            } else {
-                cs[j] = 1.f;
-                sn[j] = 0.f;
+            cs[j] = __shfl(c[0], f & 63, kWave);
+            sn[j] = __shfl(s[0], f & 63, kWave);
+            if (D > 128 && half > 64) {
+                const float c1 = __shfl(c[1], f & 63, kWave), s1 = __shfl(s[1], f & 63, kWave);
+                cs[j] = f >= 64 ? c1 : cs[j];
+                sn[j] = f >= 64 ? s1 : sn[j];
             }
+            sn[j] *= sg;
         }
     }
     float qf = 1.f;
@@ -150,41 +196,35 @@ __global__ __launch_bounds__(256) void beam_attn_prep(AttnPrepArgs a, int units,
         slot = a.slots[t];
         if ((int64_t)slot >= ((int64_t)a.c.n_pages << a.c.pshift)) slot = -1;
     }
+    float g[8];
+    if (a.gq) wid8(ld8<BF>(a.gq, e0), g);
+    bool g_is_q = true;
 
-    // the next group's loads are in flight while a group is worked on
-    const int gend = min(g0 + gpw, (units + HPW - 1) / HPW);
-    auto load = [&](int gi) {
-        const int u = min(gi * HPW + lane / LPH, units - 1);
-        const bool is_q = u < a.Hq, is_v = u >= a.Hq + a.Hkv;
-        const void* src = is_q ? a.q : (is_v ? a.v : a.k);
-        const size_t rs = is_q ? a.qs : (is_v ? a.vs : a.ks);
-        const int h = is_q ? u : (is_v ? u - a.Hq - a.Hkv : u - a.Hq);
-        return ld8<BF>(src, (size_t)t * rs + (size_t)h * D + e0);
-    };
-    float gq[8], gk[8];
-    if (a.gq) {
-        wid8(ld8<BF>(a.gq, e0), gq);
-        wid8(ld8<BF>(a.gk, e0), gk);
-    }
-    Raw8<BF> next = load(g0);
     for (int gi = g0; gi < gend; ++gi) {
         const int u = gi * HPW + lane / LPH;
-        const bool is_q = u < a.Hq;
-        const bool is_v = u >= a.Hq + a.Hkv;
-        const bool in = u < units;   // lanes past the last unit go along with it and store nothing
-        const int h = is_q ? u : (is_v ? u - a.Hq - a.Hkv : u - a.Hq);
+        const bool only_q = (gi + 1) * HPW <= a.Hq;   // the same for the whole wave
+        const bool is_q = only_q || u < a.Hq;
+        const bool is_v = !only_q && u >= a.Hq + a.Hkv;
         float x[8];
         wid8(next, x);
         if (gi + 1 < gend) next = load(gi + 1);
+        float f = 1.f;
         if (a.gq) {
+            if (!only_q && g_is_q) {   // units only go on from queries to keys to values
+                float gk[8];
+                wid8(ld8<BF>(a.gk, e0), gk);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) g[j] = is_q ? g[j] : gk[j];
+                g_is_q = gi * HPW < a.Hq;   // lanes of this group that are queries change at the next
+            }
             float ss = 0.f;
 #pragma unroll
             for (int j = 0; j < 8; ++j) ss = fmaf(x[j], x[j], ss);
             ss = head_sum<LPH>(ss);
             if (!is_v) {
-                const float rinv = 1.0f / sqrtf(ss * (1.0f / D) + a.eps);
+                f = 1.0f / sqrtf(ss * (1.0f / D) + a.eps);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) x[j] = x[j] * rinv * (is_q ? gq[j] : gk[j]);
+                for (int j = 0; j < 8; ++j) x[j] *= g[j];
             }
         }
         if (a.R > 0) {
@@ -199,7 +239,6 @@ __global__ __launch_bounds__(256) void beam_attn_prep(AttnPrepArgs a, int units,
                 }
             } else {
                 const int d = a.R / 16;   // lanes between the two elements of a pair
-                const float sg = e0 < half ? -1.f : 1.f;
                 float o[8];
                 if (d == 8) {             // the other half of a row of 16 lanes
 #pragma unroll
@@ -211,22 +250,25 @@ __global__ __launch_bounds__(256) void beam_attn_prep(AttnPrepArgs a, int units,
                 }
                 if (!is_v && turns) {
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) x[j] = x[j] * cs[j] + sg * (o[j] * sn[j]);
+                    for (int j = 0; j < 8; ++j) x[j] = fmaf(o[j], sn[j], x[j] * cs[j]);
                 }
             }
         }
-        if (is_q) {
+        if (is_q) f *= qf;
+        if (!is_v) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) x[j] *= qf;
-            st8<BF>(a.q_out, ((size_t)t * a.Hq + h) * D + e0, x);
+            for (int j = 0; j < 8; ++j) x[j] *= f;
         }
+        if (is_q) st8<BF>(a.q_out, ((size_t)t * a.Hq + u) * D + e0, x);
+        if (only_q) continue;
+        const bool kv = !is_q && u < units;   // lanes past the last unit store nothing
+        const int h = is_v ? u - a.Hq - a.Hkv : u - a.Hq;
         if constexpr (CK < 0) {
-            if (in && !is_q) st8<BF>(a.k_out, ((size_t)t * a.Hkv + h) * D + e0, x);
-        } else if (gi * HPW + HPW > a.Hq) {   // a group with keys or values
+            if (kv) st8<BF>(a.k_out, ((size_t)t * a.Hkv + h) * D + e0, x);
+        } else {
             const size_t page = slot >= 0 ? (size_t)(slot >> a.c.pshift) : 0;
             const size_t row = ((page * a.Hkv + h) << a.c.pshift) + (slot & ((1 << a.c.pshift) - 1));
-            store_cache<CK, D>(is_v ? a.c.v : a.c.k, is_v ? a.c.vs : a.c.ks, row, e0, x,
-                               in && !is_q && slot >= 0);
+            store_cache<CK, D>(is_v ? a.c.v : a.c.k, is_v ? a.c.vs : a.c.ks, row, e0, x, kv && slot >= 0);
         }
     }
 }
@@ -268,65 +310,106 @@ hipError_t launch_attn_prep(const AttnPrepArgs& a, hipStream_t st) {
 }
 
 // ---------------------------------------------------------------------------
-// Cache rows back to dense rows.  A workgroup takes kReadRows consecutive
-// output rows; thread group (row, head, side) of D/8 lanes copies one head
-// row.
+// Cache rows back to dense rows.  A workgroup takes `rows` (at most 64)
+// consecutive output rows: each lane finds one row's place in the cache, then
+// groups of D/8 lanes copy one head row of one side at a time, kReadBatch of
+// them with all their loads in flight.
 // ---------------------------------------------------------------------------
-template <int CK> BEAM_DEV void load_cache8(const void* side, const float* scales, size_t row, int D, int e0,
-                                            float (&x)[8]) {
+template <int CK> struct RawC8;                       // 8 cache elements as stored
+template <> struct RawC8<A_BF16> { Raw8<true> v; };
+template <> struct RawC8<A_F32> { Raw8<false> v; };
+template <> struct RawC8<A_FP8> { uint2 v; float s; };
+template <int CK> BEAM_DEV RawC8<CK> ld_cache8(const void* side, const float* scales, size_t row, int D, int e0) {
+    RawC8<CK> r;
     if constexpr (CK == A_FP8) {
-        const uint2 c = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(side) + row * D + e0);
-        const float s = scales[row];
-        typedef float f32x2v __attribute__((ext_vector_type(2)));
-        const f32x2v p0 = __builtin_amdgcn_cvt_pk_f32_fp8((int)c.x, false), p1 = __builtin_amdgcn_cvt_pk_f32_fp8((int)c.x, true);
-        const f32x2v p2 = __builtin_amdgcn_cvt_pk_f32_fp8((int)c.y, false), p3 = __builtin_amdgcn_cvt_pk_f32_fp8((int)c.y, true);
-        x[0] = p0.x * s; x[1] = p0.y * s; x[2] = p1.x * s; x[3] = p1.y * s;
-        x[4] = p2.x * s; x[5] = p2.y * s; x[6] = p3.x * s; x[7] = p3.y * s;
+        r.v = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(side) + row * D + e0);
+        r.s = scales[row];
     } else {
-        wid8(ld8<CK == A_BF16>(side, row * D + e0), x);
+        r.v = ld8<CK == A_BF16>(side, row * D + e0);
+    }
+    return r;
+}
+template <int CK> BEAM_DEV void wid_cache8(const RawC8<CK>& r, float (&x)[8]) {
+    if constexpr (CK == A_FP8) {
+        typedef float f32x2v __attribute__((ext_vector_type(2)));
+        const uint32_t w[2] = {r.v.x, r.v.y};
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const f32x2v lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)w[j], false);
+            const f32x2v hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)w[j], true);
+            x[4 * j] = lo.x * r.s;
+            x[4 * j + 1] = lo.y * r.s;
+            x[4 * j + 2] = hi.x * r.s;
+            x[4 * j + 3] = hi.y * r.s;
+        }
+    } else {
+        wid8(r.v, x);
     }
 }
 
+constexpr int kReadBatch = 4, kReadRowsFrom = 16384;
+
 template <bool BF, int CK, int D>
-__global__ __launch_bounds__(256) void beam_kv_read(KvReadArgs a) {
+__global__ __launch_bounds__(256) void beam_kv_read(KvReadArgs a, int rows) {
     constexpr int LPH = D / 8, HPB = 256 / LPH;
-    const int row = blockIdx.x;
-    // last sequence whose first row is at or before this one
-    int lo = 0, hi = a.B;   // offsets[lo] <= row < offsets[hi], if there is one
-    if (row >= a.offsets[a.B]) return;
+    const int lane = threadIdx.x & 63;
+    const int row0 = blockIdx.x * rows;
+    const int last = a.offsets[a.B];   // rows at and behind it stay
+    if (row0 >= last) return;
+    // lane i: cache row (of head 0) and page of output row row0 + i
+    const int mine = row0 + min(lane, rows - 1);
+    int lo = 0, hi = a.B;              // offsets[lo] <= mine < offsets[hi]
     while (hi - lo > 1) {
         const int mid = (lo + hi) / 2;
-        if (a.offsets[mid] <= row) lo = mid;
+        if (a.offsets[mid] <= mine) lo = mid;
         else hi = mid;
     }
-    const int64_t tok = (int64_t)row - a.offsets[lo] + (a.first ? a.first[lo] : 0);
+    const int64_t tok = (int64_t)mine - a.offsets[lo] + (a.first ? a.first[lo] : 0);
     const int64_t pi = tok >> a.c.pshift;
     int page = -1;
     if (tok >= 0 && pi < a.max_pages) page = a.table[(size_t)lo * a.max_pages + pi];
-    const bool ok = page >= 0 && page < a.c.n_pages;
+    if (page >= a.c.n_pages) page = -1;
     const int off = (int)(tok & ((1 << a.c.pshift) - 1));
+
     const int e0 = (threadIdx.x % LPH) * 8;
-    for (int u = threadIdx.x / LPH; u < 2 * a.Hkv; u += HPB) {
-        const bool is_v = u >= a.Hkv;
-        const int h = is_v ? u - a.Hkv : u;
-        float x[8];
-        if (ok) {
-            load_cache8<CK>(is_v ? a.c.v : a.c.k, is_v ? a.c.vs : a.c.ks,
-                            (((size_t)page * a.Hkv + h) << a.c.pshift) + off, D, e0, x);
-        } else {
+    const int per_row = 2 * a.Hkv, n = min(rows, min(a.N, last) - row0) * per_row;
+    for (int base = 0; base < n; base += kReadBatch * HPB) {
+        RawC8<CK> v[kReadBatch];
+        int row[kReadBatch], h[kReadBatch];
+        bool is_v[kReadBatch], ok[kReadBatch];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) x[j] = 0.f;
+        for (int k = 0; k < kReadBatch; ++k) {
+            const int i = min(base + k * HPB + (int)threadIdx.x / LPH, n - 1);
+            row[k] = i / per_row;
+            h[k] = i - row[k] * per_row;
+            is_v[k] = h[k] >= a.Hkv;
+            if (is_v[k]) h[k] -= a.Hkv;
+            const int pg = __shfl(page, row[k], kWave), at = __shfl(off, row[k], kWave);
+            ok[k] = pg >= 0;
+            const size_t from = (((size_t)(ok[k] ? pg : 0) * a.Hkv + h[k]) << a.c.pshift) + at;
+            v[k] = ld_cache8<CK>(is_v[k] ? a.c.v : a.c.k, is_v[k] ? a.c.vs : a.c.ks, from, D, e0);
         }
-        st8<BF>(is_v ? a.v_out : a.k_out, ((size_t)row * a.Hkv + h) * D + e0, x);
+#pragma unroll
+        for (int k = 0; k < kReadBatch; ++k) {
+            if (base + k * HPB + (int)threadIdx.x / LPH >= n) continue;
+            float x[8];
+            wid_cache8<CK>(v[k], x);
+            if (!ok[k]) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) x[j] = 0.f;
+            }
+            st8<BF>(is_v[k] ? a.v_out : a.k_out, ((size_t)(row0 + row[k]) * a.Hkv + h[k]) * D + e0, x);
+        }
     }
 }
 
 template <bool BF, int CK>
 static void launch_read_d(const KvReadArgs& a, hipStream_t st) {
-    const dim3 grid(a.N), block(256);
-    if (a.D == 64) hipLaunchKernelGGL((beam_kv_read<BF, CK, 64>), grid, block, 0, st, a);
-    else if (a.D == 128) hipLaunchKernelGGL((beam_kv_read<BF, CK, 128>), grid, block, 0, st, a);
-    else hipLaunchKernelGGL((beam_kv_read<BF, CK, 256>), grid, block, 0, st, a);
+    const int rows = a.N >= kReadRowsFrom ? 16 : 4;
+    const dim3 grid((a.N + rows - 1) / rows), block(256);
+    if (a.D == 64) hipLaunchKernelGGL((beam_kv_read<BF, CK, 64>), grid, block, 0, st, a, rows);
+    else if (a.D == 128) hipLaunchKernelGGL((beam_kv_read<BF, CK, 128>), grid, block, 0, st, a, rows);
+    else hipLaunchKernelGGL((beam_kv_read<BF, CK, 256>), grid, block, 0, st, a, rows);
 }
 
 template <bool BF>

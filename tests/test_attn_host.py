@@ -172,7 +172,7 @@ def test_binding_refusals():
     with pytest.raises(ValueError):
         beam.KVCache(torch.zeros((2, 1, 64, 64)), torch.zeros((2, 1, 64, 64)))
     m = torch.zeros((3, 4, 64), dtype=torch.bfloat16)
-    dev = m.device
+    dev = -1      # the CPU, as a device index
     assert beam._heads(dev, m[:, 1:3], 3, 2, 64, m.dtype, "x")[1] == 256
     assert beam._heads(dev, m[:1, 1:3], 1, 2, 64, m.dtype, "x")[1] == 128      # one row: no stride to keep
     for bad in (m[:, ::2], m.transpose(0, 1)[:3, :2], m[:, :2].float(), m[:, :3]):
