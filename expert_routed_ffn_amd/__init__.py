@@ -614,11 +614,12 @@ def _launch(fn, dev, stream, *args):
         raise BeamError(fn, st)
 
 
-@dataclasses.dataclass(frozen=True)
+@dataclasses.dataclass(frozen=True, eq=False)
 class KVCache:
     """The paged key-value cache of one layer: k, v [n_pages, n_kv_heads,
     page_size, head_dim] in bf16, fp32 or e4m3 codes (float8_e4m3fn or
-    uint8); the codes with fp32 scales [n_pages, n_kv_heads, page_size]."""
+    uint8); the codes with fp32 scales [n_pages, n_kv_heads, page_size].  The
+    tensors are checked here, once, and must keep their storage."""
     k: torch.Tensor
     v: torch.Tensor
     k_scale: torch.Tensor | None = None

@@ -9,8 +9,9 @@
 
 namespace {
 
-constexpr int64_t kMaxT = 1 << 22;          // tokens (or sequences, or rows read) per call
-constexpr int64_t kMaxGrid = 0x7FFFFFFF;    // workgroups per launch
+constexpr int64_t kMaxT = 1 << 22;          // tokens or sequences per call
+constexpr int64_t kMaxRows = 1 << 30;       // rows read back per call
+constexpr int64_t kMaxParts = 1 << 27;      // query heads times parts per decode call
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
@@ -191,7 +192,8 @@ beam_status beam_moe_kv_read(const beam_moe_attn_cfg* cfg, int32_t B, int32_t N,
                              const int32_t* first, void* k_out, void* v_out, beam_dtype dtype, void* stream) {
     beam_status st = check_attn_cfg(cfg);
     if (st != BEAM_OK) return st;
-    if (B < 0 || B > kMaxT || N < 0 || max_pages < 0 || !act_dtype(dtype)) return BEAM_ERR_INVALID_ARG;
+    if (B < 0 || B > kMaxT || N < 0 || N > kMaxRows || max_pages < 0 || !act_dtype(dtype))
+        return BEAM_ERR_INVALID_ARG;
     if (B == 0 || N == 0) return BEAM_OK;
     if (!row_offsets || !aligned4(row_offsets) || !aligned4(first) || !k_out || !v_out || !aligned16(k_out) ||
         !aligned16(v_out))
@@ -241,7 +243,7 @@ beam_status beam_moe_attn_decode(const beam_moe_attn_cfg* cfg, int32_t B, const 
     const size_t es = dtype == BEAM_BF16 ? 2 : 4;
     if (overlap(out, (size_t)B * qw * es, q, span_bytes(B, q_stride, qw, es))) return BEAM_ERR_INVALID_ARG;
     beam::attn_decode_split(B, cfg->n_kv_heads, max_len, cfg->window, &a.S, &a.cshift);
-    if ((int64_t)B * a.S * cfg->n_heads > kMaxGrid / 16) return BEAM_ERR_UNSUPPORTED;
+    if ((int64_t)B * a.S * cfg->n_heads > kMaxParts) return BEAM_ERR_UNSUPPORTED;
     const size_t need = beam::attn_decode_ws_bytes(B, cfg->n_heads, cfg->n_kv_heads, cfg->head_dim, max_len,
                                                    cfg->window);
     if (need > 0 && (!ws || ws_bytes < need || !aligned16(ws))) return BEAM_ERR_WORKSPACE;

@@ -484,8 +484,8 @@ beam_status beam_moe_kv_write(const beam_moe_attn_cfg* cfg, int32_t T, const voi
  *   row_offsets [B+1] int32, ascending from 0;  first [B] int32, nullable (0)
  *   k_out, v_out [N, n_kv_heads, D] out, dtype BF16 or F32, dense.  Rows at
  *               and behind row_offsets[B] are left as they were.
- * A token whose page is outside [0, n_pages) or outside the table reads as
- * zeros; nothing outside the cache or the table is accessed.
+ * At most 2^22 sequences and 2^30 rows.  A token whose page is outside
+ * [0, n_pages) or outside the table reads as zeros; nothing outside the cache or the table is accessed.
  */
 beam_status beam_moe_kv_read(const beam_moe_attn_cfg* cfg, int32_t B, int32_t N,
                              const beam_moe_kv_cache* cache, const int32_t* page_table, int32_t max_pages,
@@ -513,6 +513,7 @@ beam_status beam_moe_kv_read(const beam_moe_attn_cfg* cfg, int32_t B, int32_t N,
  *          [0, n_pages) are skipped.
  *   max_len  the longest length to expect, 0 .. 2^30: it sizes the split
  *          over the cache's length.  Results hold for longer ones too, more slowly.
+ *          At most 2^27 query heads times parts (BEAM_ERR_UNSUPPORTED).
  *   ws     beam_moe_attn_workspace_bytes(cfg, B, max_len) bytes, 16-byte
  *          aligned (may be null where that is 0); its contents need no
  *          initialisation, and calls that overlap in time must not share it.

@@ -130,7 +130,7 @@ def test_write_arguments(L, bad):
     assert write(L, **bad) == 1
 
 
-@pytest.mark.parametrize("bad", [dict(B=-1), dict(N=-1), dict(mp=-1), dict(dt=2), dict(tab=None), dict(off=None),
+@pytest.mark.parametrize("bad", [dict(B=-1), dict(N=-1), dict(N=(1 << 30) + 1), dict(mp=-1), dict(dt=2), dict(tab=None), dict(off=None),
                                  dict(off=A + 2), dict(first=A + 1), dict(ko=None), dict(vo=None), dict(ko=A * 3 + 4),
                                  dict(vo=A * 3), dict(vo=A * 3 + 2048)])
 def test_read_arguments(L, bad):
@@ -152,6 +152,10 @@ def test_decode_dtypes(L):
     assert decode(L, cache=kv(dt=beam.BEAM_F32), dt=1, **ws) == 2     # fp32 cache, bf16 queries
     assert decode(L, cache=kv(dt=beam.BEAM_F32), dt=0, **ws) == 3     # past the dtype check
     assert decode(L, cache=kv(dt=beam.BEAM_FP8_E4M3, ks=A, vs=A), dt=0, **ws) == 2
+
+
+def test_decode_too_many_parts(L):
+    assert decode(L, B=1 << 22, qs=6144, ml=64) == 2          # 48 * 2^22 query heads
 
 
 def test_workspace_bytes(L):
