@@ -155,7 +155,7 @@ def test_decode_dtypes(L):
 
 
 def test_decode_too_many_parts(L):
-    assert decode(L, B=1 << 22, qs=6144, ml=64) == 2          # 48 * 2^22 query heads
+    assert decode(L, B=1 << 22, qs=6144, ml=64, out=A * 100) == 2          # 48 * 2^22 query heads
 
 
 def test_workspace_bytes(L):
