@@ -26,35 +26,39 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 // Tokens per wave step, by cache element.
 template <int KIND> constexpr int tile_tokens() { return KIND == A_F32 ? 16 : 32; }
 
-// Parts of a sequence: kMinPart to kMaxPart tokens (a power of two), no more
-// of them than kWantWG workgroups need while kMaxPart allows.  Two workgroups
-// per CU keep the memory busy, and a sequence in one part needs no join (64
+// Parts of a sequence, chosen on the device from its own length: 2^kMinShift
+// to 2^kMaxShift tokens each, and no more than `want` of them while that
+// allows; `want` is what gives kWantWG workgroups in all.  Two workgroups per
+// CU keep the memory busy, and a sequence in one part needs no join (64
 // sequences, window 512, e4m3: 13.8 us in one part, 24.2 in two); parts are
 // bounded so that a batch of very different lengths still spreads over the
-// chip (1 .. 32768 tokens: 285 us at 2048, 289 at 1024, 302 at 512), until the
-// sequences alone are enough for that (kMostWG, which also bounds the workspace).
-constexpr int kWantWG = 512, kMostWG = 16384, kMinPart = 256, kMaxPart = 2048;
-void attn_decode_split(int B, int Hkv, int max_len, int window, int* S, int* cshift) {
+// chip (1 .. 32768 tokens: 285 us at 2048, 289 at 1024, 302 at 512) until the
+// sequences alone do that (kMostWG, which also bounds the workspace).  S, the
+// most parts a sequence of max_len tokens can have, sizes grid and workspace.
+constexpr int kWantWG = 512, kMostWG = 16384, kMinShift = 8, kMaxShift = 11;
+void attn_decode_split(int B, int Hkv, int max_len, int window, int* S, int* want) {
     // a window's tokens begin inside a 16-token block
     const int64_t span = window > 0 && window < max_len ? (int64_t)window + 15 : max_len;
     const int64_t heads = (int64_t)B * Hkv;
-    int sh = 0;
-    while ((1 << sh) < kMinPart) ++sh;
-    const auto parts = [&] { return span <= (int64_t)1 << sh ? 1 : (span + ((int64_t)1 << sh) - 1) >> sh; };
-    while (parts() > 1 && heads * parts() > ((1 << sh) < kMaxPart ? kWantWG : kMostWG)) ++sh;
-    *S = (int)parts();
-    *cshift = sh;
+    const auto at_least_1 = [](int64_t v) { return v < 1 ? 1 : v; };
+    const auto parts = [&](int shift) { return at_least_1((span + (1 << shift) - 1) >> shift); };
+    const int64_t w = at_least_1(kWantWG / heads);
+    const int64_t most = w > parts(kMaxShift) ? w : parts(kMaxShift);
+    int64_t s = parts(kMinShift) < most ? parts(kMinShift) : most;
+    if (s > at_least_1(kMostWG / heads)) s = at_least_1(kMostWG / heads);
+    *S = (int)s;
+    *want = (int)w;
 }
 
 size_t attn_decode_ws_bytes(int B, int Hq, int Hkv, int D, int max_len, int window) {
-    int S, C;
-    attn_decode_split(B, Hkv, max_len, window, &S, &C);
+    int S, want;
+    attn_decode_split(B, Hkv, max_len, window, &S, &want);
     return S > 1 ? (size_t)B * S * Hq * (D + 2) * sizeof(float) : 0;
 }
 
 // The tokens that a sequence's query sees, [start, len), cut into n parts of
-// 2^shift tokens from `base` on.  Parts double until S of them cover a
-// sequence that is longer than expected.
+// 2^shift tokens from `base` on.  Parts double further until S of them cover
+// a sequence that is longer than expected.
 struct Span {
     int start, len, base, shift, n;
 };
@@ -65,7 +69,8 @@ BEAM_DEV Span span_of(const AttnDecodeArgs& a, int b) {
     p.start = a.window > 0 ? max(0, p.len - a.window) : 0;
     p.base = p.start & ~15;
     const uint32_t all = (uint32_t)(p.len - p.base);
-    p.shift = a.cshift;
+    p.shift = kMinShift;
+    while (p.shift < kMaxShift && (uint64_t)a.want << p.shift < all) ++p.shift;
     while (((uint64_t)a.S << p.shift) < all) ++p.shift;
     p.n = (int)((all + (1u << p.shift) - 1) >> p.shift);
     return p;

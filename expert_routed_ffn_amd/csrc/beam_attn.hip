@@ -242,7 +242,7 @@ beam_status beam_moe_attn_decode(const beam_moe_attn_cfg* cfg, int32_t B, const 
     if ((a.c.kind == beam::A_F32) != (dtype == BEAM_F32)) return BEAM_ERR_UNSUPPORTED;
     const size_t es = dtype == BEAM_BF16 ? 2 : 4;
     if (overlap(out, (size_t)B * qw * es, q, span_bytes(B, q_stride, qw, es))) return BEAM_ERR_INVALID_ARG;
-    beam::attn_decode_split(B, cfg->n_kv_heads, max_len, cfg->window, &a.S, &a.cshift);
+    beam::attn_decode_split(B, cfg->n_kv_heads, max_len, cfg->window, &a.S, &a.want);
     if ((int64_t)B * a.S * cfg->n_heads > kMaxParts) return BEAM_ERR_UNSUPPORTED;
     const size_t need = beam::attn_decode_ws_bytes(B, cfg->n_heads, cfg->n_kv_heads, cfg->head_dim, max_len,
                                                    cfg->window);

@@ -511,8 +511,10 @@ beam_status beam_moe_kv_read(const beam_moe_attn_cfg* cfg, int32_t B, int32_t N,
  *          max_pages * page_size (or 2^30).  A row with no token (or whose scores are all
  *          -inf) gets out = 0 and lse = -inf.  Tokens on a page outside
  *          [0, n_pages) are skipped.
- *   max_len  the longest length to expect, 0 .. 2^30: it sizes the split
- *          over the cache's length.  Results hold for longer ones too, more slowly.
+ *   max_len  the longest length to expect, 0 .. 2^30: it sizes the grid and
+ *          the workspace.  Results hold for longer ones too, more slowly; too
+ *          large a value costs little, since a sequence is split by its own
+ *          length.
  *          At most 2^27 query heads times parts (BEAM_ERR_UNSUPPORTED).
  *   ws     beam_moe_attn_workspace_bytes(cfg, B, max_len) bytes, 16-byte
  *          aligned (may be null where that is 0); its contents need no
