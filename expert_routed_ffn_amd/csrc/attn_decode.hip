@@ -30,12 +30,16 @@ template <int KIND> constexpr int tile_tokens() { return KIND == A_F32 ? 16 : 32
 // to 2^kMaxShift tokens each, and no more than `want` of them while that
 // allows; `want` is what gives kWantWG workgroups in all.  Two workgroups per
 // CU keep the memory busy, and a sequence in one part needs no join (64
-// sequences, window 512, e4m3: 13.8 us in one part, 24.2 in two); parts are
+// sequences, window 512, e4m3: 13.5 us in one part, 19.3 in two).  Parts are
 // bounded so that a batch of very different lengths still spreads over the
-// chip (1 .. 32768 tokens: 285 us at 2048, 289 at 1024, 302 at 512) until the
-// sequences alone do that (kMostWG, which also bounds the workspace).  S, the
-// most parts a sequence of max_len tokens can have, sizes grid and workspace.
-constexpr int kWantWG = 512, kMostWG = 16384, kMinShift = 8, kMaxShift = 11;
+// chip (1 .. 32768 tokens, e4m3: 302, 292, 288 and 304 us for parts of up to
+// 1024, 2048, 4096 and 8192 tokens) until the sequences alone do that.  S, the
+// most parts a sequence of max_len tokens can have, sizes grid and workspace;
+// parts are numbered outermost, so that those which a short sequence lacks
+// come last and only end (64 sequences of 2048 tokens, e4m3: 43.6 us where
+// 2048 are expected, 48 where 131072 are; 120 us numbered innermost with
+// kMostWG = 16384).
+constexpr int kWantWG = 512, kMostWG = 4096, kMinShift = 8, kMaxShift = 12;
 void attn_decode_split(int B, int Hkv, int max_len, int window, int* S, int* want) {
     // a window's tokens begin inside a 16-token block
     const int64_t span = window > 0 && window < max_len ? (int64_t)window + 15 : max_len;
@@ -187,8 +191,8 @@ __global__ __launch_bounds__(256) void beam_attn_decode(AttnDecodeArgs a, int qg
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int r = lane & 15, g = lane >> 4;
     const int h = work % a.Hkv, bs = work / a.Hkv;
-    const int s = bs % a.S, b = bs / a.S;
-    if (b >= a.B) return;
+    const int b = bs % a.B, s = bs / a.B;
+    if (s >= a.S) return;
     const int G = a.Hq / a.Hkv;
     const Span sp = span_of(a, b);
     if (s > 0 && s >= sp.n) return;               // no tokens; part 0 of an empty row goes on
