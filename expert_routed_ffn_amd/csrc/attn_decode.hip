@@ -182,18 +182,20 @@ __global__ __launch_bounds__(256) void beam_attn_decode(AttnDecodeArgs a, int qg
     __shared__ float sO[4][16][D + 4];
     __shared__ float sM[4][16], sL[4][16];
 
-    // Workgroups of one (sequence, part, head) differ in their query rows
-    // only: they follow each other on one XCD, so that its L2 serves the
-    // keys and values of all but the first.
-    const int x = blockIdx.x;
-    const int work = (x >> 3) / qgroups * 8 + (x & 7), qg = (x >> 3) % qgroups;
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int r = lane & 15, g = lane >> 4;
-    const int h = work % a.Hkv, bs = work / a.Hkv;
-    const int b = bs % a.B, s = bs / a.B;
-    if (s >= a.S) return;
-    const int G = a.Hq / a.Hkv;
+    // Grid: (sequence, head) along x, parts along y.  Workgroups that differ in
+    // their query rows only follow each other on one XCD, so that its L2
+    // serves the keys and values of all but the first.
+    int bh = blockIdx.x, qg = 0;
+    if (qgroups > 1) {
+        const int j = bh >> 3;
+        qg = j % qgroups;
+        bh = j / qgroups * 8 + (bh & 7);
+    }
+    const int b = bh / a.Hkv, h = bh - b * a.Hkv, s = blockIdx.y, G = a.G;
+    if (b >= a.B) return;
     const Span sp = span_of(a, b);
     if (s > 0 && s >= sp.n) return;               // no tokens; part 0 of an empty row goes on
     const int t0 = sp.base + (int)((uint32_t)s << sp.shift);
@@ -580,10 +582,10 @@ __global__ __launch_bounds__(256) void beam_attn_join(AttnDecodeArgs a) {
 
 template <int KIND, int D, int QT>
 static hipError_t launch_decode(const AttnDecodeArgs& a, hipStream_t st) {
-    const int qgroups = (a.Hq / a.Hkv + 16 * QT - 1) / (16 * QT);
-    const size_t work = (size_t)a.B * a.S * a.Hkv;
-    const unsigned grid = (unsigned)((work + 7) / 8 * 8 * qgroups);
-    hipLaunchKernelGGL((beam_attn_decode<KIND, D, QT>), dim3(grid), dim3(256), 0, st, a, qgroups);
+    const int qgroups = (a.G + 16 * QT - 1) / (16 * QT);
+    const size_t bh = (size_t)a.B * a.Hkv;
+    const unsigned grid = (unsigned)(qgroups == 1 ? bh : (bh + 7) / 8 * 8 * qgroups);
+    hipLaunchKernelGGL((beam_attn_decode<KIND, D, QT>), dim3(grid, a.S), dim3(256), 0, st, a, qgroups);
     hipError_t err = hipGetLastError();
     if (err != hipSuccess || a.S == 1) return err;
     hipLaunchKernelGGL((beam_attn_join<KIND, D>), dim3((unsigned)((size_t)a.B * a.Hq)), dim3(256), 0, st, a);
@@ -594,7 +596,7 @@ static hipError_t launch_decode(const AttnDecodeArgs& a, hipStream_t st) {
 // is read half as often; at D = 256 their sums would not fit the registers.
 template <int KIND>
 static hipError_t launch_decode_d(const AttnDecodeArgs& a, hipStream_t st) {
-    const bool wide = a.Hq / a.Hkv > 16;
+    const bool wide = a.G > 16;
     if (a.D == 64) return wide ? launch_decode<KIND, 64, 2>(a, st) : launch_decode<KIND, 64, 1>(a, st);
     if (a.D == 128) return wide ? launch_decode<KIND, 128, 2>(a, st) : launch_decode<KIND, 128, 1>(a, st);
     return launch_decode<KIND, 256, 1>(a, st);

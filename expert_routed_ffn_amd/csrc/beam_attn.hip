@@ -250,6 +250,7 @@ beam_status beam_moe_attn_decode(const beam_moe_attn_cfg* cfg, int32_t B, const 
     a.B = B;
     a.Hq = cfg->n_heads;
     a.Hkv = cfg->n_kv_heads;
+    a.G = a.Hq / a.Hkv;
     a.D = cfg->head_dim;
     a.max_pages = max_pages;
     a.window = cfg->window;

@@ -158,7 +158,7 @@ struct KvReadArgs {
 hipError_t launch_kv_read(const KvReadArgs& a, hipStream_t st);
 
 struct AttnDecodeArgs {
-    int B, Hq, Hkv, D, max_pages, window;
+    int B, Hq, Hkv, G, D, max_pages, window;   // G = Hq / Hkv
     int S, want;            // most parts a sequence can have, parts wanted (attn_decode_split)
     float scale;
     const void* q;
