@@ -126,6 +126,11 @@ ROPE = [
     ("bf16", 7, 3, 1, 64, 48, False, 0.0, False, 8),
     ("bf16", 4, 7, 7, 256, 16, True, 0.0, True, 0),
     ("f32", 130, 3, 1, 128, 64, False, 0.0, False, 0),
+    ("bf16", 6, 2, 2, 256, 128, False, 0.0, True, 0),
+    ("bf16", 6, 5, 1, 128, 96, False, 0.0, True, 0),
+    ("f32", 4, 4, 2, 64, 64, False, 0.0, True, 0),
+    ("bf16", 3, 2, 1, 256, 256, True, 0.0, True, 8),
+    ("bf16", 2, 256, 4, 64, 32, False, 0.0, True, 0),
 ]
 
 
@@ -143,6 +148,57 @@ def test_qk_norm_rope(act, T, hq, hkv, D, R, inter, ssmax, norm, gap):
     check_rows("q", qo[:T], rope_ref(cfg, q, gq, pos, f, True), HALF[ACT[act]])
     check_rows("k", ko[:T], rope_ref(cfg, k, gk, pos, f, False), HALF[ACT[act]])
     assert (qo[T] == 5).all() and (ko[T] == 5).all()       # rows behind the last stay
+
+
+def rope_torch(cfg, x, gamma, pos, f, is_q):
+    """The formula over many tokens at once, in fp64 torch."""
+    x = x.double()
+    x = x / (x.square().mean(-1, keepdim=True) + cfg.rms_eps).sqrt() * gamma.double()
+    if cfg.rope_dim:
+        a = pos.double()[:, None, None] * f.double()
+        half, y = cfg.rope_dim // 2, x.clone()
+        iu, iw = (slice(0, cfg.rope_dim, 2), slice(1, cfg.rope_dim, 2)) if cfg.rope_interleaved else (
+            slice(0, half), slice(half, cfg.rope_dim))
+        y[..., iu] = x[..., iu] * a.cos() - x[..., iw] * a.sin()
+        y[..., iw] = x[..., iw] * a.cos() + x[..., iu] * a.sin()
+        x = y
+    if is_q and cfg.ssmax_len:
+        x = x * ((1 + pos.double().clamp(min=0) / cfg.ssmax_len) ** cfg.ssmax_exp)[:, None, None]
+    return x
+
+
+# many tokens: a wave then takes several groups of a token's heads, here 2, 3
+# (of 16, so the last wave of a token has one), 2 with one group of queries,
+# keys and values together, and all 4
+@pytest.mark.parametrize("act,kind,T,hq,hkv,D,R,inter,ssmax", [
+    ("bf16", "bf16", 5000, 48, 8, 128, 128, False, 0.0), ("bf16", "fp8", 7001, 48, 8, 128, 128, False, 0.0),
+    ("f32", "f32", 33000, 9, 3, 64, 32, True, 0.0), ("bf16", "fp8", 40000, 4, 2, 256, 0, False, 2048.0),
+])
+def test_qk_norm_rope_many_tokens(act, kind, T, hq, hkv, D, R, inter, ssmax):
+    say(f"many tokens {act} -> {kind} T={T} {hq}/{hkv} D={D}")
+    cfg = beam.AttnCfg(hq, hkv, D, R, inter, 0, 64, ssmax)
+    q, k, v, pos, gq, gk, f = rope_inputs(cfg, T, act, T)
+    n_pages = T // 64 + 2
+    slots = torch.randperm(n_pages * 64, generator=gen(1), device=DEV)[:T].to(torch.int32)
+    c = beam.kv_cache(cfg, n_pages, KIND[kind], DEV)
+    qo, q2 = (torch.empty((T, hq, D), dtype=ACT[act], device=DEV) for _ in range(2))
+    ko = torch.empty((T, hkv, D), dtype=ACT[act], device=DEV)
+    beam.beam_moe_qk_norm_rope(cfg, q, k, pos, qo, ko, f, gq, gk)
+    beam.beam_moe_qk_norm_rope_cache(cfg, q, k, v, pos, slots, q2, c, f, gq, gk)
+    torch.cuda.synchronize()
+    assert torch.equal(qo, q2)
+    half = HALF[ACT[act]]
+    rq, rk = rope_torch(cfg, q, gq, pos, f, True), rope_torch(cfg, k, gk, pos, f, False)
+    for got, ref in ((qo, rq), (ko, rk)):
+        top = ref.abs().amax(-1, keepdim=True)
+        assert ((got.double() - ref).abs() <= half * ref.abs() + 2.0 ** -18 * top).all()
+    at = (slots // 64).long(), slice(None), (slots % 64).long()
+    for side, scale, ref in ((c.k, c.k_scale, rk), (c.v, c.v_scale, v.double())):
+        got = side[at].double() if kind != "fp8" else side.view(torch.uint8)[at].view(
+            torch.float8_e4m3fn).double() * scale[at].double()[..., None]
+        top = ref.abs().amax(-1, keepdim=True)
+        step = 2.0 ** -4 * ref.abs() + 2.0 ** -10 * top / 448 if kind == "fp8" else HALF[ACT[kind]] * ref.abs()
+        assert ((got - ref).abs() <= step + 2.0 ** -17 * top).all()
 
 
 def test_qk_norm_rope_in_place():
@@ -294,6 +350,66 @@ def test_kv_write_then_read(act, kind, T, hkv, D, P):
             assert (got[len(rows):] == 7).all()
 
 
+def test_codes_as_bytes():
+    """A cache of uint8 codes is the same cache as one of float8_e4m3fn."""
+    cfg = beam.AttnCfg(4, 2, 64, 0, False, 0, 16)
+    c, _ = filled(cfg, 4, "fp8", 3)
+    b = beam.KVCache(c.k.view(torch.uint8), c.v.view(torch.uint8), c.k_scale, c.v_scale)
+    t = torch.tensor([[2, 0, 3]], dtype=torch.int32, device=DEV)
+    q = torch.randn((1, 4, 64), generator=gen(1), device=DEV).bfloat16()
+    outs = []
+    for x in (c, b):
+        o = torch.empty_like(q)
+        beam.beam_moe_attn_decode(cfg, q, x, t, torch.tensor([40], dtype=torch.int32, device=DEV), 40, o, None)
+        outs.append(o)
+    torch.cuda.synchronize()
+    assert torch.equal(*outs)
+
+
+def test_every_code_is_exact():
+    """All 256 e4m3 codes through both readers: the row of one seen token is
+    the decode's result (its probability is 1), NaN codes included."""
+    cfg = beam.AttnCfg(2, 2, 128, 0, False, 0, 16)
+    c = beam.kv_cache(cfg, 1, beam.BEAM_FP8_E4M3, DEV)
+    c.k.view(torch.uint8).zero_()
+    codes = torch.arange(256, device=DEV, dtype=torch.int32).to(torch.uint8).view(2, 128)
+    c.v.view(torch.uint8)[0, :, 0] = codes
+    c.k_scale.fill_(1.0)
+    c.v_scale.fill_(1.0)
+    t = torch.zeros((1, 1), dtype=torch.int32, device=DEV)
+    one = torch.ones(1, dtype=torch.int32, device=DEV)
+    q = torch.zeros((1, 2, 128), dtype=torch.bfloat16, device=DEV)
+    out = torch.empty_like(q)
+    beam.beam_moe_attn_decode(cfg, q, c, t, one, 1, out, None)
+    ko, vo = (torch.empty((1, 2, 128), device=DEV) for _ in range(2))
+    beam.beam_moe_kv_read(cfg, c, t, torch.tensor([0, 1], dtype=torch.int32, device=DEV), ko, vo)
+    torch.cuda.synchronize()
+    want = oracle.e4m3_decode(codes.cpu().numpy())
+    for got in (out, vo):
+        assert np.array_equal(f64(got)[0], want, equal_nan=True)
+
+
+def test_kv_read_empty_sequences_between():
+    """Sequences without rows at the front, in the middle and at the end, and
+    many sequences."""
+    cfg = beam.AttnCfg(3, 3, 64, 0, False, 0, 16)
+    B = 700
+    g = np.random.default_rng(1)
+    n = g.integers(0, 4, B) * g.integers(0, 12, B)
+    n[0], n[-1] = 0, 0
+    c, (k, v) = filled(cfg, 50, "bf16", 2)
+    table = g.integers(0, 50, (B, 3)).astype(np.int32)
+    off = np.concatenate([[0], np.cumsum(n)]).astype(np.int32)
+    N = int(off[-1])
+    ko, vo = (torch.empty((N, 3, 64), device=DEV) for _ in range(2))
+    beam.beam_moe_kv_read(cfg, c, torch.tensor(table, device=DEV), torch.tensor(off, device=DEV), ko, vo)
+    torch.cuda.synchronize()
+    b = np.repeat(np.arange(B), n)
+    t = np.arange(N) - off[b]
+    for got, ref in ((ko, k), (vo, v)):
+        assert np.array_equal(f64(got), ref[table[b, t // 16], :, t % 16])
+
+
 def test_kv_read_outside_the_cache():
     """Bad pages, tokens before the first and behind the table read as zeros."""
     cfg = beam.AttnCfg(2, 2, 64, 0, False, 0, 16)
@@ -358,7 +474,7 @@ def check_decode(cfg, q, c, vals, table, lens, max_len, name, n_pages=None, stre
     B = len(lens)
     dt = torch.tensor(table, device=DEV)
     dl = torch.tensor(lens, dtype=torch.int32, device=DEV)
-    out = torch.full(q.shape, 9.0, dtype=q.dtype, device=DEV)
+    out = torch.full(q.shape, 9.0, dtype=q.dtype, device=DEV)     # dense, whatever q's rows are
     lse = torch.full((B, cfg.n_heads), 9.0, device=DEV)
     ws = beam.attn_workspace(cfg, B, max_len)
     ws.view(torch.uint8).fill_(0xFF)                       # its contents do not matter
@@ -460,6 +576,20 @@ def test_decode_parts(kind, B, lens, max_len, window):
     q = torch.randn((B, 6, 128), generator=gen(6), device=DEV) * 3
     check_decode(cfg, q.to(ACT["f32" if kind == "f32" else "bf16"]), c, vals, tables(lens, P, n_pages, 2), lens,
                  max_len, "parts")
+
+
+def test_decode_many_sequences_strided_queries():
+    """Thousands of short sequences sharing pages, the largest page size, and
+    queries that are columns of a wider matrix."""
+    B, P, n_pages = 3000, 1024, 5
+    cfg = beam.AttnCfg(6, 3, 64, 0, False, 0, P, softmax_scale=0.125)
+    c, vals = filled(cfg, n_pages, "fp8", 4)
+    g = np.random.default_rng(3)
+    lens = g.integers(0, 40, B).tolist()
+    table = g.integers(0, n_pages, (B, 1)).astype(np.int32)
+    wide = torch.randn((B, 12 * 64), generator=gen(5), device=DEV).bfloat16()
+    q = wide[:, 64:7 * 64].unflatten(1, (6, 64))
+    check_decode(cfg, q, c, vals, table, lens, 40, "many sequences")
 
 
 @pytest.mark.parametrize("kind", ["bf16", "fp8", "f32"])
