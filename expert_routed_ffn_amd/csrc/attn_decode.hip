@@ -166,8 +166,10 @@ template <int D, int QT> struct Acc {
     f32x4 o[QT][D / 16];
 };
 
+// With 32 queries a wave the registers are held to two waves per SIMD (64
+// queries on one head, e4m3: 61 -> 52 us); else what the compiler takes is best.
 template <int KIND, int D, int QT>
-__global__ __launch_bounds__(256) void beam_attn_decode(AttnDecodeArgs a, int qgroups) {
+__global__ __launch_bounds__(256, KIND != A_F32 && QT == 2 ? 2 : 1) void beam_attn_decode(AttnDecodeArgs a, int qgroups) {
     constexpr int TILE = tile_tokens<KIND>(), NU = TILE / 16;   // 16-token blocks per step
     constexpr int STEP = 4 * TILE;                              // tokens per workgroup step
     constexpr int ES = KIND == A_F32 ? 4 : (KIND == A_BF16 ? 2 : 1);   // bytes per cache element
@@ -175,7 +177,7 @@ __global__ __launch_bounds__(256) void beam_attn_decode(AttnDecodeArgs a, int qg
     constexpr int NK = KIND == A_F32 ? D / 16 : D / 32;         // key fragments per token
     constexpr int KW = KIND == A_FP8 ? 2 : 4;                   // words per key fragment
     constexpr int NC = NK * KW / 4;                             // 16-byte key pieces per lane and token
-    constexpr int NT = KIND != A_FP8 ? 1 : (NC < 4 ? NC : 4);   // pieces exchanged among NT lanes
+    constexpr int NT = KIND == A_F32 || (KIND == A_BF16 && QT == 1) ? 1 : (NC < 4 ? NC : 4);   // pieces exchanged among NT lanes
     constexpr int PF = 4 / KW;                                  // fragments per piece
     constexpr int KE = 4 * KW / ES;                             // elements per key fragment
     constexpr int VW = DL * ES / 4;                             // words per lane and value row
@@ -212,8 +214,9 @@ __global__ __launch_bounds__(256) void beam_attn_decode(AttnDecodeArgs a, int qg
         const size_t qoff = (size_t)b * a.qs + (size_t)(h * G + min(qrow, G - 1)) * D;
 #pragma unroll
         for (int c = 0; c < NK; ++c) {
-            if constexpr (KIND == A_F32) ldw<4>(static_cast<const float*>(a.q) + qoff + KE * (4 * c + g), qf[j][c]);
-            else ldw<4>(static_cast<const uint16_t*>(a.q) + qoff + KE * (NT > 1 ? NK * g + c : (c / PF * 4 + g) * PF + c % PF), qf[j][c]);
+            const int e = KE * (NT > 1 ? NK * g + c : (c / PF * 4 + g) * PF + c % PF);
+            if constexpr (KIND == A_F32) ldw<4>(static_cast<const float*>(a.q) + qoff + e, qf[j][c]);
+            else ldw<4>(static_cast<const uint16_t*>(a.q) + qoff + e, qf[j][c]);
         }
     }
 
@@ -260,11 +263,15 @@ __global__ __launch_bounds__(256) void beam_attn_decode(AttnDecodeArgs a, int qg
         float4 ks[NU], vs[NU];
 #pragma unroll
         for (int u = 0; u < NU; ++u) {
-            // bf16, fp32: the four lanes of a row read 64 bytes of it at a time.
-            // e4m3: NT neighbouring lanes read one row's pieces side by side,
-            // the lowest lane's row, then the next one's, and exchange them
-            // below: the cache unit takes four lanes at a time, in pieces that
-            // adjoin, and at one byte an element those accesses bound the kernel
+            // The cache unit takes four lanes at a time, in pieces that adjoin.
+            // NT = 1: the lanes of a row are 16 apart, and each reads 16 bytes
+            // of its row on its own.  NT > 1: neighbouring lanes read one row's
+            // pieces side by side, the lowest lane's row, then the next one's,
+            // and exchange them below.  That pays where those accesses bound
+            // the kernel: at one byte an element (64 sequences of 8192: 234 ->
+            // 217 us) and where several workgroups read the same keys (64
+            // queries on one head, bf16: 68 -> 63 us); elsewhere HBM bounds it
+            // and the exchange costs a percent.
             const uint8_t* kr = kc + (row[u] + (r & ~(NT - 1))) * (D * ES) +
                                 (NT > 1 ? g * (D * ES / 4) + (r & (NT - 1)) * 16 : g * 16);
 #pragma unroll
