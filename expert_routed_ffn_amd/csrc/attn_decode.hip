@@ -12,10 +12,18 @@
 // (r, g) reads the same tokens' value elements r * D/16 .. + D/16 - 1 as whole
 // row pieces; output block t then holds rows d = r * D/16 + t.
 //
-// The cache's length is split over workgroups (S parts per sequence) and over
-// the four waves of a workgroup (32-token tiles in turn).  The waves' results
-// are joined through LDS, the parts' through the workspace by a second
-// kernel.
+// The cache's length is split over workgroups (parts) and over the four waves
+// of a workgroup (tiles in turn).  The waves' results are joined through LDS,
+// the parts' through the workspace by a second kernel.
+//
+// HBM bounds it: 4 flops per byte and query head are far below what the matrix
+// cores give, and the padding of G to 16 columns with them.  64 sequences of
+// 8192 tokens, 48 heads over 8 of 128: bf16 340 us, 6.3 TB/s; e4m3 189 us,
+// 5.9 TB/s; fp32 695 us, 6.2 TB/s; one sequence of 131071: 91 us, 5.9 TB/s (a
+// read-only stream on this card reaches 6.3 with plain loads, 7.0 with
+// non-temporal ones; a copy 4.7).  Small calls are latency: 8 sequences of up
+// to 2048 tokens take 9 us for a chain of length, page, keys, join, store, and
+// 3 us to join their parts.
 #include "common.h"
 #include "kernels.h"
 
@@ -169,7 +177,8 @@ template <int D, int QT> struct Acc {
 // With 32 queries a wave the registers are held to two waves per SIMD (64
 // queries on one head, e4m3: 61 -> 52 us); else what the compiler takes is best.
 template <int KIND, int D, int QT>
-__global__ __launch_bounds__(256, KIND != A_F32 && QT == 2 ? 2 : 1) void beam_attn_decode(AttnDecodeArgs a, int qgroups) {
+__global__ __launch_bounds__(256, KIND != A_F32 && QT == 2 ? 2 : 1) void beam_attn_decode(AttnDecodeArgs a,
+                                                                                         int qgroups) {
     constexpr int TILE = tile_tokens<KIND>(), NU = TILE / 16;   // 16-token blocks per step
     constexpr int STEP = 4 * TILE;                              // tokens per workgroup step
     constexpr int ES = KIND == A_F32 ? 4 : (KIND == A_BF16 ? 2 : 1);   // bytes per cache element
@@ -177,7 +186,8 @@ __global__ __launch_bounds__(256, KIND != A_F32 && QT == 2 ? 2 : 1) void beam_at
     constexpr int NK = KIND == A_F32 ? D / 16 : D / 32;         // key fragments per token
     constexpr int KW = KIND == A_FP8 ? 2 : 4;                   // words per key fragment
     constexpr int NC = NK * KW / 4;                             // 16-byte key pieces per lane and token
-    constexpr int NT = KIND == A_F32 || (KIND == A_BF16 && QT == 1) ? 1 : (NC < 4 ? NC : 4);   // pieces exchanged among NT lanes
+    // pieces exchanged among NT lanes (see the key loads)
+    constexpr int NT = KIND == A_F32 || (KIND == A_BF16 && QT == 1) ? 1 : (NC < 4 ? NC : 4);
     constexpr int PF = 4 / KW;                                  // fragments per piece
     constexpr int KE = 4 * KW / ES;                             // elements per key fragment
     constexpr int VW = DL * ES / 4;                             // words per lane and value row

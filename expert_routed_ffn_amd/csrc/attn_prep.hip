@@ -128,6 +128,11 @@ BEAM_DEV void store_cache(void* side, float* scales, size_t row, int e0, float (
 // 512/D units of one token; the rotation's cosines and sines depend on the
 // lane's place in the head only, so they are formed once per wave, one or two
 // frequencies per lane, and handed round.
+//   For a row x: y = R(x * gamma) * f, with f = 1/sqrt(mean(x^2) + eps) times
+// the position factor: the rotation R is linear, so both factors wait until
+// after it.  Bound by HBM where there are many tokens (16384 of 48 + 8 + 8 heads
+// of 128, bf16 into e4m3: 100 us, 5.0 TB/s; values and keys alone: 24 us, 4.2
+// TB/s; a copy reaches 4.7), by latency where there are few (64: 3.8 us).
 // ---------------------------------------------------------------------------
 template <bool BF, int CK, int D>
 __global__ __launch_bounds__(256) void beam_attn_prep(AttnPrepArgs a, int units, int wpt, int gpw) {
@@ -282,8 +287,8 @@ static void launch_prep(const AttnPrepArgs& a, hipStream_t st) {
     const int groups = (units + HPW - 1) / HPW;
     // groups per wave: one while that leaves the chip with few waves, more
     // once the waves suffice, which forms a token's cosines fewer times (16384
-    // tokens of 16 groups into an 8-bit cache: 106 us at 65536 waves, 100 at
-    // 32768, 108 at 8192; 313 us with one group per wave)
+    // tokens of 16 groups into an 8-bit cache: 124 us at 131072 waves, 106 at
+    // 65536, 100 at 32768, 108 at 8192)
     const int gpw = (int)min((int64_t)groups, max((int64_t)1, (int64_t)a.T * groups / kPrepWaves));
     const int wpt = (groups + gpw - 1) / gpw;
     const unsigned grid = (unsigned)(((size_t)a.T * wpt + 3) / 4);

@@ -10,8 +10,9 @@
 namespace {
 
 constexpr int64_t kMaxT = 1 << 22;          // tokens or sequences per call
-constexpr int64_t kMaxRows = 1 << 30;       // rows read back per call
-constexpr int64_t kMaxParts = 1 << 27;      // query heads times parts per decode call
+// launches of 256-thread workgroups hold fewer than 2^32 threads
+constexpr int64_t kMaxRows = 1 << 26;       // rows read back per call, 8 per workgroup
+constexpr int64_t kMaxParts = 1 << 23;      // query heads times parts per decode call
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }

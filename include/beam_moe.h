@@ -484,8 +484,9 @@ beam_status beam_moe_kv_write(const beam_moe_attn_cfg* cfg, int32_t T, const voi
  *   row_offsets [B+1] int32, ascending from 0;  first [B] int32, nullable (0)
  *   k_out, v_out [N, n_kv_heads, D] out, dtype BF16 or F32, dense.  Rows at
  *               and behind row_offsets[B] are left as they were.
- * At most 2^22 sequences and 2^30 rows.  A token whose page is outside
- * [0, n_pages) or outside the table reads as zeros; nothing outside the cache or the table is accessed.
+ * The outputs must not overlap each other or the cache.  A token whose page
+ * is outside [0, n_pages) or outside the table reads as zeros; nothing outside
+ * the cache or the table is accessed.  At most 2^22 sequences and 2^26 rows.
  */
 beam_status beam_moe_kv_read(const beam_moe_attn_cfg* cfg, int32_t B, int32_t N,
                              const beam_moe_kv_cache* cache, const int32_t* page_table, int32_t max_pages,
@@ -501,21 +502,22 @@ beam_status beam_moe_kv_read(const beam_moe_attn_cfg* cfg, int32_t B, int32_t N,
  *   out = sum_j softmax(z)_j v_j,   lse = log sum_j exp(z_j)
  * Sums, maxima and the join of the parts are fp32; with a BF16 or FP8_E4M3
  * cache the probabilities (times the value row's scale) are rounded to bf16
- * for the matrix cores.
+ * for the matrix cores.  Values are summed before the division by the
+ * probabilities' sum: magnitudes beyond 2^96 may overflow there.
  *   q      [B, n_heads, D] dtype, rows q_stride apart; out [B, n_heads, D]
  *          dtype, dense, must not overlap q.  dtype is BF16 for a BF16 or
  *          FP8_E4M3 cache and F32 for an F32 one.
  *   lse    [B, n_heads] fp32 out, nullable (natural logarithm)
  *   page_table as in beam_moe_kv_read; seq_lens [B] int32.  A length below 0
  *          counts as 0 and one beyond the table as the table's
- *          max_pages * page_size (or 2^30).  A row with no token (or whose scores are all
- *          -inf) gets out = 0 and lse = -inf.  Tokens on a page outside
- *          [0, n_pages) are skipped.
+ *          max_pages * page_size (or 2^30).  A row with no token (or whose
+ *          scores are all -inf) gets out = 0 and lse = -inf.  Tokens on a
+ *          page outside [0, n_pages) are skipped.
  *   max_len  the longest length to expect, 0 .. 2^30: it sizes the grid and
  *          the workspace.  Results hold for longer ones too, more slowly; too
  *          large a value costs little, since a sequence is split by its own
- *          length.
- *          At most 2^27 query heads times parts (BEAM_ERR_UNSUPPORTED).
+ *          length.  At most 2^23 sequences times query heads times parts
+ *          (BEAM_ERR_UNSUPPORTED).
  *   ws     beam_moe_attn_workspace_bytes(cfg, B, max_len) bytes, 16-byte
  *          aligned (may be null where that is 0); its contents need no
  *          initialisation, and calls that overlap in time must not share it.

@@ -130,7 +130,7 @@ def test_write_arguments(L, bad):
     assert write(L, **bad) == 1
 
 
-@pytest.mark.parametrize("bad", [dict(B=-1), dict(N=-1), dict(N=(1 << 30) + 1), dict(mp=-1), dict(dt=2), dict(tab=None), dict(off=None),
+@pytest.mark.parametrize("bad", [dict(B=-1), dict(N=-1), dict(N=(1 << 26) + 1), dict(mp=-1), dict(dt=2), dict(tab=None), dict(off=None),
                                  dict(off=A + 2), dict(first=A + 1), dict(ko=None), dict(vo=None), dict(ko=A * 3 + 4),
                                  dict(vo=A * 3), dict(vo=A * 3 + 2048)])
 def test_read_arguments(L, bad):
@@ -155,7 +155,8 @@ def test_decode_dtypes(L):
 
 
 def test_decode_too_many_parts(L):
-    assert decode(L, B=1 << 22, qs=6144, ml=64, out=A * 100) == 2          # 48 * 2^22 query heads
+    assert decode(L, B=(1 << 23) // 48 + 1, ml=64, out=A * 100) == 2      # one sequence too many for 2^23 query heads
+    assert decode(L, B=1, ml=1 << 30) == 3                                 # few parts however long: on to the workspace
 
 
 def test_workspace_bytes(L):
