@@ -320,7 +320,7 @@ hipError_t launch_attn_prep(const AttnPrepArgs& a, hipStream_t st) {
 // Cache rows back to dense rows.  A workgroup takes kReadRows consecutive
 // output rows: each lane finds one row's place in the cache, then groups of
 // D/8 lanes copy one head row of one side at a time, kReadBatch of them with
-// all their loads in flight.  Bound by HBM (165000 rows of 8 heads of 128, e4m3
+// all their loads in flight.  Bound by HBM (91500 rows of 8 heads of 128, e4m3
 // to bf16: 110 us, 5.2 TB/s; one row per workgroup: 137 us; 4 rows and loads
 // at a time: 119 us).
 // ---------------------------------------------------------------------------
