@@ -1,7 +1,8 @@
-"""Builds libbeam_moe.so (HIP, gfx950) in-tree from csrc/.
+"""Builds libbeam_moe.so (HIP, gfx950) in-tree from csrc/, and _bind.so, the
+native argument marshalling of the Python package's attention calls.
 
 Every call compiles from scratch: each .hip file to an object under
-_build/, then one shared library next to this file.
+_build/, then the shared libraries next to this file.
 """
 
 from __future__ import annotations
@@ -10,6 +11,7 @@ import concurrent.futures
 import os
 import shutil
 import subprocess
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -17,6 +19,7 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(ROOT, "_build")
 LIB_PATH = os.path.join(HERE, "libbeam_moe.so")
+BIND_PATH = os.path.join(HERE, "_bind.so")
 SOURCES = ["beam_moe.hip", "route.hip", "permute.hip", "experts.hip", "combine_norm.hip", "pack.hip", "mx.hip",
            "beam_attn.hip", "attn_prep.hip", "attn_decode.hip"]
 
@@ -62,7 +65,16 @@ def build(verbose: bool = False, extra_flags=()) -> str:
     tmp = LIB_PATH + ".tmp"
     _run([cc, f"--offload-arch={ARCH}", "-shared", "-fPIC", *[j[0] for j in jobs], "-o", tmp])
     os.replace(tmp, LIB_PATH)
+    _build_bind(cc, extra_flags)
     return LIB_PATH
+
+
+def _build_bind(cc: str, extra_flags) -> None:
+    import torch   # its DLPack header; nothing of torch is linked
+    tmp = BIND_PATH + ".tmp"
+    _run([cc, *HIP_FLAGS, *extra_flags, "-I", os.path.join(os.path.dirname(torch.__file__), "include"),
+          "-I", sysconfig.get_paths()["include"], "-shared", os.path.join(CSRC, "bind.hip"), "-o", tmp])
+    os.replace(tmp, BIND_PATH)
 
 
 if __name__ == "__main__":

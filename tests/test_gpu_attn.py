@@ -823,3 +823,129 @@ def test_attention_between_two_boundaries():
     beam.moe_layer(cfg, xn, wr, bias, pgu, pd, h, one, one, 3, mb)
     torch.cuda.synchronize()
     assert torch.isfinite(mb.x_next).all()
+
+
+# ------------------------------------------------------------------ the binding
+
+def binding_state():
+    cfg = beam.AttnCfg(6, 2, 64, 32, False, 0, 16)
+    q, k, v, pos, gq, gk, f = rope_inputs(cfg, 5, "bf16", 3, 8)
+    c, _ = filled(cfg, 4, "fp8", 1)
+    slots = torch.arange(5, dtype=torch.int32, device=DEV)
+    return dict(
+        cfg=cfg, q=q, k=k, v=v, pos=pos, gq=gq, gk=gk, f=f, cache=c, slots=slots,
+        qo=torch.empty((5, 6, 64), dtype=torch.bfloat16, device=DEV),
+        ko=torch.empty((5, 2, 64), dtype=torch.bfloat16, device=DEV),
+        kr=torch.empty((7, 2, 64), dtype=torch.bfloat16, device=DEV),
+        vr=torch.empty((7, 2, 64), dtype=torch.bfloat16, device=DEV),
+        table=torch.tensor([[0, 1], [2, 3], [1, 2], [3, 0], [0, 0]], dtype=torch.int32, device=DEV),
+        off=torch.tensor([0, 3, 3, 7, 7, 7], dtype=torch.int32, device=DEV),
+        first=torch.tensor([2, 0, 20, 0, 0], dtype=torch.int32, device=DEV),
+        lens=torch.tensor([9, 32, 0, 17, 1], dtype=torch.int32, device=DEV),
+        out=torch.empty((5, 6, 64), dtype=torch.bfloat16, device=DEV), lse=torch.empty((5, 6), device=DEV),
+        ws=beam.attn_workspace(cfg, 5, 32))
+
+
+CALLS = {
+    "rope": lambda s, **kw: beam.beam_moe_qk_norm_rope(s["cfg"], s["q"], s["k"], s["pos"], s["qo"], s["ko"], s["f"],
+                                                       s["gq"], s["gk"], **kw),
+    "rope_cache": lambda s, **kw: beam.beam_moe_qk_norm_rope_cache(
+        s["cfg"], s["q"], s["k"], s["v"], s["pos"], s["slots"], s["qo"], s["cache"], s["f"], s["gq"], s["gk"], **kw),
+    "write": lambda s, **kw: beam.beam_moe_kv_write(s["cfg"], s["k"], s["v"], s["slots"], s["cache"], **kw),
+    "read": lambda s, **kw: beam.beam_moe_kv_read(s["cfg"], s["cache"], s["table"], s["off"], s["kr"], s["vr"],
+                                                  first=s["first"], **kw),
+    "decode": lambda s, **kw: beam.beam_moe_attn_decode(s["cfg"], s["qo"], s["cache"], s["table"], s["lens"], 32,
+                                                        s["out"], s["ws"], s["lse"], **kw),
+}
+RESULTS = {"rope": ("qo", "ko"), "rope_cache": ("qo",), "write": (), "read": ("kr", "vr"), "decode": ("out", "lse")}
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_native_marshalling_is_the_python_one(name, monkeypatch):
+    """A good call goes through the native marshalling, parameters that
+    require gradients and tensors without a slope in their strides too, and
+    does what the Python one does (taken with an explicit stream)."""
+    s = binding_state()
+    s["qo"].copy_(s["q"])
+    s["gq"], s["f"] = torch.nn.Parameter(s["gq"]), torch.nn.Parameter(s["f"])
+    side = [t for t in (s["cache"].k, s["cache"].v, s["cache"].k_scale, s["cache"].v_scale)]
+    start = [t.clone() for t in side]
+    CALLS[name](s, stream=torch.cuda.current_stream())
+    torch.cuda.synchronize()
+    want = [s[r].clone() for r in RESULTS[name]] + [t.clone() for t in side]
+    for t, u in zip(side, start):
+        t.copy_(u)
+    for r in RESULTS[name]:
+        s[r].zero_()
+    if name == "decode":
+        s["qo"].copy_(s["q"])
+    monkeypatch.setattr(beam, "_launch", None)             # the Python way would fail
+    CALLS[name](s)
+    torch.cuda.synchronize()
+    for a, b in zip([s[r] for r in RESULTS[name]] + side, want):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
+BAD = [
+    ("rope", "q", lambda t: t[:, :5]), ("rope", "q", lambda t: t.float()), ("rope", "q", lambda t: t.half()),
+    ("rope", "q", lambda t: t.cpu()), ("rope", "k", lambda t: t[:4]), ("rope", "k", lambda t: t.transpose(0, 1)),
+    ("rope", "pos", lambda t: t.long()), ("rope", "pos", lambda t: t.cpu()), ("rope", "pos", lambda t: t[:3]),
+    ("rope", "qo", lambda t: t.transpose(1, 2)), ("rope", "ko", lambda t: t[:, :1]), ("rope", "f", lambda t: None),
+    ("rope", "f", lambda t: t.double()), ("rope", "f", lambda t: t[:8]), ("rope", "gq", lambda t: t[:32]),
+    ("rope", "gk", lambda t: t.float()), ("rope", "qo", lambda t: t.expand(5, 6, 64)[:, ::2]),
+    ("rope_cache", "v", lambda t: t[:, :1]), ("rope_cache", "slots", lambda t: t.long()),
+    ("rope_cache", "slots", lambda t: t[::2]), ("write", "v", lambda t: t.float()), ("write", "slots", lambda t: t[1:]),
+    ("read", "table", lambda t: t.long()), ("read", "table", lambda t: t.t()), ("read", "off", lambda t: t[1:]),
+    ("read", "vr", lambda t: t[1:]), ("read", "first", lambda t: t[1:]), ("decode", "lens", lambda t: t[1:]),
+    ("decode", "table", lambda t: t[1:]), ("decode", "table", lambda t: t.cpu()), ("decode", "out", lambda t: t.float()),
+    ("decode", "lse", lambda t: t.double()), ("decode", "lse", lambda t: t[:, :3]), ("decode", "ws", lambda t: t.float()),
+]
+
+
+@pytest.mark.parametrize("i", range(len(BAD)))
+def test_bad_tensors_are_refused(i):
+    name, key, spoil = BAD[i]
+    s = binding_state()
+    kept = {r: s[r].fill_(3.0).clone() for r in RESULTS[name] if r != key}
+    s[key] = spoil(s[key])
+    with pytest.raises((ValueError, TypeError)):
+        CALLS[name](s)
+    torch.cuda.synchronize()
+    for r, t in kept.items():
+        assert torch.equal(s[r], t)
+
+
+def test_bad_cache_and_workspace_are_refused():
+    s = binding_state()
+    other = beam.kv_cache(beam.AttnCfg(6, 2, 64, 32, False, 0, 32), 4, beam.BEAM_FP8_E4M3)      # another page size
+    for name in ("rope_cache", "write", "read", "decode"):
+        with pytest.raises(ValueError):
+            CALLS[name](dict(s, cache=other))
+    f32 = beam.kv_cache(s["cfg"], 4, beam.BEAM_F32)
+    with pytest.raises(beam.BeamError) as e:
+        CALLS["decode"](dict(s, cache=f32))
+    assert e.value.status == 2                              # bf16 queries over an fp32 cache
+    c = beam.AttnCfg(6, 2, 64, 0, False, 0, 16)
+    table = torch.zeros((1, 200), dtype=torch.int32, device=DEV)
+    with pytest.raises(beam.BeamError) as e:
+        beam.beam_moe_attn_decode(c, s["qo"][:1], s["cache"], table, s["lens"][:1], 3000, s["out"][:1], s["ws"])
+    assert e.value.status == 3                              # many parts, little workspace
+
+
+def test_configurations_and_caches_copy():
+    """Copies have handles of their own."""
+    import copy
+    import pickle
+    s = binding_state()
+    CALLS["decode"](s)
+    want = s["out"].clone()
+    for cfg in (copy.copy(s["cfg"]), copy.deepcopy(s["cfg"]), pickle.loads(pickle.dumps(s["cfg"]))):
+        s["out"].zero_()
+        CALLS["decode"](dict(s, cfg=cfg))
+        torch.cuda.synchronize()
+        assert torch.equal(s["out"], want)
+    c = s["cache"]
+    again = beam.KVCache(c.k.clone(), c.v.clone(), c.k_scale.clone(), c.v_scale.clone())
+    CALLS["decode"](dict(s, cache=again))
+    torch.cuda.synchronize()
+    assert torch.equal(s["out"], want)
