@@ -172,10 +172,16 @@ __global__ __launch_bounds__(256) void beam_attn_prep(AttnPrepArgs a, int units,
         const double p = (double)a.pos[t];
         float c[2], s[2];
         auto angle = [&](int k) {
-            // whole turns drop out in fp64, so far positions keep their angle
+            // whole turns drop out in fp64, so far positions keep their angle;
+            // what fp32 then leaves of it enters to first order
             double rev = p * ((double)a.inv_freq[min(lane + 64 * k, half - 1)] * 0.15915494309189533577);
             rev -= rint(rev);
-            sincospif((float)(2.0 * rev), &s[k], &c[k]);
+            const float turn = (float)(2.0 * rev);
+            const float rest = (float)(2.0 * rev - (double)turn) * 3.14159265f;
+            float s0, c0;
+            sincospif(turn, &s0, &c0);
+            s[k] = fmaf(c0, rest, s0);
+            c[k] = fmaf(-s0, rest, c0);
         };
         angle(0);
         if (D > 128 && half > 64) angle(1);
