@@ -16,8 +16,8 @@
 // of a workgroup (tiles in turn).  The waves' results are joined through LDS,
 // the parts' through the workspace by a second kernel.
 //
-// HBM bounds it: 4 flops per byte and query head are far below what the matrix
-// cores give, and the padding of G to 16 columns with them.  64 sequences of
+// HBM bounds it: 2 flops per byte and query at most (e4m3) are far below what
+// the matrix cores give, with the padding of G to 16 columns too.  64 sequences of
 // 8192 tokens, 48 heads over 8 of 128: bf16 340 us, 6.3 TB/s; e4m3 189 us,
 // 5.9 TB/s; fp32 695 us, 6.2 TB/s; one sequence of 131071: 91 us, 5.9 TB/s (a
 // read-only stream on this card reaches 6.3 with plain loads, 7.0 with

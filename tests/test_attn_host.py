@@ -168,6 +168,28 @@ def test_workspace_bytes(L):
     assert w(-1, 10) == 0 and w(1, -1) == 0 and w(1, (1 << 30) + 1) == 0
 
 
+def test_native_marshalling_takes_gpu_tensors_only():
+    if torch.cuda.is_available():
+        pytest.skip("binds the module for a machine without a GPU")
+    from expert_routed_ffn_amd import _bind
+    c = cfg(n_heads=2, n_kv_heads=1, head_dim=64, rope_dim=0)
+    x, i = torch.zeros((3, 2, 64), dtype=torch.bfloat16), torch.zeros(3, dtype=torch.int32)
+    args = (c._c, x, x[:, :1], i, x.clone(), x[:, :1].clone(), None, None, None)
+    assert _bind.qk_norm_rope(*args) is False               # not bound to a library yet
+    L = beam.lib()
+    at = [ctypes.cast(getattr(L, "beam_moe_" + f), ctypes.c_void_p).value
+          for f in ("qk_norm_rope", "qk_norm_rope_cache", "kv_write", "kv_read", "attn_decode")]
+    _bind.bind(torch.Tensor.__dlpack_c_exchange_api__, 10, *at)
+    assert _bind.qk_norm_rope(*args) is False               # tensors of the CPU
+    assert _bind.qk_norm_rope(*args[:8]) is False           # too few arguments
+    assert _bind.kv_write(c._c, 3, None, "x", i, i) is False
+    assert _bind.kv_read(c._c, c._c, x, i, i, x, x, None) is False
+    assert _bind.attn_decode(c._c, x, c._c, x, i, i, -1, x, None, None) is False
+    assert _bind.qk_norm_rope_cache(*([None] * 12)) is False
+    with pytest.raises(TypeError):
+        _bind.bind(1, 2)
+
+
 def test_binding_refusals():
     c = cfg(n_heads=2, n_kv_heads=1, head_dim=64, rope_dim=0)
     x = torch.zeros((3, 2, 64), dtype=torch.bfloat16)
