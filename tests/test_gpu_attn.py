@@ -389,13 +389,14 @@ def test_every_code_is_exact():
         assert np.array_equal(f64(got)[0], want, equal_nan=True)
 
 
-def test_kv_read_empty_sequences_between():
+@pytest.mark.parametrize("B,every", [(3, 1), (64, 1), (65, 1), (700, 1), (700, 150), (9000, 1), (9000, 400)])
+def test_kv_read_empty_sequences_between(B, every):
     """Sequences without rows at the front, in the middle and at the end, and
-    many sequences."""
+    many sequences; long runs of empty ones inside a workgroup's rows."""
     cfg = beam.AttnCfg(3, 3, 64, 0, False, 0, 16)
-    B = 700
     g = np.random.default_rng(1)
-    n = g.integers(0, 4, B) * g.integers(0, 12, B)
+    n = g.integers(0, 4, B) * g.integers(0, 12, B) if every == 1 else np.where(np.arange(B) % every == 7, 3, 0)
+    n[1] = 40
     n[0], n[-1] = 0, 0
     c, (k, v) = filled(cfg, 50, "bf16", 2)
     table = g.integers(0, 50, (B, 3)).astype(np.int32)
@@ -949,3 +950,35 @@ def test_configurations_and_caches_copy():
     CALLS["decode"](dict(s, cache=again))
     torch.cuda.synchronize()
     assert torch.equal(s["out"], want)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp8"])
+def test_padded_batch(kind):
+    """Idle rows of a step (slot -1, length 0, no pages, NaN inputs, any
+    position) get a zero result, store nothing and change no other row."""
+    cfg, table, c, qkv, gq, gk, f, pos, slots = step_state(kind, seed=5)
+    B = qkv.shape[1]
+    bufs = beam.attn_buffers(cfg, B, 1024, keep_lse=True)
+    sides = [x for x in (c.k, c.v, c.k_scale, c.v_scale) if x is not None]
+    before = [x.clone() for x in sides]
+    beam.attn_layer(cfg, qkv[0], pos[0], slots[0], c, torch.tensor(table, device=DEV), pos[0] + 1, 1024, bufs, f, gq, gk)
+    torch.cuda.synchronize()
+    want, after = (bufs.out.clone(), bufs.lse.clone()), [x.clone() for x in sides]
+    for x, y in zip(sides, before):
+        x.copy_(y)
+    # the same rows with idle ones between them
+    at = [0, 2, 3, 5, 8, 10]
+    N = 12
+    spread = lambda x, fill: torch.full((N,) + tuple(x.shape[1:]), fill, dtype=x.dtype, device=DEV)
+    q, p, s, n, t = (spread(qkv[0], float("nan")), spread(pos[0], -1), spread(slots[0], -1), spread(pos[0], 0),
+                     spread(torch.tensor(table, device=DEV), -1))
+    q[at], p[at], s[at], n[at], t[at] = qkv[0], pos[0], slots[0], pos[0] + 1, torch.tensor(table, device=DEV)
+    big = beam.attn_buffers(cfg, N, 1024, keep_lse=True)
+    beam.attn_layer(cfg, q, p, s, c, t, n, 1024, big, f, gq, gk)
+    torch.cuda.synchronize()
+    idle = [i for i in range(N) if i not in at]
+    assert (big.out[idle] == 0).all() and torch.isneginf(big.lse[idle]).all()
+    # the same split of each sequence, so the same bits
+    assert torch.equal(big.out[at], want[0]) and torch.equal(big.lse[at], want[1])
+    for x, y in zip(sides, after):
+        assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
