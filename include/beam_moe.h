@@ -15,6 +15,11 @@
  *   combine_norm weighted combine of the K expert outputs, post-RMSNorm,
  *                depth-scaled residual h <- sqrt((n-1)/n) h + p / sqrt(n),
  *                next pre-RMSNorm
+ * and the operators of the attention sublayer between two such boundaries,
+ * for decode serving (second half of this file):
+ *   qk_norm_rope  per-head norm of queries and keys with the rotation
+ *   kv_write/read paged key-value cache, bf16, fp32 or e4m3
+ *   attn_decode   attention of one new token per sequence over that cache
  *
  * Conventions for every entry point:
  *   - All tensor pointers are DEVICE pointers, row-major, densely packed,
