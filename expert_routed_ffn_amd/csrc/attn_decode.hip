@@ -34,45 +34,46 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 // Tokens per wave step, by cache element.
 template <int KIND> constexpr int tile_tokens() { return KIND == A_F32 ? 16 : 32; }
 
-// Parts of a sequence, chosen on the device from its own length: 2^kMinShift
-// to 2^kMaxShift tokens each, and no more than `want` of them while that
-// allows; `want` is what gives kWantWG workgroups in all.  Two workgroups per
-// CU keep the memory busy, and a sequence in one part needs no join (64
-// sequences, window 512, e4m3: 13.5 us in one part, 19.3 in two).  Parts are
-// bounded so that a batch of very different lengths still spreads over the
-// chip (1 .. 32768 tokens, e4m3: 302, 292, 288 and 304 us for parts of up to
-// 1024, 2048, 4096 and 8192 tokens) until the sequences alone do that.  S, the
+// Parts of a sequence, chosen on the device from its own length: `want` even
+// ones, of kMinPart to kMaxPart tokens; `want` is what gives kWantWG workgroups
+// in all.  Two workgroups per CU keep the memory busy, and a sequence in one
+// part needs no join (64 sequences, window 512, e4m3: 13.5 us in one part, 19.3
+// in two).  Parts are bounded so that a batch of very different lengths still
+// spreads over the chip (1 .. 32768 tokens, e4m3: 302, 292, 288 and 304 us for
+// parts of up to 1024, 2048, 4096 and 8192 tokens) until the sequences alone
+// do that, and even because a power of two leaves a small batch of different
+// lengths with few, long ones (8 of 94 .. 5985, bf16: 28.5 -> 23.9 us).  S, the
 // most parts a sequence of max_len tokens can have, sizes grid and workspace;
 // parts are numbered outermost, so that those which a short sequence lacks
 // come last and only end (64 sequences of 2048 tokens, e4m3: 43.6 us where
 // 2048 are expected, 48 where 131072 are; 120 us numbered innermost with
 // kMostWG = 16384).
-constexpr int kWantWG = 512, kMostWG = 4096, kMinShift = 8, kMaxShift = 12;
-void attn_decode_split(int B, int Hkv, int max_len, int window, int* S, int* want) {
+constexpr int kWantWG = 512, kMostWG = 4096, kMinPart = 256, kMaxPart = 4096, kRound = 128;
+void attn_decode_split(int B, int Hkv, int max_len, int window, uint32_t* S, uint32_t* want) {
     // a window's tokens begin inside a 16-token block
     const int64_t span = window > 0 && window < max_len ? (int64_t)window + 15 : max_len;
     const int64_t heads = (int64_t)B * Hkv;
     const auto at_least_1 = [](int64_t v) { return v < 1 ? 1 : v; };
-    const auto parts = [&](int shift) { return at_least_1((span + (1 << shift) - 1) >> shift); };
+    const auto parts = [&](int of) { return at_least_1((span + of - 1) / of); };
     const int64_t w = at_least_1(kWantWG / heads);
-    const int64_t most = w > parts(kMaxShift) ? w : parts(kMaxShift);
-    int64_t s = parts(kMinShift) < most ? parts(kMinShift) : most;
+    const int64_t most = w > parts(kMaxPart) ? w : parts(kMaxPart);
+    int64_t s = parts(kMinPart) < most ? parts(kMinPart) : most;
     if (s > at_least_1(kMostWG / heads)) s = at_least_1(kMostWG / heads);
-    *S = (int)s;
-    *want = (int)w;
+    *S = (uint32_t)s;
+    *want = (uint32_t)w;
 }
 
 size_t attn_decode_ws_bytes(int B, int Hq, int Hkv, int D, int max_len, int window) {
-    int S, want;
+    uint32_t S, want;
     attn_decode_split(B, Hkv, max_len, window, &S, &want);
     return S > 1 ? (size_t)B * S * Hq * (D + 2) * sizeof(float) : 0;
 }
 
 // The tokens that a sequence's query sees, [start, len), cut into n parts of
-// 2^shift tokens from `base` on.  Parts double further until S of them cover
-// a sequence that is longer than expected.
+// `part` tokens (whole workgroup steps) from `base` on, and into no more than S
+// where the sequence is longer than expected.
 struct Span {
-    int start, len, base, shift, n;
+    int start, len, base, part, n;
 };
 BEAM_DEV Span span_of(const AttnDecodeArgs& a, int b) {
     const int64_t cap = min((int64_t)a.max_pages << a.c.pshift, (int64_t)kMaxLen);
@@ -81,10 +82,12 @@ BEAM_DEV Span span_of(const AttnDecodeArgs& a, int b) {
     p.start = a.window > 0 ? max(0, p.len - a.window) : 0;
     p.base = p.start & ~15;
     const uint32_t all = (uint32_t)(p.len - p.base);
-    p.shift = kMinShift;
-    while (p.shift < kMaxShift && (uint64_t)a.want << p.shift < all) ++p.shift;
-    while (((uint64_t)a.S << p.shift) < all) ++p.shift;
-    p.n = (int)((all + (1u << p.shift) - 1) >> p.shift);
+    uint32_t part = (all + a.want - 1) / a.want;
+    part = min(max(part, (uint32_t)kMinPart), (uint32_t)kMaxPart);
+    if ((uint64_t)part * a.S < all) part = (all + a.S - 1) / a.S;
+    part = (part + kRound - 1) & ~(uint32_t)(kRound - 1);
+    p.part = (int)part;
+    p.n = (int)((all + part - 1) / part);
     return p;
 }
 
@@ -174,10 +177,12 @@ template <int D, int QT> struct Acc {
     f32x4 o[QT][D / 16];
 };
 
-// With 32 queries a wave the registers are held to two waves per SIMD (64
-// queries on one head, e4m3: 61 -> 52 us); else what the compiler takes is best.
+// With 32 queries a wave, or heads of 256, the registers are held to two waves
+// per SIMD (64 queries on one head, e4m3: 61 -> 52 us; D = 256, 253 windows of 128,
+// e4m3: 51 -> 32 us); fp32 would spill there (129 -> 146 us), and else what the
+// compiler takes is best.
 template <int KIND, int D, int QT>
-__global__ __launch_bounds__(256, KIND != A_F32 && QT == 2 ? 2 : 1) void beam_attn_decode(AttnDecodeArgs a,
+__global__ __launch_bounds__(256, KIND != A_F32 && (QT == 2 || D == 256) ? 2 : 1) void beam_attn_decode(AttnDecodeArgs a,
                                                                                          int qgroups) {
     constexpr int TILE = tile_tokens<KIND>(), NU = TILE / 16;   // 16-token blocks per step
     constexpr int STEP = 4 * TILE;                              // tokens per workgroup step
@@ -210,8 +215,8 @@ __global__ __launch_bounds__(256, KIND != A_F32 && QT == 2 ? 2 : 1) void beam_at
     if (b >= a.B) return;
     const Span sp = span_of(a, b);
     if (s > 0 && s >= sp.n) return;               // no tokens; part 0 of an empty row goes on
-    const int t0 = sp.base + (int)((uint32_t)s << sp.shift);
-    const int t1 = (int)min((int64_t)sp.len, (int64_t)t0 + ((int64_t)1 << sp.shift));
+    const int t0 = sp.base + s * sp.part;
+    const int t1 = s + 1 < sp.n ? t0 + sp.part : sp.len;
 
     // query fragments: lane (r, g) holds column r of each 16-query block; the
     // reduction index (g, c, j) stands for the key element that lane g's
@@ -539,7 +544,7 @@ __global__ __launch_bounds__(256) void beam_attn_join(AttnDecodeArgs a) {
     auto load = [&](int s0) {
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) {
-            const size_t pr = first + (size_t)min(s0 + k * NG, a.S - 1) * a.Hq;
+            const size_t pr = first + (size_t)min(s0 + k * NG, (int)a.S - 1) * a.Hq;
             v[k] = ml[pr];
             o[k] = *reinterpret_cast<const float4*>(a.parts + pr * D + d);
         }

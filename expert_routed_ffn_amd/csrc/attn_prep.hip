@@ -323,12 +323,13 @@ hipError_t launch_attn_prep(const AttnPrepArgs& a, hipStream_t st) {
 }
 
 // ---------------------------------------------------------------------------
-// Cache rows back to dense rows.  A workgroup takes kReadRows consecutive
+// Cache rows back to dense rows.  A workgroup takes `rows` consecutive
 // output rows: each lane finds one row's place in the cache, then groups of
 // D/8 lanes copy one head row of one side at a time, kReadBatch of them with
 // all their loads in flight.  Bound by HBM (91500 rows of 8 heads of 128, e4m3
 // to bf16: 110 us, 5.2 TB/s; one row per workgroup: 137 us; 4 rows and loads
-// at a time: 119 us).
+// at a time: 119 us; one head of 128 instead of 8: 17.6 us with the 64 rows it
+// gets, 50 with 8).
 // ---------------------------------------------------------------------------
 template <int CK> struct RawC8;                       // 8 cache elements as stored
 template <> struct RawC8<A_BF16> { Raw8<true> v; };
@@ -365,17 +366,17 @@ template <int CK> BEAM_DEV void wid_cache8(const RawC8<CK>& r, float (&x)[8]) {
     }
 }
 
-constexpr int kReadRows = 8, kReadBatch = 8;
+constexpr int kReadBatch = 8;
 
 template <bool BF, int CK, int D>
-__global__ __launch_bounds__(256) void beam_kv_read(KvReadArgs a) {
+__global__ __launch_bounds__(256) void beam_kv_read(KvReadArgs a, int rows) {
     constexpr int LPH = D / 8, HPB = 256 / LPH;
     const int lane = threadIdx.x & 63;
-    const int row0 = blockIdx.x * kReadRows;
+    const int row0 = blockIdx.x * rows;
     const int last = a.offsets[a.B];   // rows at and behind it stay
     if (row0 >= last) return;
     // lane i: cache row (of head 0) and page of output row row0 + i
-    const int mine = row0 + min(lane, kReadRows - 1);
+    const int mine = row0 + min(lane, rows - 1);
     int lo = 0, hi = a.B;              // offsets[lo] <= mine < offsets[hi]
     while (hi - lo > 1) {
         const int mid = (lo + hi) / 2;
@@ -390,7 +391,7 @@ __global__ __launch_bounds__(256) void beam_kv_read(KvReadArgs a) {
     const int off = (int)(tok & ((1 << a.c.pshift) - 1));
 
     const int e0 = (threadIdx.x % LPH) * 8;
-    const int per_row = 2 * a.Hkv, n = min(kReadRows, min(a.N, last) - row0) * per_row;
+    const int per_row = 2 * a.Hkv, n = min(rows, min(a.N, last) - row0) * per_row;
     for (int base = 0; base < n; base += kReadBatch * HPB) {
         RawC8<CK> v[kReadBatch];
         int row[kReadBatch], h[kReadBatch];
@@ -421,12 +422,20 @@ __global__ __launch_bounds__(256) void beam_kv_read(KvReadArgs a) {
     }
 }
 
+constexpr int kReadWG = 512;
+
 template <bool BF, int CK>
 static void launch_read_d(const KvReadArgs& a, hipStream_t st) {
-    const dim3 grid((unsigned)(((size_t)a.N + kReadRows - 1) / kReadRows)), block(256);
-    if (a.D == 64) hipLaunchKernelGGL((beam_kv_read<BF, CK, 64>), grid, block, 0, st, a);
-    else if (a.D == 128) hipLaunchKernelGGL((beam_kv_read<BF, CK, 128>), grid, block, 0, st, a);
-    else hipLaunchKernelGGL((beam_kv_read<BF, CK, 256>), grid, block, 0, st, a);
+    // as many rows as give each thread kReadBatch loads (8 with 8 heads of
+    // 128; at most the 64 that a wave's lanes look up), fewer where that leaves
+    // CUs without a workgroup
+    int rows = 256 * kReadBatch / (2 * a.Hkv * (a.D / 8));
+    rows = rows < 1 ? 1 : (rows > 64 ? 64 : rows);
+    while (rows > 8 && a.N / rows < kReadWG) rows /= 2;
+    const dim3 grid((unsigned)(((size_t)a.N + rows - 1) / rows)), block(256);
+    if (a.D == 64) hipLaunchKernelGGL((beam_kv_read<BF, CK, 64>), grid, block, 0, st, a, rows);
+    else if (a.D == 128) hipLaunchKernelGGL((beam_kv_read<BF, CK, 128>), grid, block, 0, st, a, rows);
+    else hipLaunchKernelGGL((beam_kv_read<BF, CK, 256>), grid, block, 0, st, a, rows);
 }
 
 template <bool BF>

@@ -159,7 +159,7 @@ hipError_t launch_kv_read(const KvReadArgs& a, hipStream_t st);
 
 struct AttnDecodeArgs {
     int B, Hq, Hkv, G, D, max_pages, window;   // G = Hq / Hkv
-    int S, want;            // most parts a sequence can have, parts wanted (attn_decode_split)
+    uint32_t S, want;       // most parts a sequence can have, parts wanted (attn_decode_split)
     float scale;
     const void* q;
     size_t qs;
@@ -171,7 +171,7 @@ struct AttnDecodeArgs {
     KvCache c;
 };
 constexpr int kMaxLen = 1 << 30;   // longest sequence attn_decode counts
-void attn_decode_split(int B, int Hkv, int max_len, int window, int* S, int* want);
+void attn_decode_split(int B, int Hkv, int max_len, int window, uint32_t* S, uint32_t* want);
 size_t attn_decode_ws_bytes(int B, int Hq, int Hkv, int D, int max_len, int window);
 hipError_t launch_attn_decode(const AttnDecodeArgs& a, hipStream_t st);
 
