@@ -506,8 +506,8 @@ beam_status beam_moe_kv_read(const beam_moe_attn_cfg* cfg, int32_t B, int32_t N,
  *         [max(0, len - window), len) (window 0: [0, len)), len = seq_lens[b]
  *   out = sum_j softmax(z)_j v_j,   lse = log sum_j exp(z_j)
  * Sums, maxima and the join of the parts are fp32; with a BF16 or FP8_E4M3
- * cache the probabilities (times the value row's scale) are rounded to bf16
- * for the matrix cores.  Values are summed before the division by the
+ * cache a probability (times the value row's scale) enters the matrix cores as
+ * two bf16 parts, off by 2^-15 of it at most.  Values are summed before the division by the
  * probabilities' sum: magnitudes beyond 2^96 may overflow there.
  *   q      [B, n_heads, D] dtype, rows q_stride apart; out [B, n_heads, D]
  *          dtype, dense, must not overlap q.  dtype is BF16 for a BF16 or

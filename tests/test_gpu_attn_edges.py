@@ -1,0 +1,107 @@
+"""GPU tests of the attention sublayer where a wrong answer is easy to miss:
+weights of the second product, values that are infinite.
+
+Tolerances follow test_gpu_attn.py's head (h, u, A, e and n as there).  With a
+bf16 or e4m3 cache a probability enters the second product as two bf16 parts:
+its leading 8 bits, which leave less than 2^-7 of it, and the rounded rest, so
+it is off by 2^-8 * 2^-7 = 2^-15 at most (and by 2^-24 where the rest is
+nothing), in place of that head's h(bf16).
+"""
+
+import numpy as np
+import pytest
+import torch
+
+import oracle
+import test_gpu_attn as base
+from parity_util import say
+
+beam = pytest.importorskip("expert_routed_ffn_amd")
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+
+def i32(x):
+    return torch.tensor(x, dtype=torch.int32, device=DEV)
+
+
+# ------------------------------------------------------------------ weights of the second product
+
+@pytest.mark.parametrize("kind", ["bf16", "fp8", "f32"])
+@pytest.mark.parametrize("hq,hkv,D", [(8, 2, 128), (16, 1, 64), (40, 1, 128), (6, 2, 256)])
+def test_equal_values_come_back(kind, hq, hkv, D):
+    """The mean of equal values is that value, whatever the weights are: here
+    scores that are equal, but not equal to the ones before them (which set
+    the reference of the softmax)."""
+    say(f"equal values {kind} {hq}/{hkv} D={D}")
+    n, first = 2048, 128                                   # 128 tokens: one step of a workgroup
+    cfg = beam.AttnCfg(hq, hkv, D, 0, False, 0, 64, softmax_scale=1.0)
+    c = beam.kv_cache(cfg, n // 64, base.KIND[kind])
+    scale = 0.5 if kind == "fp8" else 1.0
+    c.k.copy_(torch.zeros(c.k.shape, device=DEV))
+    c.k[first // 64:, :, :, 0] = torch.full((), 1 / scale, device=DEV).to(c.k.dtype)
+    c.v.copy_(torch.full(c.v.shape, 1 / scale, device=DEV))
+    if kind == "fp8":
+        c.k_scale.fill_(scale)
+        c.v_scale.fill_(scale)
+    q = torch.zeros((1, hq, D), device=DEV)
+    q[0, :, 0] = torch.linspace(0.0037, 0.75, hq, device=DEV)
+    q = q.to(base.ACT["f32" if kind == "f32" else "bf16"])
+    out, lse = torch.empty_like(q), torch.empty((1, hq), device=DEV)
+    table = torch.arange(n // 64, dtype=torch.int32, device=DEV)[None]
+    # far fewer tokens expected: they all go to one workgroup
+    beam.beam_moe_attn_decode(cfg, q, c, table, i32([n]), 100, out, None, lse)
+    torch.cuda.synchronize()
+    got = out.double()
+    say(f"  off by {(got - 1).abs().max().item():.2e}")
+    if kind == "f32":
+        assert ((got - 1).abs() <= (n / 32 + 64) * 2.0 ** -24).all()
+    else:                                                   # 2^-15 is far below half a step, 2^-9
+        assert (got == 1).all()
+    ref = torch.log(first + (n - first) * q[0, :, 0].double().exp())
+    assert ((lse[0].double() - ref).abs() <= (n / 32 + 64 + ref) * 2.0 ** -24).all()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp8"])
+@pytest.mark.parametrize("hq,hkv,D", [(48, 8, 128), (4, 4, 64), (64, 1, 128), (16, 1, 256)])
+@pytest.mark.parametrize("window", [0, 100])
+def test_decode_to_the_last_rounding(kind, hq, hkv, D, window):
+    """The result is one rounding to bf16 away from the formula's."""
+    say(f"last rounding {kind} {hq}/{hkv} D={D} window={window}")
+    lens, P = [1, 33, 300, 900], 32
+    cfg = beam.AttnCfg(hq, hkv, D, 0, False, window, P, softmax_scale=D ** -0.5)
+    n_pages = sum(-(-n // P) for n in lens) + 1
+    c, (k, v) = base.filled(cfg, n_pages, kind, 17)
+    table = base.tables(lens, P, n_pages, 5)
+    q = (2 * torch.randn((len(lens), hq, D), generator=base.gen(3), device=DEV)).bfloat16()
+    out = torch.empty_like(q)
+    beam.beam_moe_attn_decode(cfg, q, c, torch.tensor(table, device=DEV), i32(lens), 900, out,
+                              beam.attn_workspace(cfg, len(lens), 900))
+    torch.cuda.synchronize()
+    u, over = base.U, -1.0
+    for b, n in enumerate(lens):
+        toks = range(max(0, n - window) if window else 0, n)
+        kr, _ = oracle.cached_rows(k, table[b], toks, n_pages)
+        vr, _ = oracle.cached_rows(v, table[b], toks, n_pages)
+        qb = base.f64(q[b]).reshape(hkv, hq // hkv, D)
+        ref, _, mag = oracle.decode_attention(qb, kr, vr, cfg.softmax_scale)
+        Z = cfg.softmax_scale * max((np.abs(qb[h]) @ np.abs(kr[:, h]).T).max() for h in range(hkv))
+        bound = (2.0 ** -15 + 2 * u + 2 * (D / 4 + 8) * u * Z + (len(kr) / 32 + 64) * u) * mag + 2.0 ** -8 * np.abs(ref)
+        over = max(over, (np.abs(base.f64(out[b]).reshape(ref.shape) - ref) - bound).max())
+    say(f"  over the bound by {over:.2e}")
+    assert over <= 0
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+def test_infinite_values(kind):
+    """An infinite value that is seen makes its own column infinite."""
+    cfg = beam.AttnCfg(4, 2, 64, 0, False, 0, 16, softmax_scale=0.5)
+    c, _ = base.filled(cfg, 4, kind, 2)
+    q = torch.randn((1, 4, 64), generator=base.gen(4), device=DEV).to(base.ACT[kind])
+    q[0, 0] = 0                                             # equal scores: weights of 1
+    c.v[1, 0, 3, 5], c.v[2, 0, 9, 6] = float("inf"), float("-inf")
+    out = torch.empty_like(q)
+    beam.beam_moe_attn_decode(cfg, q, c, i32([[0, 1, 2, 3]]), i32([60]), 60, out, None)
+    torch.cuda.synchronize()
+    assert torch.isposinf(out[0, :2, 5]).all() and torch.isneginf(out[0, :2, 6]).all()
+    assert torch.isfinite(out).sum() == out.numel() - 4
