@@ -553,7 +553,8 @@ _CODES = (torch.uint8, torch.float8_e4m3fn)
 # A decode step calls these entry points with a dozen small tensors.  On the
 # current device and stream the native module checks them and calls the library
 # (3.7 us a call instead of 8.1); for anything else, and for whatever does not fit, the
-# checks below run, which name what is wrong.  `dev` is a device index.
+# checks below run, which name what is wrong.  A call that failed in HIP raises at once:
+# it is not made a second time.  `dev` is a device index.
 _native = None
 
 
@@ -572,7 +573,7 @@ def _marshal():
                            "(python -c 'import __graft_entry__ as g; g.build()')") from e
     at = [ctypes.cast(getattr(L, "beam_moe_" + f), ctypes.c_void_p).value
           for f in ("qk_norm_rope", "qk_norm_rope_cache", "kv_write", "kv_read", "attn_decode")]
-    _bind.bind(api, int(torch.empty(0, device="cuda").__dlpack_device__()[0]), *at)
+    _bind.bind(api, int(torch.empty(0, device="cuda").__dlpack_device__()[0]), *at, BeamError)
     _native = _bind
     return _bind
 

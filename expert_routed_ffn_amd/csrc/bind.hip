@@ -7,8 +7,10 @@
 // what the Python function checks, and calls the C entry point on the
 // device's current stream.  It returns True when that call returned BEAM_OK
 // (3.7 us for the call above).
-// Whatever does not fit returns False with nothing enqueued, and the Python
-// function then goes its own way, which names what is wrong.
+// Whatever does not fit, here or in the entry point's own checks, returns
+// False with nothing enqueued, and the Python function then goes its own way,
+// which names what is wrong.  A call that failed in HIP may have enqueued work
+// (in place, it must not be made twice): it raises.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
@@ -22,6 +24,7 @@ namespace {
 
 const DLPackExchangeAPI* g_api = nullptr;
 int g_gpu_type = 0;   // DLPack's device type of this torch's GPU tensors
+PyObject* g_error = nullptr;   // what a failed call raises: g_error(entry point, status)
 
 decltype(&beam_moe_qk_norm_rope) g_norm_rope = nullptr;
 decltype(&beam_moe_qk_norm_rope_cache) g_norm_rope_cache = nullptr;
@@ -110,16 +113,19 @@ struct Call {
 bool open_call(PyObject* cfg, const DLTensor& act, Call& c) {
     c.cfg = struct_of<beam_moe_attn_cfg>(cfg);
     if (!c.cfg) return false;
-    int cur = -1;
     c.dev = act.device.device_id;
-    if ((int)act.device.device_type != g_gpu_type || act.ndim != 3 || hipGetDevice(&cur) != hipSuccess || cur != c.dev)
-        return false;
+    if ((int)act.device.device_type != g_gpu_type || act.ndim != 3) return false;
     c.T = act.shape[0];
     c.dt = act.dtype;
     if (same(c.dt, kBF16)) c.code = BEAM_BF16;
     else if (same(c.dt, kF32)) c.code = BEAM_F32;
     else return false;
-    if (c.T > INT32_MAX || g_api->current_work_stream(act.device.device_type, c.dev, &c.stream) != 0) {
+    if (c.T > INT32_MAX) return false;
+    c.stream = nullptr;
+    if (g_gpu_type == kDLCPU) return true;   // bound for host tensors: no current device, no stream
+    int cur = -1;
+    if (hipGetDevice(&cur) != hipSuccess || cur != c.dev) return false;
+    if (g_api->current_work_stream(act.device.device_type, c.dev, &c.stream) != 0) {
         PyErr_Clear();
         return false;
     }
@@ -139,7 +145,17 @@ const beam_moe_kv_cache* cache_of(const Call& c, PyObject* cache, PyObject* k) {
     return kv;
 }
 
-PyObject* answer(bool ok) { return PyBool_FromLong(ok); }
+PyObject* does_not_fit() { Py_RETURN_FALSE; }
+
+// What a made call comes to.
+PyObject* outcome(const char* fn, beam_status st) {
+    if (st == BEAM_OK) Py_RETURN_TRUE;
+    if (st == BEAM_ERR_INVALID_ARG || st == BEAM_ERR_UNSUPPORTED || st == BEAM_ERR_WORKSPACE) Py_RETURN_FALSE;
+    PyObject* e = PyObject_CallFunction(g_error, "si", fn, (int)st);
+    if (e) PyErr_SetObject(g_error, e);
+    Py_XDECREF(e);
+    return nullptr;
+}
 
 struct Prep {
     void *q, *k, *gq, *gk, *pos, *freq, *q_out;
@@ -164,12 +180,13 @@ PyObject* qk_norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
     Call c;
     Prep p;
     void* k_out;
-    if (n != 9 || !g_norm_rope || !prep(c, a[0], a[1], a[2], a[3], a[4], a[6], a[7], a[8], p)) return answer(false);
+    if (n != 9 || !g_norm_rope || !prep(c, a[0], a[1], a[2], a[3], a[4], a[6], a[7], a[8], p)) return does_not_fit();
     const int64_t ks[3] = {c.T, c.cfg->n_kv_heads, c.cfg->head_dim};
-    if (!dense(a[5], c.dev, c.dt, 3, ks, &k_out)) return answer(false);
-    return answer(g_norm_rope(c.cfg, (int32_t)c.T, p.q, p.qs, p.k, p.ks, c.code, p.gq, p.gk,
-                              static_cast<const int32_t*>(p.pos), static_cast<const float*>(p.freq), p.q_out, k_out,
-                              c.stream) == BEAM_OK);
+    if (!dense(a[5], c.dev, c.dt, 3, ks, &k_out)) return does_not_fit();
+    const beam_status st = g_norm_rope(c.cfg, (int32_t)c.T, p.q, p.qs, p.k, p.ks, c.code, p.gq, p.gk,
+                                       static_cast<const int32_t*>(p.pos), static_cast<const float*>(p.freq), p.q_out,
+                                       k_out, c.stream);
+    return outcome("beam_moe_qk_norm_rope", st);
 }
 
 // (cfg, q, k, v, positions, slots, q_out, cache, cache.k, inv_freq, gamma_q, gamma_k)
@@ -179,14 +196,15 @@ PyObject* qk_norm_rope_cache(PyObject*, PyObject* const* a, Py_ssize_t n) {
     void *v, *slots;
     int64_t vs;
     if (n != 12 || !g_norm_rope_cache || !prep(c, a[0], a[1], a[2], a[4], a[6], a[9], a[10], a[11], p))
-        return answer(false);
+        return does_not_fit();
     const beam_moe_kv_cache* kv = cache_of(c, a[7], a[8]);
     if (!kv || !heads(a[3], c.dev, c.dt, c.T, c.cfg->n_kv_heads, c.cfg->head_dim, &v, &vs) ||
         !dense1(a[5], c.dev, kI32, c.T, &slots))
-        return answer(false);
-    return answer(g_norm_rope_cache(c.cfg, (int32_t)c.T, p.q, p.qs, p.k, p.ks, v, vs, c.code, p.gq, p.gk,
-                                    static_cast<const int32_t*>(p.pos), static_cast<const float*>(p.freq),
-                                    static_cast<const int32_t*>(slots), p.q_out, kv, c.stream) == BEAM_OK);
+        return does_not_fit();
+    const beam_status st = g_norm_rope_cache(c.cfg, (int32_t)c.T, p.q, p.qs, p.k, p.ks, v, vs, c.code, p.gq, p.gk,
+                                             static_cast<const int32_t*>(p.pos), static_cast<const float*>(p.freq),
+                                             static_cast<const int32_t*>(slots), p.q_out, kv, c.stream);
+    return outcome("beam_moe_qk_norm_rope_cache", st);
 }
 
 // (cfg, k, v, slots, cache, cache.k)
@@ -195,14 +213,15 @@ PyObject* kv_write(PyObject*, PyObject* const* a, Py_ssize_t n) {
     DLTensor t;
     void *k, *v, *slots;
     int64_t ks, vs;
-    if (n != 6 || !g_kv_write || !view(a[1], t) || !open_call(a[0], t, c)) return answer(false);
+    if (n != 6 || !g_kv_write || !view(a[1], t) || !open_call(a[0], t, c)) return does_not_fit();
     const int64_t h = c.cfg->n_kv_heads, D = c.cfg->head_dim;
     const beam_moe_kv_cache* kv = cache_of(c, a[4], a[5]);
     if (!kv || !heads(t, c.dev, c.dt, c.T, h, D, &k, &ks) || !heads(a[2], c.dev, c.dt, c.T, h, D, &v, &vs) ||
         !dense1(a[3], c.dev, kI32, c.T, &slots))
-        return answer(false);
-    return answer(g_kv_write(c.cfg, (int32_t)c.T, k, ks, v, vs, c.code, static_cast<const int32_t*>(slots), kv,
-                             c.stream) == BEAM_OK);
+        return does_not_fit();
+    const beam_status st = g_kv_write(c.cfg, (int32_t)c.T, k, ks, v, vs, c.code, static_cast<const int32_t*>(slots), kv,
+                                      c.stream);
+    return outcome("beam_moe_kv_write", st);
 }
 
 // [B, width] int32 page table; B and width come out
@@ -222,17 +241,18 @@ PyObject* kv_read(PyObject*, PyObject* const* a, Py_ssize_t n) {
     DLTensor t;
     void *table, *off, *k, *v, *first;
     int64_t B = -1, width;
-    if (n != 8 || !g_kv_read || !view(a[5], t) || !open_call(a[0], t, c)) return answer(false);
+    if (n != 8 || !g_kv_read || !view(a[5], t) || !open_call(a[0], t, c)) return does_not_fit();
     const int64_t shape[3] = {c.T, c.cfg->n_kv_heads, c.cfg->head_dim};
     const beam_moe_kv_cache* kv = cache_of(c, a[1], a[2]);
     if (!kv || !fits(t, c.dev, c.dt, 3, shape) || !contiguous(t) || !dense(a[6], c.dev, c.dt, 3, shape, &v) ||
         !page_table(a[3], c.dev, &B, &width, &table) || !dense1(a[4], c.dev, kI32, B + 1, &off) ||
         !dense1_or_none(a[7], c.dev, kI32, B, &first))
-        return answer(false);
+        return does_not_fit();
     k = data(t);
-    return answer(g_kv_read(c.cfg, (int32_t)B, (int32_t)c.T, kv, static_cast<const int32_t*>(table), (int32_t)width,
-                            static_cast<const int32_t*>(off), static_cast<const int32_t*>(first), k, v, c.code,
-                            c.stream) == BEAM_OK);
+    const beam_status st = g_kv_read(c.cfg, (int32_t)B, (int32_t)c.T, kv, static_cast<const int32_t*>(table),
+                                     (int32_t)width, static_cast<const int32_t*>(off),
+                                     static_cast<const int32_t*>(first), k, v, c.code, c.stream);
+    return outcome("beam_moe_kv_read", st);
 }
 
 // (cfg, q, cache, cache.k, page_table, seq_lens, max_len, out, ws, lse)
@@ -241,7 +261,7 @@ PyObject* attn_decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
     DLTensor t, w;
     void *q, *table, *lens, *out, *lse = nullptr, *ws = nullptr;
     int64_t qs, width, wn = 0;
-    if (n != 10 || !g_decode || !view(a[1], t) || !open_call(a[0], t, c)) return answer(false);
+    if (n != 10 || !g_decode || !view(a[1], t) || !open_call(a[0], t, c)) return does_not_fit();
     const int64_t h = c.cfg->n_heads, D = c.cfg->head_dim, shape[3] = {c.T, h, D}, ls[2] = {c.T, h};
     int64_t B = c.T;
     const beam_moe_kv_cache* kv = cache_of(c, a[2], a[3]);
@@ -250,24 +270,30 @@ PyObject* attn_decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (!kv || max_len < 0 || max_len > INT32_MAX || !heads(t, c.dev, c.dt, B, h, D, &q, &qs) ||
         !page_table(a[4], c.dev, &B, &width, &table) || !dense1(a[5], c.dev, kI32, B, &lens) ||
         !dense(a[7], c.dev, c.dt, 3, shape, &out))
-        return answer(false);
-    if (a[9] != Py_None && !dense(a[9], c.dev, kF32, 2, ls, &lse)) return answer(false);
+        return does_not_fit();
+    if (a[9] != Py_None && !dense(a[9], c.dev, kF32, 2, ls, &lse)) return does_not_fit();
     if (a[8] != Py_None) {
-        if (!view(a[8], w) || w.ndim != 1 || !fits(w, c.dev, kU8, 1, w.shape) || !contiguous(w)) return answer(false);
+        if (!view(a[8], w) || w.ndim != 1 || !fits(w, c.dev, kU8, 1, w.shape) || !contiguous(w)) return does_not_fit();
         ws = data(w);
         wn = w.shape[0];
     }
-    return answer(g_decode(c.cfg, (int32_t)B, q, qs, c.code, kv, static_cast<const int32_t*>(table), (int32_t)width,
-                           static_cast<const int32_t*>(lens), (int32_t)max_len, out, static_cast<float*>(lse), ws,
-                           (size_t)wn, c.stream) == BEAM_OK);
+    const beam_status st = g_decode(c.cfg, (int32_t)B, q, qs, c.code, kv, static_cast<const int32_t*>(table),
+                                    (int32_t)width, static_cast<const int32_t*>(lens), (int32_t)max_len, out,
+                                    static_cast<float*>(lse), ws, (size_t)wn, c.stream);
+    return outcome("beam_moe_attn_decode", st);
 }
 
-// bind(exchange capsule, gpu device type, addresses of the five entry points)
+// bind(exchange capsule, gpu device type, addresses of the five entry points[,
+// class of the errors])
 PyObject* bind(PyObject*, PyObject* args) {
-    PyObject* cap;
+    PyObject *cap, *error = PyExc_RuntimeError;
     int type;
     unsigned long long f[5];
-    if (!PyArg_ParseTuple(args, "OiKKKKK", &cap, &type, &f[0], &f[1], &f[2], &f[3], &f[4])) return nullptr;
+    if (!PyArg_ParseTuple(args, "OiKKKKK|O", &cap, &type, &f[0], &f[1], &f[2], &f[3], &f[4], &error)) return nullptr;
+    if (!PyExceptionClass_Check(error)) {
+        PyErr_SetString(PyExc_TypeError, "not an exception class");
+        return nullptr;
+    }
     auto* api = static_cast<const DLPackExchangeAPI*>(PyCapsule_GetPointer(cap, "dlpack_exchange_api"));
     if (!api) return nullptr;
     if (api->header.version.major != DLPACK_MAJOR_VERSION || !api->dltensor_from_py_object_no_sync ||
@@ -277,6 +303,9 @@ PyObject* bind(PyObject*, PyObject* args) {
     }
     g_api = api;
     g_gpu_type = type;
+    Py_INCREF(error);
+    Py_XDECREF(g_error);
+    g_error = error;
     g_norm_rope = reinterpret_cast<decltype(g_norm_rope)>(f[0]);
     g_norm_rope_cache = reinterpret_cast<decltype(g_norm_rope_cache)>(f[1]);
     g_kv_write = reinterpret_cast<decltype(g_kv_write)>(f[2]);

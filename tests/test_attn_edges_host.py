@@ -1,0 +1,85 @@
+"""Host-side tests of the attention sublayer where a wrong answer is easy to
+miss (no GPU, no kernel is launched)."""
+
+import ctypes
+
+import pytest
+import torch
+
+beam = pytest.importorskip("expert_routed_ffn_amd")
+DLPACK_CPU = 1
+
+
+# ------------------------------------------------------------------ what the native marshalling makes of a call
+
+ENTRIES = ("qk_norm_rope", "qk_norm_rope_cache", "kv_write", "kv_read", "attn_decode")
+
+
+class Stub:
+    """Entry points that note their calls and return `status`, bound for host tensors."""
+
+    def __init__(self, status):
+        from expert_routed_ffn_amd import _bind
+        self.calls, self.status, self.bind = [], status, _bind
+        L = beam.lib()
+        self.keep = []
+        for f in ENTRIES:
+            types = getattr(L, "beam_moe_" + f).argtypes
+            self.keep.append(ctypes.CFUNCTYPE(ctypes.c_int32, *types)(lambda *a, f=f: self.called(f, a)))
+        at = [ctypes.cast(k, ctypes.c_void_p).value for k in self.keep]
+        _bind.bind(torch.Tensor.__dlpack_c_exchange_api__, DLPACK_CPU, *at, beam.BeamError)
+
+    def called(self, f, args):
+        self.calls.append((f, args))
+        return self.status
+
+
+@pytest.fixture
+def stub():
+    made = []
+
+    def make(status):
+        made.append(Stub(status))
+        return made[-1]
+    yield make
+    from expert_routed_ffn_amd import _bind
+    L = beam.lib()
+    at = [ctypes.cast(getattr(L, "beam_moe_" + f), ctypes.c_void_p).value for f in ENTRIES]
+    _bind.bind(torch.Tensor.__dlpack_c_exchange_api__, 10, *at, beam.BeamError)   # no stub is called any more
+    beam._native = None                                     # bound anew by the next call
+
+
+def native_args():
+    cfg = beam.AttnCfg(2, 1, 64, 0, False, 0, 16)
+    x, i = torch.zeros((3, 2, 64), dtype=torch.bfloat16), torch.zeros(3, dtype=torch.int32)
+    kv = torch.zeros((3, 1, 64), dtype=torch.bfloat16)
+    pages = torch.zeros((2, 1, 16, 64), dtype=torch.bfloat16)
+    cache = beam.BeamMoeKvCache(pages.data_ptr(), pages.data_ptr(), None, None, 2, beam.BEAM_BF16)
+    table, off = torch.zeros((3, 2), dtype=torch.int32), torch.zeros(4, dtype=torch.int32)
+    return {
+        "qk_norm_rope": (cfg._c, x, kv, i, x, kv, None, None, None),
+        "qk_norm_rope_cache": (cfg._c, x, kv, kv, i, i, x, cache, pages, None, None, None),
+        "kv_write": (cfg._c, kv, kv, i, cache, pages),
+        "kv_read": (cfg._c, cache, pages, table, off, kv, kv.clone(), None),
+        "attn_decode": (cfg._c, x, cache, pages, table, i, 32, x.clone(), None, None),
+    }, (cfg, x, i, kv, pages)
+
+
+@pytest.mark.parametrize("name", ENTRIES)
+def test_a_call_that_failed_in_hip_is_made_once(stub, name):
+    """A launch failure may have enqueued work, and norm and rotation may run
+    in place, so the call raises; it is not handed on to be made again."""
+    s, (args, keep) = stub(4), native_args()
+    with pytest.raises(beam.BeamError) as e:
+        getattr(s.bind, name)(*args[name])
+    assert e.value.status == 4 and "beam_moe_" + name in str(e.value)
+    assert [f for f, _ in s.calls] == [name]
+
+
+@pytest.mark.parametrize("name", ENTRIES)
+@pytest.mark.parametrize("status,want", [(0, True), (1, False), (2, False), (3, False)])
+def test_refused_and_good_calls(stub, name, status, want):
+    """Only a refusal of the arguments, which enqueues nothing, is handed on."""
+    s, (args, keep) = stub(status), native_args()
+    assert getattr(s.bind, name)(*args[name]) is want
+    assert [f for f, _ in s.calls] == [name]

@@ -105,3 +105,36 @@ def test_infinite_values(kind):
     torch.cuda.synchronize()
     assert torch.isposinf(out[0, :2, 5]).all() and torch.isneginf(out[0, :2, 6]).all()
     assert torch.isfinite(out).sum() == out.numel() - 4
+
+
+# ------------------------------------------------------------------ failures
+
+def test_a_failed_launch_is_not_made_again(monkeypatch):
+    """A call that the library answers with a HIP failure raises, and neither
+    it nor the checks behind the marshalling call the library again: here the
+    norm in place, which a second call would apply twice."""
+    import ctypes
+    from expert_routed_ffn_amd import _bind
+    cfg = beam.AttnCfg(4, 2, 64, 32, False, 0, 16)
+    q, k, _, pos, gq, gk, f = base.rope_inputs(cfg, 3, "bf16", 8)
+    q, k = q.contiguous(), k.contiguous()
+    kept = q.clone(), k.clone()
+    calls = []
+    fn = beam.lib().beam_moe_qk_norm_rope
+    failing = ctypes.CFUNCTYPE(ctypes.c_int32, *fn.argtypes)(lambda *a: calls.append(a) or 4)
+    at = [ctypes.cast(failing, ctypes.c_void_p).value] + [
+        ctypes.cast(getattr(beam.lib(), "beam_moe_" + n), ctypes.c_void_p).value
+        for n in ("qk_norm_rope_cache", "kv_write", "kv_read", "attn_decode")]
+    _bind.bind(torch.Tensor.__dlpack_c_exchange_api__, int(q.__dlpack_device__()[0]), *at)
+    monkeypatch.setattr(beam, "_native", _bind)
+    try:
+        with pytest.raises(RuntimeError):
+            beam.beam_moe_qk_norm_rope(cfg, q, k, pos, q, k, f, gq, gk)
+    finally:
+        monkeypatch.undo()
+        beam._native = None                                 # bound to the library anew
+    torch.cuda.synchronize()
+    assert len(calls) == 1 and torch.equal(q, kept[0]) and torch.equal(k, kept[1])
+    beam.beam_moe_qk_norm_rope(cfg, q, k, pos, q, k, f, gq, gk)
+    torch.cuda.synchronize()
+    assert not torch.equal(q, kept[0])
