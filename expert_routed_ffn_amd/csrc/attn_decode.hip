@@ -633,11 +633,9 @@ static hipError_t launch_decode(const AttnDecodeArgs& a, hipStream_t st) {
     const int qgroups = (a.G + 16 * QT - 1) / (16 * QT);
     const size_t bh = (size_t)a.B * a.Hkv;
     const unsigned grid = (unsigned)(qgroups == 1 ? bh : (bh + 7) / 8 * 8 * qgroups);
-    hipLaunchKernelGGL((beam_attn_decode<KIND, D, QT>), dim3(grid, a.S), dim3(256), 0, st, a, qgroups);
-    hipError_t err = hipGetLastError();
+    const hipError_t err = launch(beam_attn_decode<KIND, D, QT>, dim3(grid, a.S), dim3(256), st, a, qgroups);
     if (err != hipSuccess || a.S == 1) return err;
-    hipLaunchKernelGGL((beam_attn_join<KIND, D>), dim3((unsigned)((size_t)a.B * a.Hq)), dim3(256), 0, st, a);
-    return hipGetLastError();
+    return launch(beam_attn_join<KIND, D>, dim3((unsigned)((size_t)a.B * a.Hq)), dim3(256), st, a);
 }
 
 // Above 16 queries per key-value head a wave takes 32 at once, so the cache

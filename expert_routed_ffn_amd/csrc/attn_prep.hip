@@ -287,7 +287,7 @@ __global__ __launch_bounds__(256) void beam_attn_prep(AttnPrepArgs a, int units,
 constexpr int kPrepWaves = 32768;
 
 template <bool BF, int CK, int D>
-static void launch_prep(const AttnPrepArgs& a, hipStream_t st) {
+static hipError_t launch_prep(const AttnPrepArgs& a, hipStream_t st) {
     constexpr int HPW = 512 / D;
     const int units = a.Hq + a.Hkv * (CK < 0 ? 1 : 2);
     const int groups = (units + HPW - 1) / HPW;
@@ -298,28 +298,26 @@ static void launch_prep(const AttnPrepArgs& a, hipStream_t st) {
     const int gpw = (int)min((int64_t)groups, max((int64_t)1, (int64_t)a.T * groups / kPrepWaves));
     const int wpt = (groups + gpw - 1) / gpw;
     const unsigned grid = (unsigned)(((size_t)a.T * wpt + 3) / 4);
-    hipLaunchKernelGGL((beam_attn_prep<BF, CK, D>), dim3(grid), dim3(256), 0, st, a, units, wpt, gpw);
+    return launch(beam_attn_prep<BF, CK, D>, dim3(grid), dim3(256), st, a, units, wpt, gpw);
 }
 
 template <bool BF, int CK>
-static void launch_prep_d(const AttnPrepArgs& a, hipStream_t st) {
-    if (a.D == 64) launch_prep<BF, CK, 64>(a, st);
-    else if (a.D == 128) launch_prep<BF, CK, 128>(a, st);
-    else launch_prep<BF, CK, 256>(a, st);
+static hipError_t launch_prep_d(const AttnPrepArgs& a, hipStream_t st) {
+    if (a.D == 64) return launch_prep<BF, CK, 64>(a, st);
+    if (a.D == 128) return launch_prep<BF, CK, 128>(a, st);
+    return launch_prep<BF, CK, 256>(a, st);
 }
 
 template <bool BF>
-static void launch_prep_c(const AttnPrepArgs& a, hipStream_t st) {
-    if (a.k_out) launch_prep_d<BF, -1>(a, st);
-    else if (a.c.kind == A_F32) launch_prep_d<BF, A_F32>(a, st);
-    else if (a.c.kind == A_BF16) launch_prep_d<BF, A_BF16>(a, st);
-    else launch_prep_d<BF, A_FP8>(a, st);
+static hipError_t launch_prep_c(const AttnPrepArgs& a, hipStream_t st) {
+    if (a.k_out) return launch_prep_d<BF, -1>(a, st);
+    if (a.c.kind == A_F32) return launch_prep_d<BF, A_F32>(a, st);
+    if (a.c.kind == A_BF16) return launch_prep_d<BF, A_BF16>(a, st);
+    return launch_prep_d<BF, A_FP8>(a, st);
 }
 
 hipError_t launch_attn_prep(const AttnPrepArgs& a, hipStream_t st) {
-    if (a.bf16) launch_prep_c<true>(a, st);
-    else launch_prep_c<false>(a, st);
-    return hipGetLastError();
+    return a.bf16 ? launch_prep_c<true>(a, st) : launch_prep_c<false>(a, st);
 }
 
 // ---------------------------------------------------------------------------
@@ -425,7 +423,7 @@ __global__ __launch_bounds__(256) void beam_kv_read(KvReadArgs a, int rows) {
 constexpr int kReadWG = 512;
 
 template <bool BF, int CK>
-static void launch_read_d(const KvReadArgs& a, hipStream_t st) {
+static hipError_t launch_read_d(const KvReadArgs& a, hipStream_t st) {
     // as many rows as give each thread kReadBatch loads (8 with 8 heads of
     // 128; at most the 64 that a wave's lanes look up), fewer where that leaves
     // CUs without a workgroup
@@ -433,22 +431,20 @@ static void launch_read_d(const KvReadArgs& a, hipStream_t st) {
     rows = rows < 1 ? 1 : (rows > 64 ? 64 : rows);
     while (rows > 8 && a.N / rows < kReadWG) rows /= 2;
     const dim3 grid((unsigned)(((size_t)a.N + rows - 1) / rows)), block(256);
-    if (a.D == 64) hipLaunchKernelGGL((beam_kv_read<BF, CK, 64>), grid, block, 0, st, a, rows);
-    else if (a.D == 128) hipLaunchKernelGGL((beam_kv_read<BF, CK, 128>), grid, block, 0, st, a, rows);
-    else hipLaunchKernelGGL((beam_kv_read<BF, CK, 256>), grid, block, 0, st, a, rows);
+    if (a.D == 64) return launch(beam_kv_read<BF, CK, 64>, grid, block, st, a, rows);
+    if (a.D == 128) return launch(beam_kv_read<BF, CK, 128>, grid, block, st, a, rows);
+    return launch(beam_kv_read<BF, CK, 256>, grid, block, st, a, rows);
 }
 
 template <bool BF>
-static void launch_read_c(const KvReadArgs& a, hipStream_t st) {
-    if (a.c.kind == A_F32) launch_read_d<BF, A_F32>(a, st);
-    else if (a.c.kind == A_BF16) launch_read_d<BF, A_BF16>(a, st);
-    else launch_read_d<BF, A_FP8>(a, st);
+static hipError_t launch_read_c(const KvReadArgs& a, hipStream_t st) {
+    if (a.c.kind == A_F32) return launch_read_d<BF, A_F32>(a, st);
+    if (a.c.kind == A_BF16) return launch_read_d<BF, A_BF16>(a, st);
+    return launch_read_d<BF, A_FP8>(a, st);
 }
 
 hipError_t launch_kv_read(const KvReadArgs& a, hipStream_t st) {
-    if (a.bf16) launch_read_c<true>(a, st);
-    else launch_read_c<false>(a, st);
-    return hipGetLastError();
+    return a.bf16 ? launch_read_c<true>(a, st) : launch_read_c<false>(a, st);
 }
 
 }  // namespace beam

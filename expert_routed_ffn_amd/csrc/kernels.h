@@ -6,6 +6,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <tuple>
+
 namespace beam {
 
 struct RouteArgs {
@@ -109,6 +111,22 @@ struct CombineArgs {
     bool partial_only;      // write m to moe_out and stop (no norm boundary)
 };
 hipError_t launch_combine_norm(const CombineArgs& a, hipStream_t st);
+
+// Launches a kernel with its arguments.  The status is this launch's own:
+// hipGetLastError() alone also gives what an earlier, unrelated call left, and
+// a launch that ran would be reported as failed.
+template <typename... P, typename... A>
+hipError_t launch(void (*kernel)(P...), dim3 grid, dim3 block, hipStream_t st, const A&... args) {
+    std::tuple<P...> values(args...);
+    const hipError_t err = std::apply(
+        [&](auto&... v) {
+            void* at[] = {&v...};
+            return hipLaunchKernel(reinterpret_cast<const void*>(kernel), grid, block, at, 0, st);
+        },
+        values);
+    if (err != hipSuccess) (void)hipGetLastError();   // returned here, not left for the next call
+    return err;
+}
 
 // Element kinds of the attention sublayer's activations and cache.
 enum AKind { A_F32 = 0, A_BF16 = 1, A_FP8 = 2 };

@@ -138,3 +138,42 @@ def test_a_failed_launch_is_not_made_again(monkeypatch):
     beam.beam_moe_qk_norm_rope(cfg, q, k, pos, q, k, f, gq, gk)
     torch.cuda.synchronize()
     assert not torch.equal(q, kept[0])
+
+
+def hip_runtime():
+    """The HIP runtime that this process has loaded."""
+    import ctypes
+    with open("/proc/self/maps") as f:
+        paths = {line.split()[-1] for line in f if "libamdhip64" in line}
+    assert len(paths) == 1, paths
+    return ctypes.CDLL(paths.pop())
+
+
+@pytest.mark.parametrize("name", base.CALLS)
+@pytest.mark.parametrize("native", [True, False])
+def test_an_earlier_error_is_not_this_calls(name, native):
+    """An error that an unrelated HIP call left (a device that is not there)
+    neither fails a call that runs nor makes it run twice."""
+    hip = hip_runtime()
+    s = base.binding_state()
+    s["k"], s["q"] = s["k"].contiguous(), s["q"].contiguous()
+    if name == "rope":
+        s["ko"], s["qo"] = s["k"], s["q"]                   # in place
+    kw = {} if native else {"stream": torch.cuda.current_stream()}
+    sides = (s["cache"].k, s["cache"].v, s["cache"].k_scale, s["cache"].v_scale)
+    touched = [s[r] for r in base.RESULTS[name]] + list(sides)
+    start = [t.clone() for t in touched]
+    base.CALLS[name](s, **kw)
+    torch.cuda.synchronize()
+    want = [t.clone() for t in touched]
+    for t, u in zip(touched, start):
+        t.copy_(u)
+    torch.cuda.synchronize()
+    assert hip.hipSetDevice(1 << 10) != 0
+    try:
+        base.CALLS[name](s, **kw)
+    finally:
+        hip.hipGetLastError()
+    torch.cuda.synchronize()
+    for t, u in zip(touched, want):
+        assert torch.equal(t.view(torch.uint8), u.view(torch.uint8))
