@@ -420,16 +420,22 @@ __global__ __launch_bounds__(256) void beam_kv_read(KvReadArgs a, int rows) {
     }
 }
 
-constexpr int kReadWG = 512;
+// Rows of a workgroup: as many as give each thread kReadBatch loads (8 with 8
+// heads of 128; at most the 64 that a wave's lanes look up), fewer where that
+// leaves CUs without a workgroup, more where a launch could not hold the
+// workgroups (it holds fewer than 2^32 threads).
+constexpr int kReadWG = 512, kMostReadWG = 1 << 23;
+int kv_read_rows(int N, int Hkv, int D) {
+    int rows = 256 * kReadBatch / (2 * Hkv * (D / 8));
+    rows = rows < 1 ? 1 : (rows > 64 ? 64 : rows);
+    while (rows > 8 && N / rows < kReadWG) rows /= 2;
+    const int least = (int)(((int64_t)N + kMostReadWG - 1) / kMostReadWG);   // 8 for the most rows of a call
+    return rows < least ? least : rows;
+}
 
 template <bool BF, int CK>
 static hipError_t launch_read_d(const KvReadArgs& a, hipStream_t st) {
-    // as many rows as give each thread kReadBatch loads (8 with 8 heads of
-    // 128; at most the 64 that a wave's lanes look up), fewer where that leaves
-    // CUs without a workgroup
-    int rows = 256 * kReadBatch / (2 * a.Hkv * (a.D / 8));
-    rows = rows < 1 ? 1 : (rows > 64 ? 64 : rows);
-    while (rows > 8 && a.N / rows < kReadWG) rows /= 2;
+    const int rows = kv_read_rows(a.N, a.Hkv, a.D);
     const dim3 grid((unsigned)(((size_t)a.N + rows - 1) / rows)), block(256);
     if (a.D == 64) return launch(beam_kv_read<BF, CK, 64>, grid, block, st, a, rows);
     if (a.D == 128) return launch(beam_kv_read<BF, CK, 128>, grid, block, st, a, rows);

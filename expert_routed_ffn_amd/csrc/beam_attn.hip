@@ -10,9 +10,8 @@
 namespace {
 
 constexpr int64_t kMaxT = 1 << 22;          // tokens or sequences per call
-// launches of 256-thread workgroups hold fewer than 2^32 threads
-constexpr int64_t kMaxRows = 1 << 26;       // rows read back per call, 8 per workgroup
-constexpr int64_t kMaxParts = 1 << 23;      // query heads times parts per decode call
+constexpr int64_t kMaxParts = 1 << 23;      // query heads times parts per decode call: a launch of 256-thread
+                                            // workgroups holds fewer than 2^32 threads
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
@@ -193,7 +192,7 @@ beam_status beam_moe_kv_read(const beam_moe_attn_cfg* cfg, int32_t B, int32_t N,
                              const int32_t* first, void* k_out, void* v_out, beam_dtype dtype, void* stream) {
     beam_status st = check_attn_cfg(cfg);
     if (st != BEAM_OK) return st;
-    if (B < 0 || B > kMaxT || N < 0 || N > kMaxRows || max_pages < 0 || !act_dtype(dtype))
+    if (B < 0 || B > kMaxT || N < 0 || N > beam::kMaxReadRows || max_pages < 0 || !act_dtype(dtype))
         return BEAM_ERR_INVALID_ARG;
     if (B == 0 || N == 0) return BEAM_OK;
     if (!row_offsets || !aligned4(row_offsets) || !aligned4(first) || !k_out || !v_out || !aligned16(k_out) ||

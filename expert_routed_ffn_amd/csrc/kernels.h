@@ -173,6 +173,8 @@ struct KvReadArgs {
     void* v_out;
     KvCache c;
 };
+constexpr int kMaxReadRows = 1 << 26;   // rows read back per call
+int kv_read_rows(int N, int Hkv, int D);   // output rows of a workgroup
 hipError_t launch_kv_read(const KvReadArgs& a, hipStream_t st);
 
 struct AttnDecodeArgs {

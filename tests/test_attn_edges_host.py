@@ -83,3 +83,18 @@ def test_refused_and_good_calls(stub, name, status, want):
     s, (args, keep) = stub(status), native_args()
     assert getattr(s.bind, name)(*args[name]) is want
     assert [f for f, _ in s.calls] == [name]
+
+
+# ------------------------------------------------------------------ what a launch can hold
+
+@pytest.mark.parametrize("N", [1, 511, 4096, (1 << 22) + 1, (1 << 24) - 1, 1 << 24, (1 << 25) + 7, 1 << 26])
+def test_every_read_back_that_is_accepted_can_be_launched(N):
+    """Output rows per workgroup: between one and the 64 that a wave looks up,
+    and so many that a launch stays below 2^32 threads."""
+    rows = beam.lib()._ZN4beam12kv_read_rowsEiii
+    rows.argtypes, rows.restype = [ctypes.c_int32] * 3, ctypes.c_int32
+    for hkv in (1, 2, 3, 8, 16, 32, 33, 64, 100, 256):
+        for D in (64, 128, 256):
+            r = rows(N, hkv, D)
+            assert 1 <= r <= 64
+            assert -(-N // r) * 256 < 1 << 32, (N, hkv, D, r)

@@ -177,3 +177,22 @@ def test_an_earlier_error_is_not_this_calls(name, native):
     torch.cuda.synchronize()
     for t, u in zip(touched, want):
         assert torch.equal(t.view(torch.uint8), u.view(torch.uint8))
+
+
+# ------------------------------------------------------------------ read back
+
+@pytest.mark.parametrize("kind", ["bf16", "fp8"])
+@pytest.mark.parametrize("hkv,D,N", [(64, 128, 90), (256, 64, 70), (33, 256, 41), (1, 64, 3000), (256, 256, 5)])
+def test_read_back_of_many_and_few_heads(kind, hkv, D, N):
+    """Rows that take a workgroup several turns, and as many rows as it takes."""
+    cfg = beam.AttnCfg(hkv, hkv, D, 0, False, 0, 16)
+    n_pages = -(-N // 16) + 2
+    c, (k, v) = base.filled(cfg, n_pages, kind, 5)
+    table = base.tables([N], 16, n_pages, 2)
+    ko, vo = (torch.full((N + 2, hkv, D), 3.0, device=DEV) for _ in range(2))
+    beam.beam_moe_kv_read(cfg, c, torch.tensor(table, device=DEV), i32([0, N]), ko, vo)
+    torch.cuda.synchronize()
+    t = np.arange(N)
+    for got, ref in ((ko, k), (vo, v)):
+        assert np.array_equal(base.f64(got[:N]), ref[table[0, t // 16], :, t % 16].astype(np.float32))
+        assert (got[N:] == 3).all()
