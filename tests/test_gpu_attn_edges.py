@@ -196,3 +196,75 @@ def test_read_back_of_many_and_few_heads(kind, hkv, D, N):
     for got, ref in ((ko, k), (vo, v)):
         assert np.array_equal(base.f64(got[:N]), ref[table[0, t // 16], :, t % 16].astype(np.float32))
         assert (got[N:] == 3).all()
+
+
+# ------------------------------------------------------------------ e4m3 rows
+
+def awkward_rows(T, hkv, D, act, seed):
+    """Rows with zeros of both signs in them, of both signs only, of extreme
+    sizes (whose division goes another way), of values at the codes' borders."""
+    g = base.gen(seed)
+    x = torch.randn((T, hkv, D), generator=g, device=DEV)
+    x = torch.where(torch.rand(x.shape, generator=g, device=DEV) < 0.2, torch.zeros_like(x), x)
+    x = torch.where(torch.rand(x.shape, generator=g, device=DEV) < 0.5, -x, x)
+    x[3::11] *= 1e-30
+    x[5::11] *= 1e30
+    x[7::11, 0] *= 0
+    x[8::11] = torch.arange(D, device=DEV) * (448.0 / 256)
+    x[9::11, :, ::2] *= 2.0 ** -12
+    return x.to(base.ACT[act])
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("special", [False, True])
+def test_cache_codes_are_the_quantisers(D, special):
+    """Codes and scales of a stored row are, byte for byte, those of
+    beam_moe_quantize_fp8, whatever rows stand beside it: signs of zeros,
+    rows of extreme sizes, NaN and infinities too."""
+    T, hkv = 66, 3
+    x = awkward_rows(T, hkv, D, "bf16", D)
+    if special:
+        x[0, 0, 3], x[1, 1, 5], x[2, 2, 7], x[4, 0, 9] = (float(s) for s in ("nan", "inf", "-inf", "nan"))
+        x.view(torch.int16)[4, 0, 9] = -64                  # a NaN with its sign set
+    cfg = beam.AttnCfg(hkv, hkv, D, 0, False, 0, 16)
+    c = beam.kv_cache(cfg, 5, beam.BEAM_FP8_E4M3)
+    beam.beam_moe_kv_write(cfg, x, x.flip(0), torch.arange(T, dtype=torch.int32, device=DEV), c)
+    wide = torch.zeros((T * hkv, 256), dtype=torch.bfloat16, device=DEV)     # zeros behind a row change nothing of it
+    wide[:, :D] = x.view(T * hkv, D)
+    codes = torch.empty((T * hkv, 256), dtype=torch.uint8, device=DEV)
+    scale = torch.empty(T * hkv, device=DEV)
+    beam.beam_moe_quantize_fp8(beam.LayerCfg(hidden=256), wide, codes, scale)
+    torch.cuda.synchronize()
+    want, ws = codes[:, :D].view(T, hkv, D), scale.view(T, hkv)
+    t = torch.arange(T, device=DEV)
+    for side, sc, order in ((c.k, c.k_scale, t), (c.v, c.v_scale, t.flip(0))):
+        got = side.view(torch.uint8)[t // 16, :, t % 16]
+        assert torch.equal(sc[t // 16, :, t % 16].view(torch.int32), ws[order].view(torch.int32))
+        bad = torch.nonzero(got != want[order])
+        say(f"  D={D}: {len(bad)} codes differ")
+        assert len(bad) == 0
+    assert special or (want[:, :, :] == 0x80).any()         # there are zeros below zero
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_cache_codes_of_fp32_rows(D):
+    """fp32 rows: each code is e4m3 of the correctly rounded fp32 quotient."""
+    T, hkv = 660, 3
+    x = awkward_rows(T, hkv, D, "f32", D + 1)
+    # a scale of 2 - 2^-23, whose reciprocal lies next to the middle of two
+    # floats: 2^-9 / scale is just above 2^-10, the middle of codes 0 and 1
+    x[0, 0] = 0
+    x[0, 0, 0], x[0, 0, 1], x[0, 0, 2] = 896 - 2.0 ** -14, 2.0 ** -9, -2.0 ** -9
+    cfg = beam.AttnCfg(hkv, hkv, D, 0, False, 0, 64)
+    c = beam.kv_cache(cfg, 11, beam.BEAM_FP8_E4M3)
+    beam.beam_moe_kv_write(cfg, x, x, torch.arange(T, dtype=torch.int32, device=DEV), c)
+    torch.cuda.synchronize()
+    h = x.cpu().numpy()
+    top = np.abs(h).max(-1)
+    s = np.where(top > 0, top / np.float32(448), np.float32(1))
+    want = torch.tensor(h / s[..., None]).to(torch.float8_e4m3fn).view(torch.uint8)
+    assert s[0, 0] == 2 - 2.0 ** -23 and want[0, 0, 1] == 1 and want[0, 0, 2] == 0x81
+    t = torch.arange(T, device=DEV)
+    for side, sc in ((c.k, c.k_scale), (c.v, c.v_scale)):
+        assert np.array_equal(sc[t // 64, :, t % 64].cpu().numpy(), s)
+        assert torch.equal(side.view(torch.uint8)[t // 64, :, t % 64].cpu(), want)
