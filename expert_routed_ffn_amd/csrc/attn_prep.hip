@@ -116,7 +116,8 @@ BEAM_DEV void store_cache(void* side, float* scales, size_t row, int e0, float (
 #pragma unroll
         for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(x[j]));
         amax = head_max<D / 8>(amax);   // every lane takes part
-        const float s = amax > 0.f ? __fdiv_rn(amax, 448.0f) : 1.0f;
+        const float top = __fdiv_rn(amax, 448.0f);
+        const float s = top > 0.f ? top : 1.0f;   // 0 too where amax / 448 is less than half the least float
         divide8(x, s);
         if (!live) return;
         *reinterpret_cast<uint2*>(static_cast<uint8_t*>(side) + row * D + e0) =

@@ -453,7 +453,7 @@ beam_status beam_moe_qk_norm_rope(const beam_moe_attn_cfg* cfg, int32_t T,
  * beam_moe_qk_norm_rope_cache -- the same for q, while k goes (normed and
  * rotated) and v goes (as it is) into the cache at slots[t], in one launch.
  * What is stored is the fp32 result rounded once to the cache's dtype; for
- * FP8_E4M3, scale = amax/448 of the head row (1 for a row of zeros) and
+ * FP8_E4M3, scale = amax/448 of the head row in fp32 (1 where that is 0) and
  * code = e4m3(value / scale), rounded to nearest even, as
  * beam_moe_quantize_fp8 does per token.
  *   slots [T] int32: a row whose slot is outside [0, n_pages * page_size)

@@ -268,3 +268,23 @@ def test_cache_codes_of_fp32_rows(D):
     for side, sc in ((c.k, c.k_scale), (c.v, c.v_scale)):
         assert np.array_equal(sc[t // 64, :, t % 64].cpu().numpy(), s)
         assert torch.equal(side.view(torch.uint8)[t // 64, :, t % 64].cpu(), want)
+
+
+def test_rows_of_the_least_floats():
+    """A row so small that its scale would round to zero is stored as zeros."""
+    cfg = beam.AttnCfg(2, 2, 64, 0, False, 0, 16)
+    x = torch.zeros((4, 2, 64), device=DEV)
+    least = 2.0 ** -149
+    x[0, 0, 3], x[0, 1, 5], x[1, 0, 1], x[1, 1, 9] = least, -least, 224 * least, 225 * least
+    x[2] = -0.0
+    c = base.poisoned(cfg, 1, "fp8")
+    beam.beam_moe_kv_write(cfg, x, x, torch.arange(4, dtype=torch.int32, device=DEV), c)
+    ko, vo = (torch.empty((4, 2, 64), device=DEV) for _ in range(2))
+    beam.beam_moe_kv_read(cfg, c, i32([[0]]), i32([0, 4]), ko, vo)
+    torch.cuda.synchronize()
+    want_s = [[1, 1], [1, least], [1, 1], [1, 1]]           # 224/448 is a tie, and goes to 0
+    for got, sc in ((ko, c.k_scale), (vo, c.v_scale)):
+        assert sc[0, :, :4].t().double().tolist() == want_s
+        assert torch.isfinite(got).all()
+        assert ((got.double() - x.double()).abs() <= 224 * least).all()
+        assert got[1, 1, 9].item() == 224 * least           # code 224, the nearest to 225
