@@ -18,6 +18,7 @@ from __future__ import annotations
 
 import ctypes
 import dataclasses
+import operator
 import os
 
 import torch
@@ -64,6 +65,15 @@ class LayerCfg:
                           self.group_topn, self.d_ff, self.routed_scale, self.rms_eps)
 
 
+def _i32(v, name):
+    """An integer that the C struct or call holds as it is (ctypes would keep
+    the low 32 bits of a larger one)."""
+    i = operator.index(v)
+    if not -(1 << 31) <= i < 1 << 31:
+        raise ValueError(f"{name}: {v} does not fit 32 bits")
+    return i
+
+
 class BeamMoeAttnCfg(ctypes.Structure):
     _fields_ = [("n_heads", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
                 ("rope_dim", ctypes.c_int32), ("rope_interleaved", ctypes.c_int32), ("window", ctypes.c_int32),
@@ -94,9 +104,11 @@ class AttnCfg:
     rms_eps: float = 1e-6
 
     def __post_init__(self):
-        c = BeamMoeAttnCfg(self.n_heads, self.n_kv_heads, self.head_dim, self.rope_dim,
-                           int(self.rope_interleaved), self.window, self.page_size, self.ssmax_len,
-                           self.ssmax_exp, self.softmax_scale, self.rms_eps)
+        c = BeamMoeAttnCfg(_i32(self.n_heads, "n_heads"), _i32(self.n_kv_heads, "n_kv_heads"),
+                           _i32(self.head_dim, "head_dim"), _i32(self.rope_dim, "rope_dim"),
+                           _i32(int(self.rope_interleaved), "rope_interleaved"), _i32(self.window, "window"),
+                           _i32(self.page_size, "page_size"), self.ssmax_len, self.ssmax_exp, self.softmax_scale,
+                           self.rms_eps)
         object.__setattr__(self, "_c", c)
 
     def c(self) -> BeamMoeAttnCfg:
@@ -772,7 +784,7 @@ def beam_moe_kv_read(cfg: AttnCfg, cache: KVCache, page_table, row_offsets, k_ou
 
 
 def attn_workspace(cfg: AttnCfg, B: int, max_len: int, device="cuda") -> torch.Tensor:
-    n = int(lib().beam_moe_attn_workspace_bytes(cfg.c(), B, max_len))
+    n = int(lib().beam_moe_attn_workspace_bytes(cfg.c(), _i32(B, "B"), _i32(max_len, "max_len")))
     return torch.empty(max(n, 256), dtype=torch.uint8, device=device)
 
 
@@ -797,8 +809,8 @@ def beam_moe_attn_decode(cfg: AttnCfg, q, cache: KVCache, page_table, seq_lens, 
     if ws is not None:
         wn = ws.numel()
         wp = _on(dev, ws, (wn,), torch.uint8, "ws")
-    _launch("beam_moe_attn_decode", dev, stream, cfg._c, B, qp, qs, code, cache.c(cfg, dev), tp, width, lp, max_len,
-            op, ep, wp, wn)
+    _launch("beam_moe_attn_decode", dev, stream, cfg._c, B, qp, qs, code, cache.c(cfg, dev), tp, width, lp,
+            _i32(max_len, "max_len"), op, ep, wp, wn)
 
 
 @dataclasses.dataclass

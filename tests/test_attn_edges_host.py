@@ -98,3 +98,23 @@ def test_every_read_back_that_is_accepted_can_be_launched(N):
             r = rows(N, hkv, D)
             assert 1 <= r <= 64
             assert -(-N // r) * 256 < 1 << 32, (N, hkv, D, r)
+
+
+# ------------------------------------------------------------------ integers beyond 32 bits
+
+@pytest.mark.parametrize("field", ["n_heads", "n_kv_heads", "head_dim", "rope_dim", "rope_interleaved", "window",
+                                   "page_size"])
+@pytest.mark.parametrize("by", [1 << 32, -(1 << 32), 1 << 40])
+def test_a_configuration_is_not_cut_to_32_bits(field, by):
+    """Taken modulo 2^32, a window of 2^32 tokens would be none at all."""
+    good = getattr(beam.AttnCfg(), field)
+    assert getattr(beam.AttnCfg(**{field: good})._c, field) == good
+    with pytest.raises(ValueError, match=field):
+        beam.AttnCfg(**{field: int(good) + by})
+
+
+@pytest.mark.parametrize("B,max_len", [(1, (1 << 32) + 100), (1, -(1 << 32)), ((1 << 32) + 1, 100)])
+def test_a_workspace_is_not_cut_to_32_bits(B, max_len):
+    with pytest.raises(ValueError):
+        beam.attn_workspace(beam.AttnCfg(), B, max_len, device="cpu")
+    assert beam.attn_workspace(beam.AttnCfg(window=0), 1, 131072, device="cpu").numel() > 256

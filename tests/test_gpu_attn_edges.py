@@ -288,3 +288,19 @@ def test_rows_of_the_least_floats():
         assert torch.isfinite(got).all()
         assert ((got.double() - x.double()).abs() <= 224 * least).all()
         assert got[1, 1, 9].item() == 224 * least           # code 224, the nearest to 225
+
+
+# ------------------------------------------------------------------ refusals
+
+@pytest.mark.parametrize("max_len", [(1 << 32) + 32, 1 << 32, -(1 << 32), (1 << 31), (1 << 30) + 1, -1])
+@pytest.mark.parametrize("native", [True, False])
+def test_lengths_to_expect_beyond_the_limit(max_len, native):
+    """Refused, not taken modulo 2^32."""
+    s = base.binding_state()
+    s["out"].fill_(3.0)
+    kw = {} if native else {"stream": torch.cuda.current_stream()}
+    with pytest.raises((ValueError, beam.BeamError)):
+        beam.beam_moe_attn_decode(s["cfg"], s["qo"], s["cache"], s["table"], s["lens"], max_len, s["out"], s["ws"],
+                                  s["lse"], **kw)
+    torch.cuda.synchronize()
+    assert (s["out"] == 3).all()
