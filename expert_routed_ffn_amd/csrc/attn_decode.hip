@@ -42,53 +42,161 @@ template <int KIND> constexpr int tile_tokens() { return KIND == A_F32 ? 16 : 32
 // spreads over the chip (1 .. 32768 tokens, e4m3: 302, 292, 288 and 304 us for
 // parts of up to 1024, 2048, 4096 and 8192 tokens) until the sequences alone
 // do that, and even because a power of two leaves a small batch of different
-// lengths with few, long ones (8 of 94 .. 5985, bf16: 28.5 -> 23.9 us).  S, the
-// most parts a sequence of max_len tokens can have, sizes grid and workspace;
-// parts are numbered outermost, so that those which a short sequence lacks
-// come last and only end (64 sequences of 2048 tokens, e4m3: 43.6 us where
-// 2048 are expected, 48 where 131072 are; 120 us numbered innermost with
-// kMostWG = 16384).
-constexpr int kWantWG = 512, kMostWG = 4096, kMinPart = 256, kMaxPart = 4096, kRound = 128;
-void attn_decode_split(int B, int Hkv, int max_len, int window, uint32_t* S, uint32_t* want) {
+// lengths with few, long ones (8 of 94 .. 5985, bf16: 28.5 -> 23.9 us).
+//
+// S, the most parts a sequence of max_len tokens can have, sizes grid and
+// workspace while there are at most kMostWG workgroups; parts are numbered
+// outermost, so that those which a short sequence lacks come last and only
+// end (64 sequences of 2048 tokens, e4m3: 43.6 us where 2048 are expected; 120
+// us numbered innermost with kMostWG = 16384).
+//
+// Where that bound would make parts longer than kMaxPart, they are listed by a
+// kernel of one workgroup first (beam_attn_list): the grid holds `want` parts of
+// every sequence and kMostWG workgroups (`extra` parts of each head) more,
+// wherever they are needed, and parts grow beyond kMaxPart, to the same multiple
+// for all sequences, only where the lengths together ask for more.  Cut to S
+// parts instead, one long sequence among many runs on its own (e4m3, 131072
+// tokens beside 300 sequences of 512: 1061 us, listed 112; beside 1000: 1181 and
+// 250; 256 sequences of 1 .. 32768: 981 and 964), while without long ones the list
+// is 2 to 4 % (64 sequences of 2048, 131072 expected: 46.3 us and 48.3; 2000 of
+// 512: 363 and 378) and at worst its launch (64 of 512: 18.3 and 20.1).  Above
+// kMostListed sequences there are workgroups enough to run beside a long one
+// for most of its time, and S is cut.
+constexpr int kWantWG = 512, kMostWG = 4096, kMinPart = 256, kMaxPart = 4096, kRound = 128, kMostListed = 2048;
+AttnSplit attn_decode_split(int B, int Hkv, int max_len, int window) {
     // a window's tokens begin inside a 16-token block
     const int64_t span = window > 0 && window < max_len ? (int64_t)window + 15 : max_len;
     const int64_t heads = (int64_t)B * Hkv;
     const auto at_least_1 = [](int64_t v) { return v < 1 ? 1 : v; };
     const auto parts = [&](int of) { return at_least_1((span + of - 1) / of); };
-    const int64_t w = at_least_1(kWantWG / heads);
+    const int64_t w = at_least_1(kWantWG / heads), cap = at_least_1(kMostWG / heads);
     const int64_t most = w > parts(kMaxPart) ? w : parts(kMaxPart);
-    int64_t s = parts(kMinPart) < most ? parts(kMinPart) : most;
-    if (s > at_least_1(kMostWG / heads)) s = at_least_1(kMostWG / heads);
-    *S = (uint32_t)s;
-    *want = (uint32_t)w;
+    const int64_t s = parts(kMinPart) < most ? parts(kMinPart) : most;
+    AttnSplit p;
+    p.want = (uint32_t)w;
+    p.S = (uint32_t)(s < cap ? s : cap);
+    p.extra = cap < parts(kMaxPart) && B > 1 && B <= kMostListed ? (uint32_t)at_least_1(kMostWG / Hkv) : 0;
+    p.rows = p.extra ? (uint64_t)B * p.want + p.extra : (uint64_t)B * p.S;
+    p.joins = p.extra && p.rows - B < (uint64_t)B ? (uint32_t)(p.rows - B) : (uint32_t)B;
+    return p;
 }
 
-size_t attn_decode_ws_bytes(int B, int Hq, int Hkv, int D, int max_len, int window) {
-    uint32_t S, want;
-    attn_decode_split(B, Hkv, max_len, window, &S, &want);
-    return S > 1 ? (size_t)B * S * Hq * (D + 2) * sizeof(float) : 0;
+size_t attn_decode_ws_bytes(int B, int Hq, int D, const AttnSplit& p) {
+    if (p.extra) return (p.rows + p.joins) * sizeof(int4) + p.rows * Hq * (D + 2) * sizeof(float);
+    return p.S > 1 ? p.rows * Hq * (D + 2) * sizeof(float) : 0;
 }
 
 // The tokens that a sequence's query sees, [start, len), cut into n parts of
-// `part` tokens (whole workgroup steps) from `base` on, and into no more than S
-// where the sequence is longer than expected.
+// `part` tokens (whole workgroup steps) from `base` on: of at most `scale` times
+// kMaxPart tokens if listed, else into no more than S where the sequence is longer
+// than expected.
 struct Span {
     int start, len, base, part, n;
 };
-BEAM_DEV Span span_of(const AttnDecodeArgs& a, int b) {
-    const int64_t cap = min((int64_t)a.max_pages << a.c.pshift, (int64_t)kMaxLen);
-    Span p;
-    p.len = (int)min((int64_t)max(a.lens[b], 0), cap);
-    p.start = a.window > 0 ? max(0, p.len - a.window) : 0;
+BEAM_DEV int table_tokens(const AttnDecodeArgs& a) {
+    return (int)min((int64_t)a.max_pages << a.c.pshift, (int64_t)kMaxLen);
+}
+BEAM_DEV void see(const AttnDecodeArgs& a, int len, Span& p) {
+    p.len = len;
+    p.start = a.window > 0 ? max(0, len - a.window) : 0;
     p.base = p.start & ~15;
+}
+template <bool LISTED> BEAM_DEV Span span_of(const AttnDecodeArgs& a, int cap, int len, uint32_t scale = 1) {
+    Span p;
+    see(a, min(max(len, 0), cap), p);
     const uint32_t all = (uint32_t)(p.len - p.base);
-    uint32_t part = (all + a.want - 1) / a.want;
-    part = min(max(part, (uint32_t)kMinPart), (uint32_t)kMaxPart);
-    if ((uint64_t)part * a.S < all) part = (all + a.S - 1) / a.S;
+    uint32_t part = (all + a.p.want - 1) / a.p.want;
+    part = min(max(part, (uint32_t)kMinPart), (uint32_t)kMaxPart * scale);
+    if (!LISTED && (uint64_t)part * a.p.S < all) part = (all + a.p.S - 1) / a.p.S;
     part = (part + kRound - 1) & ~(uint32_t)(kRound - 1);
     p.part = (int)part;
     p.n = (int)((all + part - 1) / part);
     return p;
+}
+
+// The list of all parts: those of the sequences in several parts, which take
+// longest, then the sequences in one (or without tokens).  Each has its sequence,
+// its number there, the sequence's length and the tokens per part; -1 stands
+// behind the last.  For the join: the sequences in several parts, their first
+// part and how many.  The lengths are summed in units of kMaxPart, which gives the
+// scale of the parts: with U units in all and scale m = ceil(U / extra), a
+// sequence of u units has at most want + u / m parts, so there are no more than
+// rows = B * want + extra.  One workgroup; the launch and its work take 3 to 5 us.
+constexpr int kListThreads = 1024;
+__global__ __launch_bounds__(kListThreads) void beam_attn_list(AttnDecodeArgs a) {
+    constexpr int kPer = kMostListed / kListThreads;   // neighbouring sequences of a thread
+    __shared__ int at[kMostListed], seq[kMostListed], sums[kListThreads / 64];
+    const int cap = table_tokens(a), tid = threadIdx.x;
+    const auto scan = [&](int v, int* total) {         // exclusive sum over the workgroup
+        int incl = v;
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1) {
+            const int u = __shfl_up(incl, o, kWave);
+            if ((tid & 63) >= o) incl += u;
+        }
+        __syncthreads();
+        if ((tid & 63) == 63) sums[tid >> 6] = incl;
+        __syncthreads();
+        int before = 0, all = 0;
+#pragma unroll
+        for (int i = 0; i < kListThreads / 64; ++i) {
+            before += i < (tid >> 6) ? sums[i] : 0;
+            all += sums[i];
+        }
+        *total = all;
+        return before + incl - v;
+    };
+    int len[kPer], units = 0, total;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        const int b = tid * kPer + i;
+        len[i] = b < a.B ? a.lens[b] : 0;
+        const Span p = span_of<true>(a, cap, len[i]);
+        units += (p.len - p.base + kMaxPart - 1) / kMaxPart;   // 2^18 at most, of 2^11 sequences
+    }
+    scan(units, &total);
+    const uint32_t scale = max(1u, min(((uint32_t)total + a.p.extra - 1) / a.p.extra, (uint32_t)(kMaxLen / kMaxPart)));
+
+    // sequences in several parts, and their parts in the upper bits: 2^11 and 2^13 at most
+    int n[kPer], many = 0;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        n[i] = span_of<true>(a, cap, len[i], scale).n;
+        if (n[i] > 1) many += (n[i] << 12) + 1;
+    }
+    int before = scan(many, &total);
+    const int parts = total >> 12, cut = total & 0xFFF;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        const int b = tid * kPer + i;
+        if (b >= a.B) continue;
+        const int k = before & 0xFFF, first = before >> 12;
+        if (n[i] > 1) {
+            at[k] = first;
+            seq[k] = b;
+            a.lists[k] = make_int4(b, first, n[i], 0);
+            before += (n[i] << 12) + 1;
+        } else {
+            const Span p = span_of<true>(a, cap, len[i], scale);
+            a.items[parts + b - k] = make_int4(b, 0, p.len, p.part);
+        }
+    }
+    __syncthreads();
+    for (int i = tid; i < (int)a.p.rows; i += kListThreads) {
+        if (i < parts) {
+            int lo = 0, hi = cut;                      // at[lo] <= i < at[hi]
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) / 2;
+                if (at[mid] <= i) lo = mid;
+                else hi = mid;
+            }
+            const Span p = span_of<true>(a, cap, a.lens[seq[lo]], scale);
+            a.items[i] = make_int4(seq[lo], i - at[lo], p.len, p.part);
+        } else if (i >= parts + a.B - cut) {
+            a.items[i] = make_int4(-1, 0, 0, 0);
+        }
+    }
+    for (int i = cut + tid; i < (int)a.p.joins; i += kListThreads) a.lists[i] = make_int4(-1, 0, 0, 0);
 }
 
 // four e4m3 codes to bf16 (exact): codes 0, 1 and codes 2, 3
@@ -202,7 +310,7 @@ template <int D, int QT> struct Acc {
 // per SIMD (64 queries on one head, e4m3: 61 -> 52 us; D = 256, 253 windows of 128,
 // e4m3: 51 -> 32 us); fp32 would spill there (129 -> 146 us), and else what the
 // compiler takes is best.
-template <int KIND, int D, int QT>
+template <int KIND, int D, int QT, bool LISTED>
 __global__ __launch_bounds__(256, KIND != A_F32 && (QT == 2 || D == 256) ? 2 : 1) void beam_attn_decode(AttnDecodeArgs a,
                                                                                          int qgroups) {
     constexpr int TILE = tile_tokens<KIND>(), NU = TILE / 16;   // 16-token blocks per step
@@ -223,7 +331,8 @@ __global__ __launch_bounds__(256, KIND != A_F32 && (QT == 2 || D == 256) ? 2 : 1
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int r = lane & 15, g = lane >> 4;
-    // Grid: (sequence, head) along x, parts along y.  Workgroups that differ in
+    // Grid: (sequence, head) along x, parts along y; (part, head) along x where
+    // parts are listed.  Workgroups that differ in
     // their query rows only follow each other on one XCD, so that its L2
     // serves the keys and values of all but the first.
     int bh = blockIdx.x, qg = 0;
@@ -232,9 +341,22 @@ __global__ __launch_bounds__(256, KIND != A_F32 && (QT == 2 || D == 256) ? 2 : 1
         qg = j % qgroups;
         bh = j / qgroups * 8 + (bh & 7);
     }
-    const int b = bh / a.Hkv, h = bh - b * a.Hkv, s = blockIdx.y, G = a.G;
-    if (b >= a.B) return;
-    const Span sp = span_of(a, b);
+    const int h = bh % a.Hkv, G = a.G;
+    int b = bh / a.Hkv, s = blockIdx.y;           // listed: the part's number in place of b
+    Span sp;
+    const size_t prow = LISTED ? b : (size_t)b * a.p.S + s;   // the part's row in the workspace
+    if (b >= (LISTED ? (int)a.p.rows : a.B)) return;
+    if constexpr (LISTED) {
+        const int4 item = a.items[b];
+        if (item.x < 0) return;
+        b = item.x;
+        s = item.y;
+        see(a, item.z, sp);
+        sp.part = item.w;
+        sp.n = (int)((uint32_t)(sp.len - sp.base + sp.part - 1) / (uint32_t)sp.part);
+    } else {
+        sp = span_of<false>(a, table_tokens(a), a.lens[b]);
+    }
     if (s > 0 && s >= sp.n) return;               // no tokens; part 0 of an empty row goes on
     const int t0 = sp.base + s * sp.part;
     const int t1 = s + 1 < sp.n ? t0 + sp.part : sp.len;
@@ -542,41 +664,50 @@ __global__ __launch_bounds__(256, KIND != A_F32 && (QT == 2 || D == 256) ? 2 : 1
                         make_uint2(pack_bf16x2(O.x * inv, O.y * inv), pack_bf16x2(O.z * inv, O.w * inv));
                 if (a.lse && d == 0) a.lse[(size_t)b * a.Hq + head] = L == 0.f ? -INFINITY : M * kLn2 + logf(L);
             } else {
-                const size_t pr = ((size_t)b * a.S + s) * a.Hq + head;
+                const size_t pr = prow * a.Hq + head;
                 *reinterpret_cast<float4*>(a.parts + pr * D + d) = O;
                 if (d == 0)
-                    *reinterpret_cast<float2*>(a.parts + (size_t)a.B * a.S * a.Hq * D + pr * 2) = make_float2(M, L);
+                    *reinterpret_cast<float2*>(a.parts + a.p.rows * a.Hq * D + pr * 2) = make_float2(M, L);
             }
         }
     }
 }
 
-// Join of a sequence's parts: a workgroup per (sequence, query head).  Groups
+// Join of a sequence's parts: a workgroup per (sequence, query head), or per
+// (listed sequence, query head).  Groups
 // of D/4 lanes take the parts in turn, kBatch at a time with all their loads
-// in flight (the first batch's before the number of parts is known: they lie
-// in the workspace whether written or not), each group with its own running
+// in flight (the first batch's before the number of parts is known, unless they
+// are listed: they lie in the workspace whether written or not), each group with its own running
 // maximum; the groups are joined through LDS in a fixed order.
-template <int KIND, int D>
+template <int KIND, int D, bool LISTED>
 __global__ __launch_bounds__(256) void beam_attn_join(AttnDecodeArgs a) {
     constexpr int LPR = D / 4, NG = 256 / LPR, kBatch = 4;
     __shared__ float sO[NG][D];
     __shared__ float sM[NG], sL[NG];
-    const int head = blockIdx.x % a.Hq, b = blockIdx.x / a.Hq;
-    const int grp = threadIdx.x / LPR, d = threadIdx.x % LPR * 4;
-    const float2* ml = reinterpret_cast<const float2*>(a.parts + (size_t)a.B * a.S * a.Hq * D);
-    const size_t first = (size_t)b * a.S * a.Hq + head;
+    const int head = blockIdx.x % a.Hq, grp = threadIdx.x / LPR, d = threadIdx.x % LPR * 4;
+    int b = blockIdx.x / a.Hq, last = (int)a.p.S - 1;
+    size_t row = (size_t)b * a.p.S;
+    if constexpr (LISTED) {
+        const int4 list = a.lists[b];
+        if (list.x < 0) return;
+        b = list.x;
+        row = list.y;
+        last = list.z - 1;
+    }
+    const float2* ml = reinterpret_cast<const float2*>(a.parts + a.p.rows * a.Hq * D);
+    const size_t first = row * a.Hq + head, result = (size_t)b * a.Hq + head;
     float2 v[kBatch];
     float4 o[kBatch];
     auto load = [&](int s0) {
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) {
-            const size_t pr = first + (size_t)min(s0 + k * NG, (int)a.S - 1) * a.Hq;
+            const size_t pr = first + (size_t)min(s0 + k * NG, last) * a.Hq;
             v[k] = ml[pr];
             o[k] = *reinterpret_cast<const float4*>(a.parts + pr * D + d);
         }
     };
     load(grp);
-    const int n = span_of(a, b).n;
+    const int n = LISTED ? last + 1 : span_of<false>(a, table_tokens(a), a.lens[b]).n;
     if (n <= 1) return;                           // its only part wrote the result
     float M = -INFINITY, L = 0.f;
     float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -622,20 +753,27 @@ __global__ __launch_bounds__(256) void beam_attn_join(AttnDecodeArgs a) {
         Ot = fmaf(e, sO[k][t], Ot);
     }
     const float res = Lt == 0.f ? 0.f : Ot / Lt;
-    const size_t at = (size_t)blockIdx.x * D + t;
+    const size_t at = result * D + t;
     if constexpr (KIND == A_F32) static_cast<float*>(a.out)[at] = res;
     else static_cast<uint16_t*>(a.out)[at] = f32_to_bf16(res);
-    if (a.lse && t == 0) a.lse[blockIdx.x] = Lt == 0.f ? -INFINITY : top * kLn2 + logf(Lt);
+    if (a.lse && t == 0) a.lse[result] = Lt == 0.f ? -INFINITY : top * kLn2 + logf(Lt);
 }
 
 template <int KIND, int D, int QT>
 static hipError_t launch_decode(const AttnDecodeArgs& a, hipStream_t st) {
     const int qgroups = (a.G + 16 * QT - 1) / (16 * QT);
-    const size_t bh = (size_t)a.B * a.Hkv;
+    const size_t bh = (a.p.extra ? a.p.rows : (size_t)a.B) * a.Hkv;
     const unsigned grid = (unsigned)(qgroups == 1 ? bh : (bh + 7) / 8 * 8 * qgroups);
-    const hipError_t err = launch(beam_attn_decode<KIND, D, QT>, dim3(grid, a.S), dim3(256), st, a, qgroups);
-    if (err != hipSuccess || a.S == 1) return err;
-    return launch(beam_attn_join<KIND, D>, dim3((unsigned)((size_t)a.B * a.Hq)), dim3(256), st, a);
+    const dim3 heads((unsigned)((size_t)a.p.joins * a.Hq));
+    hipError_t err;
+    if (a.p.extra) {
+        err = launch(beam_attn_list, dim3(1), dim3(kListThreads), st, a);
+        if (err == hipSuccess) err = launch(beam_attn_decode<KIND, D, QT, true>, dim3(grid), dim3(256), st, a, qgroups);
+        return err == hipSuccess ? launch(beam_attn_join<KIND, D, true>, heads, dim3(256), st, a) : err;
+    }
+    err = launch(beam_attn_decode<KIND, D, QT, false>, dim3(grid, a.p.S), dim3(256), st, a, qgroups);
+    if (err != hipSuccess || a.p.S == 1) return err;
+    return launch(beam_attn_join<KIND, D, false>, heads, dim3(256), st, a);
 }
 
 // Above 16 queries per key-value head a wave takes 32 at once, so the cache
@@ -648,7 +786,13 @@ static hipError_t launch_decode_d(const AttnDecodeArgs& a, hipStream_t st) {
     return launch_decode<KIND, 256, 1>(a, st);
 }
 
-hipError_t launch_attn_decode(const AttnDecodeArgs& a, hipStream_t st) {
+hipError_t launch_attn_decode(AttnDecodeArgs a, void* ws, hipStream_t st) {
+    a.parts = static_cast<float*>(ws);
+    if (a.p.extra) {
+        a.items = static_cast<int4*>(ws);
+        a.lists = a.items + a.p.rows;
+        a.parts = reinterpret_cast<float*>(a.lists + a.p.joins);
+    }
     if (a.c.kind == A_F32) return launch_decode_d<A_F32>(a, st);
     if (a.c.kind == A_BF16) return launch_decode_d<A_BF16>(a, st);
     return launch_decode_d<A_FP8>(a, st);

@@ -220,7 +220,8 @@ beam_status beam_moe_kv_read(const beam_moe_attn_cfg* cfg, int32_t B, int32_t N,
 
 size_t beam_moe_attn_workspace_bytes(const beam_moe_attn_cfg* cfg, int32_t B, int32_t max_len) {
     if (check_attn_cfg(cfg) != BEAM_OK || B <= 0 || B > kMaxT || max_len < 0 || max_len > beam::kMaxLen) return 0;
-    return beam::attn_decode_ws_bytes(B, cfg->n_heads, cfg->n_kv_heads, cfg->head_dim, max_len, cfg->window);
+    return beam::attn_decode_ws_bytes(B, cfg->n_heads, cfg->head_dim,
+                                      beam::attn_decode_split(B, cfg->n_kv_heads, max_len, cfg->window));
 }
 
 beam_status beam_moe_attn_decode(const beam_moe_attn_cfg* cfg, int32_t B, const void* q, int64_t q_stride,
@@ -242,10 +243,9 @@ beam_status beam_moe_attn_decode(const beam_moe_attn_cfg* cfg, int32_t B, const 
     if ((a.c.kind == beam::A_F32) != (dtype == BEAM_F32)) return BEAM_ERR_UNSUPPORTED;
     const size_t es = dtype == BEAM_BF16 ? 2 : 4;
     if (overlap(out, (size_t)B * qw * es, q, span_bytes(B, q_stride, qw, es))) return BEAM_ERR_INVALID_ARG;
-    beam::attn_decode_split(B, cfg->n_kv_heads, max_len, cfg->window, &a.S, &a.want);
-    if ((int64_t)B * a.S * cfg->n_heads > kMaxParts) return BEAM_ERR_UNSUPPORTED;
-    const size_t need = beam::attn_decode_ws_bytes(B, cfg->n_heads, cfg->n_kv_heads, cfg->head_dim, max_len,
-                                                   cfg->window);
+    a.p = beam::attn_decode_split(B, cfg->n_kv_heads, max_len, cfg->window);
+    if ((int64_t)a.p.rows * cfg->n_heads > kMaxParts) return BEAM_ERR_UNSUPPORTED;
+    const size_t need = beam::attn_decode_ws_bytes(B, cfg->n_heads, cfg->head_dim, a.p);
     if (need > 0 && (!ws || ws_bytes < need || !aligned16(ws))) return BEAM_ERR_WORKSPACE;
     a.B = B;
     a.Hq = cfg->n_heads;
@@ -261,8 +261,7 @@ beam_status beam_moe_attn_decode(const beam_moe_attn_cfg* cfg, int32_t B, const 
     a.lens = seq_lens;
     a.out = out;
     a.lse = lse;
-    a.parts = static_cast<float*>(ws);
-    return ran(beam::launch_attn_decode(a, static_cast<hipStream_t>(stream)));
+    return ran(beam::launch_attn_decode(a, ws, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -177,22 +177,33 @@ constexpr int kMaxReadRows = 1 << 26;   // rows read back per call
 int kv_read_rows(int N, int Hkv, int D);   // output rows of a workgroup
 hipError_t launch_kv_read(const KvReadArgs& a, hipStream_t st);
 
+// How decode cuts sequences into parts (attn_decode_split).
+struct AttnSplit {
+    uint32_t S, want;       // most parts a sequence can have, parts wanted
+    uint32_t extra;         // 0: S parts per sequence in the grid; else the parts are listed, B * want + extra of them
+    uint32_t joins;         // sequences that the join looks at
+    uint64_t rows;          // part rows of the workspace
+};
+
 struct AttnDecodeArgs {
     int B, Hq, Hkv, G, D, max_pages, window;   // G = Hq / Hkv
-    uint32_t S, want;       // most parts a sequence can have, parts wanted (attn_decode_split)
     float scale;
     const void* q;
     size_t qs;
     const int32_t* table;
     const int32_t* lens;
+    AttnSplit p;
+    KvCache c;
     void* out;
     float* lse;
-    float* parts;           // workspace, S > 1: [B, S, Hq, D] sums, then [B, S, Hq] (max, sum) pairs
-    KvCache c;
+    // workspace (attn_decode_ws_bytes):
+    float* parts;           // [rows, Hq, D] sums, [rows, Hq] (max, sum) pairs
+    int4* items;            // [rows], listed parts only: sequence, number in it, its length, tokens per part
+    int4* lists;            // [joins], listed parts only: sequence, first row, number of parts
 };
 constexpr int kMaxLen = 1 << 30;   // longest sequence attn_decode counts
-void attn_decode_split(int B, int Hkv, int max_len, int window, uint32_t* S, uint32_t* want);
-size_t attn_decode_ws_bytes(int B, int Hq, int Hkv, int D, int max_len, int window);
-hipError_t launch_attn_decode(const AttnDecodeArgs& a, hipStream_t st);
+AttnSplit attn_decode_split(int B, int Hkv, int max_len, int window);
+size_t attn_decode_ws_bytes(int B, int Hq, int D, const AttnSplit& p);
+hipError_t launch_attn_decode(AttnDecodeArgs a, void* ws, hipStream_t st);
 
 }  // namespace beam

@@ -521,11 +521,15 @@ beam_status beam_moe_kv_read(const beam_moe_attn_cfg* cfg, int32_t B, int32_t N,
  *   max_len  the longest length to expect, 0 .. 2^30: it sizes the grid and
  *          the workspace.  Results hold for longer ones too, more slowly; too
  *          large a value costs little, since a sequence is split by its own
- *          length.  At most 2^23 sequences times query heads times parts
- *          (BEAM_ERR_UNSUPPORTED).
- *   ws     beam_moe_attn_workspace_bytes(cfg, B, max_len) bytes, 16-byte
- *          aligned (may be null where that is 0); its contents need no
- *          initialisation, and calls that overlap in time must not share it.
+ *          length, into even parts of 256 to 4096 tokens.  Parts are longer only
+ *          where the lengths together ask for more than some 4096 / n_kv_heads
+ *          of them, and with more than 2048 sequences, each of which is cut
+ *          into at most max(1, 4096 / (B * n_kv_heads)).  At most 2^23
+ *          sequences times query heads times parts (BEAM_ERR_UNSUPPORTED).
+ *   ws     beam_moe_attn_workspace_bytes(cfg, B, max_len) bytes for this B
+ *          and max_len (a larger B may need fewer), 16-byte aligned (may be
+ *          null where that is 0); its contents need no initialisation, and
+ *          calls that overlap in time must not share it.
  */
 beam_status beam_moe_attn_decode(const beam_moe_attn_cfg* cfg, int32_t B, const void* q, int64_t q_stride,
                                  beam_dtype dtype, const beam_moe_kv_cache* cache,

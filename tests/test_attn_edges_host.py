@@ -118,3 +118,18 @@ def test_a_workspace_is_not_cut_to_32_bits(B, max_len):
     with pytest.raises(ValueError):
         beam.attn_workspace(beam.AttnCfg(), B, max_len, device="cpu")
     assert beam.attn_workspace(beam.AttnCfg(window=0), 1, 131072, device="cpu").numel() > 256
+
+
+# ------------------------------------------------------------------ parts of long sequences
+
+@pytest.mark.parametrize("hq,hkv", [(48, 8), (8, 8), (64, 1), (32, 32)])
+@pytest.mark.parametrize("B", [2, 65, 257, 300, 1000, 2047, 2048])
+def test_a_long_sequence_among_many_can_be_cut(hq, hkv, B):
+    """However many sequences beside it, up to 2048: there is a workspace for
+    parts, and it does not grow as sequences times parts."""
+    L = beam.lib()
+    cfg = beam.AttnCfg(n_heads=hq, n_kv_heads=hkv, window=0)
+    rows = L.beam_moe_attn_workspace_bytes(cfg.c(), B, 131072) / (hq * 130 * 4)
+    assert rows >= B + 31                                   # one of 131072 tokens in parts of 4096, the rest whole
+    assert rows <= 4096 + 512 + B + 1
+    assert L.beam_moe_attn_workspace_bytes(cfg.c(), B, 1 << 30) > 0

@@ -304,3 +304,123 @@ def test_lengths_to_expect_beyond_the_limit(max_len, native):
                                   s["lse"], **kw)
     torch.cuda.synchronize()
     assert (s["out"] == 3).all()
+
+
+# ------------------------------------------------------------------ long sequences among many
+
+def exact_decode(cfg, q, vals, table, lens):
+    """fp64 (out, magnitude, lse) on the GPU, and the bound on a score."""
+    B, hq, D = q.shape
+    hkv, P = cfg.n_kv_heads, cfg.page_size
+    out, mag = (torch.zeros((B, hq, D), dtype=torch.float64, device=DEV) for _ in range(2))
+    lse = torch.full((B, hq), -float("inf"), dtype=torch.float64, device=DEV)
+    Z = torch.zeros(B, dtype=torch.float64, device=DEV)
+    k, v = vals
+    for b, n in enumerate(lens):
+        if n == 0:
+            continue
+        t = torch.arange(max(0, n - cfg.window) if cfg.window else 0, n, device=DEV)
+        page = table[b].long()[t // P]
+        kr, vr = (x[page, :, t % P].transpose(0, 1).contiguous() for x in (k, v))          # [hkv, n, D]
+        qb = q[b].double().view(hkv, hq // hkv, D)
+        z = cfg.softmax_scale * torch.matmul(qb, kr.transpose(1, 2).contiguous())
+        w = torch.softmax(z, -1)
+        out[b], mag[b] = (torch.matmul(w, x).view(hq, D) for x in (vr, vr.abs()))
+        lse[b] = torch.logsumexp(z, -1).view(hq)
+        Z[b] = cfg.softmax_scale * torch.matmul(qb.abs(), kr.abs().transpose(1, 2).contiguous()).max()
+    return out, mag, lse, Z
+
+
+def pages_for(lens, P, n_pages, seed):
+    """Any pages, shared by all."""
+    width = max(1, -(-max(lens) // P))
+    return torch.randint(0, n_pages, (len(lens), width), generator=base.gen(seed), device=DEV, dtype=torch.int32)
+
+
+MANY = {
+    "long first": lambda r: [20001] + [int(x) for x in r.integers(0, 300, 90)],
+    "long last": lambda r: [int(x) for x in r.integers(0, 300, 300)] + [33000],
+    "long in the middle, empty ones": lambda r: [0] * 40 + [5000, 0, 4097, 0, 4096] + [0] * 40,
+    "all long": lambda r: [int(x) for x in r.integers(4000, 9000, 70)],
+    "two": lambda r: [9000, 130],
+    "most": lambda r: [int(x) for x in r.integers(0, 40, 2047)] + [8200],
+    "all empty": lambda r: [0] * 100,
+}
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp8", "f32"])
+@pytest.mark.parametrize("name,hq,hkv,D,window,max_len", [
+    ("long first", 8, 8, 128, 0, 131072), ("long first", 48, 8, 64, 10000, 1 << 20), ("long last", 16, 8, 128, 0, 131072),
+    ("long last", 40, 2, 256, 0, 1 << 20), ("long in the middle, empty ones", 16, 16, 64, 0, 131072),
+    ("all long", 64, 64, 64, 0, 131072), ("all long", 64, 1, 128, 0, 1 << 20), ("two", 64, 1, 64, 0, 1 << 30),
+    ("most", 2, 2, 64, 0, 131072), ("all empty", 8, 8, 64, 0, 131072),
+])
+def test_decode_of_listed_parts(kind, name, hq, hkv, D, window, max_len):
+    """Batches whose parts are listed: one or all long, at any place, more
+    parts than are listed at their usual size, query heads in several groups."""
+    say(f"listed parts {kind} {name} {hq}/{hkv} D={D} expected {max_len}")
+    lens = MANY[name](np.random.default_rng(7))
+    B, P, n_pages = len(lens), 256, 9
+    cfg = beam.AttnCfg(hq, hkv, D, 0, False, window, P, softmax_scale=D ** -0.5)
+    c, vals = base.filled(cfg, n_pages, kind, 31)
+    vals = [torch.tensor(x, device=DEV) for x in vals]
+    table = pages_for(lens, P, n_pages, 3)
+    q = (2 * torch.randn((B, hq, D), generator=base.gen(5), device=DEV)).to(base.ACT["f32" if kind == "f32" else "bf16"])
+    out, lse = torch.full(q.shape, 9.0, dtype=q.dtype, device=DEV), torch.full((B, hq), 9.0, device=DEV)
+    ws = beam.attn_workspace(cfg, B, max_len)
+    ws.fill_(0xFF)                                         # its contents do not matter
+    beam.beam_moe_attn_decode(cfg, q, c, table, i32(lens), max_len, out, ws, lse)
+    torch.cuda.synchronize()
+    ro, mag, rl, Z = exact_decode(cfg, q, vals, table, lens)
+    u, n = base.U, torch.tensor(lens, device=DEV).double()
+    e, cu = (D / 4 + 8) * u * Z, (n / 32 + 64) * u
+    weight = 0.0 if kind == "f32" else 2.0 ** -15 + 2 * u
+    bound = (weight + 2 * e + cu)[:, None, None] * mag + base.HALF[q.dtype] * ro.abs()
+    over = ((out.double() - ro).abs() - bound).max().item()
+    say(f"  over the bound by {over:.2e}")
+    assert over <= 0
+    some = n > 0
+    assert torch.isneginf(lse[~some]).all() and (out[~some] == 0).all()
+    assert ((lse.double() - rl).abs()[some] <= ((e + cu)[:, None] + u * rl.abs())[some]).all()
+    again = torch.empty_like(out)
+    beam.beam_moe_attn_decode(cfg, q, c, table, i32(lens), max_len, again, ws, lse)
+    torch.cuda.synchronize()
+    assert torch.equal(out, again)
+
+
+def test_listed_parts_in_a_graph_and_on_two_streams():
+    """A captured call replayed with other lengths, and two calls at once with
+    a workspace each, give the eager bits."""
+    cfg = beam.AttnCfg(16, 8, 128, 0, False, 0, 64)
+    B, n_pages, max_len = 80, 30, 131072
+    c, _ = base.filled(cfg, n_pages, "fp8", 3)
+    r = np.random.default_rng(5)
+    batches = [[int(x) for x in r.integers(0, 500, B)] for _ in range(3)]
+    batches[0][79], batches[1][0], batches[2][40] = 12000, 9000, 1
+    table = pages_for([12000] * B, 64, n_pages, 1)
+    q = torch.randn((B, 16, 128), generator=base.gen(2), device=DEV).bfloat16()
+    ws = [beam.attn_workspace(cfg, B, max_len) for _ in range(2)]
+    out, lens = torch.empty_like(q), i32(batches[0])
+    eager = []
+    for x in batches:
+        lens.copy_(i32(x))
+        beam.beam_moe_attn_decode(cfg, q, c, table, lens, max_len, out, ws[0])
+        eager.append(out.clone())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        beam.beam_moe_attn_decode(cfg, q, c, table, lens, max_len, out, ws[0])
+    for i in (0, 1, 2, 1, 0):
+        lens.copy_(i32(batches[i]))
+        out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, eager[i])
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    outs, ls = [torch.empty_like(q) for _ in range(2)], [i32(batches[i]) for i in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for i in range(2):
+            beam.beam_moe_attn_decode(cfg, q, c, table, ls[i], max_len, outs[i], ws[i], stream=streams[i])
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert torch.equal(outs[i], eager[i])
