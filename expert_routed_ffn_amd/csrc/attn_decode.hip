@@ -56,13 +56,13 @@ template <int KIND> constexpr int tile_tokens() { return KIND == A_F32 ? 16 : 32
 // wherever they are needed, and parts grow beyond kMaxPart, to the same multiple
 // for all sequences, only where the lengths together ask for more.  Cut to S
 // parts instead, one long sequence among many runs on its own (e4m3, 131072
-// tokens beside 300 sequences of 512: 1061 us, listed 112; beside 1000: 1181 and
-// 250; 256 sequences of 1 .. 32768: 981 and 964), while without long ones the list
-// is 2 to 4 % (64 sequences of 2048, 131072 expected: 46.3 us and 48.3; 2000 of
-// 512: 363 and 378) and at worst its launch (64 of 512: 18.3 and 20.1).  Above
-// kMostListed sequences there are workgroups enough to run beside a long one
-// for most of its time, and S is cut.
-constexpr int kWantWG = 512, kMostWG = 4096, kMinPart = 256, kMaxPart = 4096, kRound = 128, kMostListed = 2048;
+// tokens beside 300 sequences of 512: 1061 us, listed 108; beside 1000: 1181 and
+// 250; 256 sequences of 1 .. 32768: 981 and 963), while without long ones the list
+// is 2 to 4 % (64 sequences of 2048, 131072 expected: 46.3 us and 48.2; 2000 of
+// 512: 363 and 376) and at worst its launch (64 of 512: 18.3 and 19.7).  From
+// kMostListed sequences on there are workgroups enough without parts, and each
+// is one: a long one among them ends by itself.
+constexpr int kWantWG = 512, kMostWG = 4096, kMinPart = 256, kMaxPart = 4096, kRound = 128, kMostListed = 4096;
 AttnSplit attn_decode_split(int B, int Hkv, int max_len, int window) {
     // a window's tokens begin inside a 16-token block
     const int64_t span = window > 0 && window < max_len ? (int64_t)window + 15 : max_len;
@@ -75,7 +75,7 @@ AttnSplit attn_decode_split(int B, int Hkv, int max_len, int window) {
     AttnSplit p;
     p.want = (uint32_t)w;
     p.S = (uint32_t)(s < cap ? s : cap);
-    p.extra = cap < parts(kMaxPart) && B > 1 && B <= kMostListed ? (uint32_t)at_least_1(kMostWG / Hkv) : 0;
+    p.extra = cap < parts(kMaxPart) && B > 1 && B < kMostListed ? (uint32_t)at_least_1(kMostWG / Hkv) : 0;
     p.rows = p.extra ? (uint64_t)B * p.want + p.extra : (uint64_t)B * p.S;
     p.joins = p.extra && p.rows - B < (uint64_t)B ? (uint32_t)(p.rows - B) : (uint32_t)B;
     return p;
@@ -124,7 +124,8 @@ template <bool LISTED> BEAM_DEV Span span_of(const AttnDecodeArgs& a, int cap, i
 // rows = B * want + extra.  One workgroup; the launch and its work take 3 to 5 us.
 constexpr int kListThreads = 1024;
 __global__ __launch_bounds__(kListThreads) void beam_attn_list(AttnDecodeArgs a) {
-    constexpr int kPer = kMostListed / kListThreads;   // neighbouring sequences of a thread
+    constexpr int kPer = kMostListed / kListThreads;
+    const int per = (a.B + kListThreads - 1) / kListThreads;   // neighbouring sequences of a thread
     __shared__ int at[kMostListed], seq[kMostListed], sums[kListThreads / 64];
     const int cap = table_tokens(a), tid = threadIdx.x;
     const auto scan = [&](int v, int* total) {         // exclusive sum over the workgroup
@@ -149,18 +150,20 @@ __global__ __launch_bounds__(kListThreads) void beam_attn_list(AttnDecodeArgs a)
     int len[kPer], units = 0, total;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-        const int b = tid * kPer + i;
+        if (i >= per) break;
+        const int b = tid * per + i;
         len[i] = b < a.B ? a.lens[b] : 0;
         const Span p = span_of<true>(a, cap, len[i]);
-        units += (p.len - p.base + kMaxPart - 1) / kMaxPart;   // 2^18 at most, of 2^11 sequences
+        units += (p.len - p.base + kMaxPart - 1) / kMaxPart;   // 2^18 at most, of 2^12 sequences
     }
     scan(units, &total);
     const uint32_t scale = max(1u, min(((uint32_t)total + a.p.extra - 1) / a.p.extra, (uint32_t)(kMaxLen / kMaxPart)));
 
-    // sequences in several parts, and their parts in the upper bits: 2^11 and 2^13 at most
+    // sequences in several parts, and their parts in the upper bits: fewer than 2^12 and 2^13
     int n[kPer], many = 0;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
+        if (i >= per) break;
         n[i] = span_of<true>(a, cap, len[i], scale).n;
         if (n[i] > 1) many += (n[i] << 12) + 1;
     }
@@ -168,8 +171,8 @@ __global__ __launch_bounds__(kListThreads) void beam_attn_list(AttnDecodeArgs a)
     const int parts = total >> 12, cut = total & 0xFFF;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-        const int b = tid * kPer + i;
-        if (b >= a.B) continue;
+        const int b = tid * per + i;
+        if (i >= per || b >= a.B) break;
         const int k = before & 0xFFF, first = before >> 12;
         if (n[i] > 1) {
             at[k] = first;

@@ -507,8 +507,9 @@ beam_status beam_moe_kv_read(const beam_moe_attn_cfg* cfg, int32_t B, int32_t N,
  *   out = sum_j softmax(z)_j v_j,   lse = log sum_j exp(z_j)
  * Sums, maxima and the join of the parts are fp32; with a BF16 or FP8_E4M3
  * cache a probability (times the value row's scale) enters the matrix cores as
- * two bf16 parts, off by 2^-15 of it at most.  Values are summed before the division by the
- * probabilities' sum: magnitudes beyond 2^96 may overflow there.
+ * two bf16 parts, off by 2^-15 of it at most.  Values are summed before the
+ * division by the probabilities' sum: magnitudes beyond 2^96 may overflow
+ * there.
  *   q      [B, n_heads, D] dtype, rows q_stride apart; out [B, n_heads, D]
  *          dtype, dense, must not overlap q.  dtype is BF16 for a BF16 or
  *          FP8_E4M3 cache and F32 for an F32 one.
@@ -523,9 +524,8 @@ beam_status beam_moe_kv_read(const beam_moe_attn_cfg* cfg, int32_t B, int32_t N,
  *          large a value costs little, since a sequence is split by its own
  *          length, into even parts of 256 to 4096 tokens.  Parts are longer only
  *          where the lengths together ask for more than some 4096 / n_kv_heads
- *          of them, and with more than 2048 sequences, each of which is cut
- *          into at most max(1, 4096 / (B * n_kv_heads)).  At most 2^23
- *          sequences times query heads times parts (BEAM_ERR_UNSUPPORTED).
+ *          of them; 4096 sequences and more are not cut.  At most 2^23
+ *          query heads times parts (BEAM_ERR_UNSUPPORTED).
  *   ws     beam_moe_attn_workspace_bytes(cfg, B, max_len) bytes for this B
  *          and max_len (a larger B may need fewer), 16-byte aligned (may be
  *          null where that is 0); its contents need no initialisation, and

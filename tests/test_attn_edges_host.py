@@ -123,9 +123,9 @@ def test_a_workspace_is_not_cut_to_32_bits(B, max_len):
 # ------------------------------------------------------------------ parts of long sequences
 
 @pytest.mark.parametrize("hq,hkv", [(48, 8), (8, 8), (64, 1), (32, 32)])
-@pytest.mark.parametrize("B", [2, 65, 257, 300, 1000, 2047, 2048])
+@pytest.mark.parametrize("B", [2, 65, 257, 300, 1000, 2047, 2048, 4095])
 def test_a_long_sequence_among_many_can_be_cut(hq, hkv, B):
-    """However many sequences beside it, up to 2048: there is a workspace for
+    """However many sequences beside it, below 4096: there is a workspace for
     parts, and it does not grow as sequences times parts."""
     L = beam.lib()
     cfg = beam.AttnCfg(n_heads=hq, n_kv_heads=hkv, window=0)

@@ -343,7 +343,8 @@ MANY = {
     "long in the middle, empty ones": lambda r: [0] * 40 + [5000, 0, 4097, 0, 4096] + [0] * 40,
     "all long": lambda r: [int(x) for x in r.integers(4000, 9000, 70)],
     "two": lambda r: [9000, 130],
-    "most": lambda r: [int(x) for x in r.integers(0, 40, 2047)] + [8200],
+    "most": lambda r: [int(x) for x in r.integers(0, 40, 4094)] + [8200],
+    "one more": lambda r: [int(x) for x in r.integers(0, 40, 4095)] + [8200],
     "all empty": lambda r: [0] * 100,
 }
 
@@ -353,7 +354,7 @@ MANY = {
     ("long first", 8, 8, 128, 0, 131072), ("long first", 48, 8, 64, 10000, 1 << 20), ("long last", 16, 8, 128, 0, 131072),
     ("long last", 40, 2, 256, 0, 1 << 20), ("long in the middle, empty ones", 16, 16, 64, 0, 131072),
     ("all long", 64, 64, 64, 0, 131072), ("all long", 64, 1, 128, 0, 1 << 20), ("two", 64, 1, 64, 0, 1 << 30),
-    ("most", 2, 2, 64, 0, 131072), ("all empty", 8, 8, 64, 0, 131072),
+    ("most", 2, 2, 64, 0, 131072), ("one more", 2, 2, 64, 0, 131072), ("all empty", 8, 8, 64, 0, 131072),
 ])
 def test_decode_of_listed_parts(kind, name, hq, hkv, D, window, max_len):
     """Batches whose parts are listed: one or all long, at any place, more
