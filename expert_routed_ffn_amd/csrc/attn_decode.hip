@@ -235,16 +235,16 @@ BEAM_DEV f32x4 mfma_bf16(uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uin
 // Eight weights as the sum of two bf16 operands: the leading 8 bits, and what
 // is left of each, rounded, so that a weight is off by 2^-15 at most.  One
 // rounded operand does not cancel against the softmax's sum, so that equal
-// values came back as their neighbours; the second product is mostly hidden
-// behind HBM (one sequence of 131071: 89.1 -> 89.6 us; 64 windows of 512, e4m3:
-// 12.6 -> 12.9).  A remainder of zero becomes 2^-24 of the weight: zero times an
-// infinite value would be NaN.
+// values came back as their neighbours.  Most of the second product hides behind
+// HBM (e4m3, one sequence of 131071: 45.1 us with and without; 64 of 8192: 179 ->
+// 181; 64 windows of 512: 13.1 -> 13.4), least where 64 queries share a head (64
+// sequences of 8192: e4m3 47 -> 52, bf16 61 -> 64).  The 2^-24 of the weight
+// keep the rest from being zero, which times an infinite value would be NaN.
 BEAM_DEV void split_bf16(const float (&y)[8], uint4& hi, uint4& lo) {
     float r[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const float left = y[i] - __uint_as_float(__float_as_uint(y[i]) & 0xFFFF0000u);
-        r[i] = left == 0.f ? y[i] * 0x1p-24f : left;
+        r[i] = fmaf(y[i], 0x1p-24f, y[i] - __uint_as_float(__float_as_uint(y[i]) & 0xFFFF0000u));
     }
     const auto top = [&](int i) {
         return __builtin_amdgcn_perm(__float_as_uint(y[i + 1]), __float_as_uint(y[i]), 0x07060302u);
