@@ -425,3 +425,46 @@ def test_listed_parts_in_a_graph_and_on_two_streams():
     torch.cuda.synchronize()
     for i in range(2):
         assert torch.equal(outs[i], eager[i])
+
+
+# ------------------------------------------------------------------ norm
+
+def test_norm_factor_is_one_rounding_off():
+    """1 / sqrt(mean(x^2) + eps), seen through rows of a power of two so small
+    that eps alone counts: half a unit in the last place (and 2^-10 of one)."""
+    g = np.random.default_rng(8)
+    x = torch.full((1, 1, 64), 2.0 ** -30, device=DEV)
+    one, pos = torch.ones(64, device=DEV), i32([0])
+    eps = np.exp2(g.uniform(-8, 8, 400)).astype(np.float32)
+    outs = []
+    for e in eps:
+        cfg = beam.AttnCfg(1, 1, 64, 0, False, 0, 16, rms_eps=float(e))
+        q, k = torch.empty_like(x), torch.empty_like(x)
+        beam.beam_moe_qk_norm_rope(cfg, x, x, pos, q, k, None, one, one)
+        outs.append(torch.stack([q[0, 0], k[0, 0]]))
+    got = base.f64(torch.stack(outs)) * 2.0 ** 30
+    assert (got == got[:, :1, :1]).all()
+    want = 1 / np.sqrt(eps.astype(np.float64))
+    unit = 2.0 ** (np.floor(np.log2(want)) - 23)
+    off = np.abs(got[:, 0, 0] - want) / unit
+    say(f"  up to {off.max():.4f} units off")
+    assert (off <= 0.5 + 2.0 ** -10).all()
+
+
+@pytest.mark.parametrize("act", ["bf16", "f32"])
+def test_norm_of_extreme_rows(act):
+    """No epsilon: rows of zeros give NaN (0/0), rows far from 1 the formula's
+    values as long as their squares' mean is a normal float, and stay finite
+    beyond."""
+    cfg = beam.AttnCfg(6, 1, 64, 0, False, 0, 16, rms_eps=0.0)
+    q = torch.randn((1, 6, 64), generator=base.gen(6), device=DEV)
+    for h, size in enumerate((0.0, 1e-17, 1e-10, 1.0, 1e10, 1e17)):
+        q[0, h] *= size
+    q = q.to(base.ACT[act])
+    k = q[:, 3:4].contiguous() * 2.0 ** 66                  # squares overflow: a factor of 0
+    one = torch.ones(64, dtype=q.dtype, device=DEV)
+    qo, ko = torch.empty_like(q), torch.empty_like(k)
+    beam.beam_moe_qk_norm_rope(cfg, q, k, i32([0]), qo, ko, None, one, one)
+    torch.cuda.synchronize()
+    assert torch.isnan(qo[0, 0]).all() and (ko == 0).all()
+    base.check_rows("q", qo[:, 1:], base.rope_ref(cfg, q[:, 1:], one, i32([0]), None, False), base.HALF[q.dtype])
