@@ -468,3 +468,69 @@ def test_norm_of_extreme_rows(act):
     torch.cuda.synchronize()
     assert torch.isnan(qo[0, 0]).all() and (ko == 0).all()
     base.check_rows("q", qo[:, 1:], base.rope_ref(cfg, q[:, 1:], one, i32([0]), None, False), base.HALF[q.dtype])
+
+
+# ------------------------------------------------------------------ calls that the other tests leave out
+
+@pytest.mark.parametrize("kind", ["bf16", "fp8", "f32"])
+@pytest.mark.parametrize("window", [0, 700])
+def test_listed_parts_with_bad_pages_and_lengths(kind, window):
+    """Lengths below zero and beyond the table, pages outside the cache."""
+    P, n_pages, B = 64, 20, 70
+    cfg = beam.AttnCfg(16, 8, 64, 0, False, window, P)
+    c, vals = base.filled(cfg, n_pages, kind, 5)
+    r = np.random.default_rng(2)
+    table = r.integers(0, n_pages, (B, 90)).astype(np.int32)
+    lens = r.integers(0, 200, B)
+    lens[[0, 3, 20, 69]] = [-5, 1 << 30, 5760, -(1 << 31)]
+    lens[[7, 8]] = [(1 << 31) - 1, 5000]
+    table[3, ::3], table[7, 10:], table[8], table[20, 64:] = -1, n_pages, 1 << 30, -(1 << 31)
+    q = torch.randn((B, 16, 64), generator=base.gen(4), device=DEV).to(base.ACT["f32" if kind == "f32" else "bf16"])
+    base.check_decode(cfg, q, c, vals, table, [int(x) for x in lens], 131072, f"bad pages, listed, window {window}")
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp8"])
+def test_decode_of_as_many_key_value_heads_as_there_are(kind):
+    lens = [1, 40, 300]
+    cfg = beam.AttnCfg(256, 256, 64, 0, False, 0, 32, softmax_scale=0.125)
+    c, vals = base.filled(cfg, 13, kind, 5)
+    q = torch.randn((3, 256, 64), generator=base.gen(4), device=DEV).bfloat16()
+    base.check_decode(cfg, q, c, vals, base.tables(lens, 32, 13, 2), lens, 300, "256 key-value heads")
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32", "fp8"])
+def test_cached_form_in_place(kind):
+    """The queries normed and rotated where they are, idle rows among them."""
+    cfg = beam.AttnCfg(6, 2, 128, 64, False, 0, 16)
+    q, k, v, pos, gq, gk, f = base.rope_inputs(cfg, 19, "bf16", 5)
+    q = q.contiguous()
+    slots = torch.arange(19, dtype=torch.int32, device=DEV)
+    slots[4], slots[18] = -1, 1 << 20
+    a, b = (base.poisoned(cfg, 2, kind) for _ in range(2))
+    qo = torch.empty_like(q)
+    beam.beam_moe_qk_norm_rope_cache(cfg, q, k, v, pos, slots, qo, a, f, gq, gk)
+    beam.beam_moe_qk_norm_rope_cache(cfg, q, k, v, pos, slots, q, b, f, gq, gk)
+    torch.cuda.synchronize()
+    assert torch.equal(q, qo)
+    for x, y in ((a.k, b.k), (a.v, b.v), (a.k_scale, b.k_scale), (a.v_scale, b.v_scale)):
+        assert x is None or torch.equal(x.view(torch.uint8), y.view(torch.uint8))
+
+
+def test_empty_calls():
+    """No tokens, no sequences, no rows: nothing to do, and nothing refused."""
+    cfg = beam.AttnCfg(4, 2, 64, 0, False, 0, 16)
+    c, _ = base.filled(cfg, 2, "bf16", 1)
+    kept = c.k.clone()
+    q, k = (torch.empty((0, h, 64), dtype=torch.bfloat16, device=DEV) for h in (4, 2))
+    none, table = torch.empty(0, dtype=torch.int32, device=DEV), torch.empty((0, 3), dtype=torch.int32, device=DEV)
+    for kw in ({}, {"stream": torch.cuda.current_stream()}):
+        beam.beam_moe_qk_norm_rope(cfg, q, k, none, q.clone(), k.clone(), **kw)
+        beam.beam_moe_qk_norm_rope_cache(cfg, q, k, k, none, none, q.clone(), c, **kw)
+        beam.beam_moe_kv_write(cfg, k, k, none, c, **kw)
+        beam.beam_moe_kv_read(cfg, c, table, i32([0]), k.clone(), k.clone(), **kw)
+        beam.beam_moe_kv_read(cfg, c, i32([[0, 1]]), i32([0, 0]), k.clone(), k.clone(), **kw)
+        ko, vo = (torch.full((3, 2, 64), 5.0, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+        beam.beam_moe_kv_read(cfg, c, table, i32([0]), ko, vo, **kw)
+        beam.beam_moe_attn_decode(cfg, q, c, table, none, 100, q.clone(), None, **kw)
+        torch.cuda.synchronize()
+        assert torch.equal(c.k, kept) and (ko == 5).all() and (vo == 5).all()
