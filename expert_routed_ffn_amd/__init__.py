@@ -837,8 +837,9 @@ def attn_layer(cfg: AttnCfg, qkv, positions, slots, cache: KVCache, page_table, 
     [B, (n_heads + 2 n_kv_heads) * D] is the merged projection of the step's
     tokens; their keys and values go into the cache at `slots`, then every
     token attends to the seq_lens [B] tokens of its sequence, itself
-    included.  The result lands in bufs.out [B,n_heads,D]; its output
-    projection is the m of beam_moe_norm_boundary."""
+    included.  The result lands in bufs.out [B,n_heads,D].  Beam's output gate
+    is not applied: the caller multiplies it in before the output projection,
+    whose result is the m of beam_moe_norm_boundary."""
     B, hq, hkv, D = qkv.shape[0], cfg.n_heads, cfg.n_kv_heads, cfg.head_dim
     if qkv.shape != (B, (hq + 2 * hkv) * D):
         raise ValueError(f"qkv: shape {tuple(qkv.shape)} != {(B, (hq + 2 * hkv) * D)}")

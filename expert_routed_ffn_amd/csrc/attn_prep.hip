@@ -149,7 +149,7 @@ BEAM_DEV void store_cache(void* side, float* scales, size_t row, int e0, float (
 //   For a row x: y = R(x * gamma) * f, with f = 1/sqrt(mean(x^2) + eps) times
 // the position factor: the rotation R is linear, so both factors wait until
 // after it.  Bound by HBM where there are many tokens (16384 of 48 + 8 + 8 heads
-// of 128, bf16 into e4m3: 100 us, 5.0 TB/s; values and keys alone: 24 us, 4.2
+// of 128, bf16 into e4m3: 97 us, 5.2 TB/s; values and keys alone: 22.7 us, 4.5
 // TB/s; a copy reaches 4.7), by latency where there are few (64: 3.8 us).
 // ---------------------------------------------------------------------------
 template <bool BF, int CK, int D>
@@ -312,7 +312,7 @@ static hipError_t launch_prep(const AttnPrepArgs& a, hipStream_t st) {
     // groups per wave: one while that leaves the chip with few waves, more
     // once the waves suffice, which forms a token's cosines fewer times (16384
     // tokens of 16 groups into an 8-bit cache: 124 us at 131072 waves, 106 at
-    // 65536, 100 at 32768, 108 at 8192)
+    // 65536, 100 at 32768, 108 at 8192; no other size was swept)
     const int gpw = (int)min((int64_t)groups, max((int64_t)1, (int64_t)a.T * groups / kPrepWaves));
     const int wpt = (groups + gpw - 1) / gpw;
     const unsigned grid = (unsigned)(((size_t)a.T * wpt + 3) / 4);

@@ -385,8 +385,9 @@ size_t beam_moe_workspace_bytes(const beam_moe_cfg* cfg, int32_t T, beam_dtype w
  *  attention section: 48 query heads over 8 key-value heads of 128, a
  *  per-head RMSNorm of queries and keys, sliding windows of 512 with rotary
  *  positions or full attention without them and queries scaled by
- *  (1 + p/2048)^0.1.)  Its output, projected, is the m of
- *  beam_moe_norm_boundary; the boundary's x_next, projected, its input.
+ *  (1 + p/2048)^0.1.)  The boundary's x_next, projected, is its input; its
+ *  output, gated and projected by the caller, the m of
+ *  beam_moe_norm_boundary (no gate is applied here).
  *
  * The conventions at the top of this file hold.  In addition q, k and v of
  * the first three calls may be columns of a wider row-major matrix: each
