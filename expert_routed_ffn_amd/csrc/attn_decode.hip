@@ -14,7 +14,8 @@
 //
 // The cache's length is split over workgroups (parts) and over the four waves
 // of a workgroup (tiles in turn).  The waves' results are joined through LDS,
-// the parts' through the workspace by a second kernel.
+// the parts' through the workspace by a second kernel; a batch of more parts
+// than the grid holds for each sequence has them listed by one before.
 //
 // HBM bounds it: 2 flops per byte and query at most (e4m3) are far below what
 // the matrix cores give, with the padding of G to 16 columns and the second
@@ -336,9 +337,9 @@ __global__ __launch_bounds__(256, KIND != A_F32 && (QT == 2 || D == 256) ? 2 : 1
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int r = lane & 15, g = lane >> 4;
     // Grid: (sequence, head) along x, parts along y; (part, head) along x where
-    // parts are listed.  Workgroups that differ in
-    // their query rows only follow each other on one XCD, so that its L2
-    // serves the keys and values of all but the first.
+    // parts are listed.  Workgroups that differ in their query rows only follow
+    // each other on one XCD, so that its L2 serves the keys and values of all
+    // but the first.
     int bh = blockIdx.x, qg = 0;
     if (qgroups > 1) {
         const int j = bh >> 3;
@@ -678,11 +679,11 @@ __global__ __launch_bounds__(256, KIND != A_F32 && (QT == 2 || D == 256) ? 2 : 1
 }
 
 // Join of a sequence's parts: a workgroup per (sequence, query head), or per
-// (listed sequence, query head).  Groups
-// of D/4 lanes take the parts in turn, kBatch at a time with all their loads
-// in flight (the first batch's before the number of parts is known, unless they
-// are listed: they lie in the workspace whether written or not), each group with its own running
-// maximum; the groups are joined through LDS in a fixed order.
+// (listed sequence in several parts, query head).  Groups of D/4 lanes take the
+// parts in turn, kBatch at a time with all their loads in flight (without a list
+// the first batch's before the number of parts is known: they lie in the
+// workspace whether written or not), each group with its own running maximum;
+// the groups are joined through LDS in a fixed order.
 template <int KIND, int D, bool LISTED>
 __global__ __launch_bounds__(256) void beam_attn_join(AttnDecodeArgs a) {
     constexpr int LPR = D / 4, NG = 256 / LPR, kBatch = 4;
