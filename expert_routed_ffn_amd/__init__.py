@@ -35,7 +35,9 @@ SYMBOLS = ("beam_moe_route", "beam_moe_permute", "beam_moe_quantize_fp8", "beam_
            "beam_moe_permute_shard", "beam_moe_combine_partial", "beam_moe_dense_mlp",
            "beam_moe_dense_workspace_bytes", "beam_moe_pack_weights", "beam_moe_workspace_bytes",
            "beam_moe_status_string", "beam_moe_qk_norm_rope", "beam_moe_qk_norm_rope_cache", "beam_moe_kv_write",
-           "beam_moe_kv_read", "beam_moe_attn_decode", "beam_moe_attn_workspace_bytes")
+           "beam_moe_kv_read", "beam_moe_attn_decode", "beam_moe_attn_workspace_bytes", "beam_moe_attn_decode_sinks",
+           "beam_moe_attn_decode_sinks_workspace_bytes", "beam_moe_attn_prompt",
+           "beam_moe_attn_prompt_workspace_bytes")
 STATIC_SCRATCH_BYTES = 64 << 20   # BEAM_MOE_STATIC_SCRATCH_BYTES
 
 
@@ -90,7 +92,8 @@ class BeamMoeKvCache(ctypes.Structure):
 class AttnCfg:
     """Shape of one attention sublayer.  Beam defaults: a rotary
     sliding-window layer.  Its full-attention layers have rope_dim=0,
-    window=0 and ssmax_len=2048."""
+    window=0 and ssmax_len=2048.  sinks: first tokens of a sequence that stay
+    visible beside a window."""
     n_heads: int = 48
     n_kv_heads: int = 8
     head_dim: int = 128
@@ -102,8 +105,10 @@ class AttnCfg:
     ssmax_exp: float = 0.1
     softmax_scale: float = 128 ** -0.5
     rms_eps: float = 1e-6
+    sinks: int = 0
 
     def __post_init__(self):
+        _i32(self.sinks, "sinks")
         c = BeamMoeAttnCfg(_i32(self.n_heads, "n_heads"), _i32(self.n_kv_heads, "n_kv_heads"),
                            _i32(self.head_dim, "head_dim"), _i32(self.rope_dim, "rope_dim"),
                            _i32(int(self.rope_interleaved), "rope_interleaved"), _i32(self.window, "window"),
@@ -161,13 +166,21 @@ def lib() -> ctypes.CDLL:
     L.beam_moe_attn_decode.argtypes = [acfgp, i32, vp, i64, i32, cachep, vp, i32, vp, i32, vp, vp, vp, sz, vp]
     L.beam_moe_attn_workspace_bytes.argtypes = [acfgp, i32, i32]
     L.beam_moe_attn_workspace_bytes.restype = sz
+    L.beam_moe_attn_decode_sinks.argtypes = [acfgp, i32, i32, vp, i64, i32, cachep, vp, i32, vp, i32, vp, vp, vp, sz,
+                                             vp]
+    L.beam_moe_attn_decode_sinks_workspace_bytes.argtypes = [acfgp, i32, i32, i32]
+    L.beam_moe_attn_decode_sinks_workspace_bytes.restype = sz
+    L.beam_moe_attn_prompt.argtypes = [acfgp, i32, i32, i32, vp, i64, i32, cachep, vp, i32, vp, vp, i32, vp, vp, vp,
+                                       sz, vp]
+    L.beam_moe_attn_prompt_workspace_bytes.argtypes = [acfgp, i32, i32, i32, i32]
+    L.beam_moe_attn_prompt_workspace_bytes.restype = sz
     L.beam_moe_status_string.argtypes = [i32]
     L.beam_moe_status_string.restype = ctypes.c_char_p
     for f in ("beam_moe_route", "beam_moe_permute", "beam_moe_quantize_mx", "beam_moe_experts",
               "beam_moe_experts_static", "beam_moe_combine_norm", "beam_moe_norm_boundary",
               "beam_moe_permute_shard", "beam_moe_combine_partial", "beam_moe_dense_mlp",
               "beam_moe_pack_weights", "beam_moe_qk_norm_rope", "beam_moe_qk_norm_rope_cache", "beam_moe_kv_write",
-              "beam_moe_kv_read", "beam_moe_attn_decode"):
+              "beam_moe_kv_read", "beam_moe_attn_decode", "beam_moe_attn_decode_sinks", "beam_moe_attn_prompt"):
         getattr(L, f).restype = i32
     _lib = L
     return L
@@ -586,6 +599,8 @@ def _marshal():
     at = [ctypes.cast(getattr(L, "beam_moe_" + f), ctypes.c_void_p).value
           for f in ("qk_norm_rope", "qk_norm_rope_cache", "kv_write", "kv_read", "attn_decode")]
     _bind.bind(api, int(torch.empty(0, device="cuda").__dlpack_device__()[0]), *at, BeamError)
+    _bind.bind_more(*(ctypes.cast(getattr(L, "beam_moe_" + f), ctypes.c_void_p).value
+                      for f in ("attn_decode_sinks", "attn_prompt")))
     _native = _bind
     return _bind
 
@@ -652,8 +667,10 @@ def _launch(fn, dev, stream, *args):
 class KVCache:
     """The paged key-value cache of one layer: k, v [n_pages, n_kv_heads,
     page_size, head_dim] in bf16, fp32 or e4m3 codes (float8_e4m3fn or
-    uint8); the codes with fp32 scales [n_pages, n_kv_heads, page_size].  The
-    tensors are checked here, once, and must keep their storage."""
+    uint8); the codes with fp32 scales [n_pages, n_kv_heads, page_size].  In 4
+    bits (MXFP4): uint8 [n_pages, n_kv_heads, page_size, head_dim/2], two E2M1
+    codes a byte, with uint8 E8M0 scales [.., head_dim/32].  The tensors are
+    checked here, once, and must keep their storage."""
     k: torch.Tensor
     v: torch.Tensor
     k_scale: torch.Tensor | None = None
@@ -671,15 +688,20 @@ class KVCache:
         kp = _on(dev, k, k.shape, k.dtype, "k")
         vp = _on(dev, v, k.shape, k.dtype, "v")
         ks = vs = None
+        page, code = tuple(k.shape[1:]), _dt(k)
         if k.dtype in _CODES:
             if self.k_scale is None or self.v_scale is None:
                 raise ValueError("e4m3 codes need k_scale and v_scale")
-            ks = _on(dev, self.k_scale, k.shape[:3], torch.float32, "k_scale")
-            vs = _on(dev, self.v_scale, k.shape[:3], torch.float32, "v_scale")
+            shape, dt = k.shape[:3], torch.float32
+            if k.dtype == torch.uint8 and self.k_scale.dtype == torch.uint8:
+                page, code = page[:2] + (2 * page[2],), BEAM_MXFP4
+                shape, dt = (*shape, page[2] // 32), torch.uint8
+            ks = _on(dev, self.k_scale, shape, dt, "k_scale")
+            vs = _on(dev, self.v_scale, shape, dt, "v_scale")
         elif self.k_scale is not None or self.v_scale is not None:
-            raise ValueError("scales go with e4m3 codes only")
-        object.__setattr__(self, "_c", BeamMoeKvCache(kp, vp, ks, vs, k.shape[0], _dt(k)))
-        object.__setattr__(self, "_page", tuple(k.shape[1:]))
+            raise ValueError("scales go with codes only")
+        object.__setattr__(self, "_c", BeamMoeKvCache(kp, vp, ks, vs, k.shape[0], code))
+        object.__setattr__(self, "_page", page)
         object.__setattr__(self, "_dev", dev)
 
     def c(self, cfg: AttnCfg, dev: int) -> BeamMoeKvCache:
@@ -693,6 +715,9 @@ class KVCache:
 def kv_cache(cfg: AttnCfg, n_pages: int, dtype: int, device="cuda") -> KVCache:
     """An empty cache (its contents are undefined until written)."""
     shape = (n_pages, cfg.n_kv_heads, cfg.page_size, cfg.head_dim)
+    if dtype == BEAM_MXFP4:
+        return KVCache(*(torch.empty((*shape[:3], cfg.head_dim // n), dtype=torch.uint8, device=device)
+                         for n in (2, 2, 32, 32)))
     t = {BEAM_F32: torch.float32, BEAM_BF16: torch.bfloat16, BEAM_FP8_E4M3: torch.float8_e4m3fn}[dtype]
     k, v = torch.empty(shape, dtype=t, device=device), torch.empty(shape, dtype=t, device=device)
     if dtype != BEAM_FP8_E4M3:
@@ -783,39 +808,85 @@ def beam_moe_kv_read(cfg: AttnCfg, cache: KVCache, page_table, row_offsets, k_ou
     _launch("beam_moe_kv_read", dev, stream, cfg._c, B, N, cache.c(cfg, dev), tp, width, op, fp, ko, vo, code)
 
 
+def _bytes(n, device):
+    return torch.empty(max(int(n), 256), dtype=torch.uint8, device=device)
+
+
 def attn_workspace(cfg: AttnCfg, B: int, max_len: int, device="cuda") -> torch.Tensor:
-    n = int(lib().beam_moe_attn_workspace_bytes(cfg.c(), _i32(B, "B"), _i32(max_len, "max_len")))
-    return torch.empty(max(n, 256), dtype=torch.uint8, device=device)
+    return _bytes(lib().beam_moe_attn_decode_sinks_workspace_bytes(cfg.c(), cfg.sinks, _i32(B, "B"),
+                                                                   _i32(max_len, "max_len")), device)
+
+
+def attn_prompt_workspace(cfg: AttnCfg, B: int, T: int, max_len: int, device="cuda") -> torch.Tensor:
+    return _bytes(lib().beam_moe_attn_prompt_workspace_bytes(cfg.c(), cfg.sinks, _i32(B, "B"), _i32(T, "T"),
+                                                             _i32(max_len, "max_len")), device)
+
+
+def _attn(cfg, q, B, page_table, seq_lens, out, lse, ws):
+    """Checks and arguments that both attention calls share, for q's T rows
+    and B sequences."""
+    dev, T, dt, code = _rows(q, "q")
+    B = T if B is None else B
+    hq, D, width = cfg.n_heads, cfg.head_dim, page_table.shape[1]
+    qp, qs = _heads(dev, q, T, hq, D, dt, "q")
+    tp = _on(dev, page_table, (B, width), torch.int32, "page_table")
+    lp = _on(dev, seq_lens, (B,), torch.int32, "seq_lens")
+    op = _on(dev, out, (T, hq, D), dt, "out")
+    ep = None if lse is None else _on(dev, lse, (T, hq), torch.float32, "lse")
+    wp, wn = None, 0
+    if ws is not None:
+        wn = ws.numel()
+        wp = _on(dev, ws, (wn,), torch.uint8, "ws")
+    return dev, T, code, qp, qs, tp, width, lp, op, ep, wp, wn
 
 
 def beam_moe_attn_decode(cfg: AttnCfg, q, cache: KVCache, page_table, seq_lens, max_len: int, out, ws, lse=None,
                          stream=None):
     """Attention of one new token per sequence: q [B,n_heads,D] over the
-    cached tokens of page_table [B,max_pages] and seq_lens [B], into out
-    [B,n_heads,D] (and lse [B,n_heads] fp32).  max_len: the longest length to
-    expect; ws from attn_workspace(cfg, B, max_len)."""
+    cached tokens of page_table [B,max_pages] and seq_lens [B] (cfg.window
+    newest and cfg.sinks first ones), into out [B,n_heads,D] (and lse
+    [B,n_heads] fp32).  max_len: the longest length to expect; ws from
+    attn_workspace(cfg, B, max_len)."""
     if stream is None and q.is_cuda:
         m = _marshal() if _native is None else _native
-        if m and m.attn_decode(cfg._c, q, cache._c, cache.k, page_table, seq_lens, max_len, out, ws, lse):
+        if m and cfg.sinks == 0:
+            if m.attn_decode(cfg._c, q, cache._c, cache.k, page_table, seq_lens, max_len, out, ws, lse):
+                return
+        elif m and m.attn_decode_sinks(cfg._c, q, cache._c, cache.k, page_table, seq_lens, max_len, out, ws, lse,
+                                       cfg.sinks):
             return
-    dev, B, dt, code = _rows(q, "q")
-    hq, D, width = cfg.n_heads, cfg.head_dim, page_table.shape[1]
-    qp, qs = _heads(dev, q, B, hq, D, dt, "q")
-    tp = _on(dev, page_table, (B, width), torch.int32, "page_table")
-    lp = _on(dev, seq_lens, (B,), torch.int32, "seq_lens")
-    op = _on(dev, out, (B, hq, D), dt, "out")
-    ep = None if lse is None else _on(dev, lse, (B, hq), torch.float32, "lse")
-    wp, wn = None, 0
-    if ws is not None:
-        wn = ws.numel()
-        wp = _on(dev, ws, (wn,), torch.uint8, "ws")
-    _launch("beam_moe_attn_decode", dev, stream, cfg._c, B, qp, qs, code, cache.c(cfg, dev), tp, width, lp,
-            _i32(max_len, "max_len"), op, ep, wp, wn)
+    dev, B, code, qp, qs, tp, width, lp, op, ep, wp, wn = _attn(cfg, q, None, page_table, seq_lens, out, lse, ws)
+    args = B, qp, qs, code, cache.c(cfg, dev), tp, width, lp, _i32(max_len, "max_len"), op, ep, wp, wn
+    if cfg.sinks == 0:
+        _launch("beam_moe_attn_decode", dev, stream, cfg._c, *args)
+    else:
+        _launch("beam_moe_attn_decode_sinks", dev, stream, cfg._c, cfg.sinks, *args)
+
+
+def beam_moe_attn_prompt(cfg: AttnCfg, q, cache: KVCache, page_table, q_offsets, seq_lens, max_len: int, out, ws,
+                         lse=None, stream=None):
+    """Attention of any number of new tokens per sequence: rows q_offsets[b] ..
+    q_offsets[b+1]-1 of q [T,n_heads,D] are the last of the seq_lens[b] cached
+    tokens of sequence b of page_table [B,max_pages], and each sees the tokens
+    up to its own (cfg.window newest and cfg.sinks first ones); into out
+    [T,n_heads,D] (and lse [T,n_heads] fp32), whose rows at and behind
+    q_offsets[B] stay.  max_len: the longest length to expect; ws from
+    attn_prompt_workspace(cfg, B, T, max_len)."""
+    if stream is None and q.is_cuda:
+        m = _marshal() if _native is None else _native
+        if m and m.attn_prompt(cfg._c, q, cache._c, cache.k, page_table, seq_lens, max_len, out, ws, lse, cfg.sinks,
+                               q_offsets):
+            return
+    B = page_table.shape[0]
+    dev, T, code, qp, qs, tp, width, lp, op, ep, wp, wn = _attn(cfg, q, B, page_table, seq_lens, out, lse, ws)
+    fp = _on(dev, q_offsets, (B + 1,), torch.int32, "q_offsets")
+    _launch("beam_moe_attn_prompt", dev, stream, cfg._c, cfg.sinks, B, T, qp, qs, code, cache.c(cfg, dev), tp, width,
+            fp, lp, _i32(max_len, "max_len"), op, ep, wp, wn)
 
 
 @dataclasses.dataclass
 class AttnBuffers:
-    """Device outputs and scratch of one decode attention for B sequences."""
+    """Device outputs and scratch of one attention call."""
     q: torch.Tensor
     out: torch.Tensor
     lse: torch.Tensor | None
@@ -831,6 +902,24 @@ def attn_buffers(cfg: AttnCfg, B: int, max_len: int, act_dtype=torch.bfloat16, k
                        ws=attn_workspace(cfg, B, max_len, device))
 
 
+def attn_prompt_buffers(cfg: AttnCfg, B: int, T: int, max_len: int, act_dtype=torch.bfloat16, keep_lse=False,
+                        device="cuda") -> AttnBuffers:
+    shape = (T, cfg.n_heads, cfg.head_dim)
+    return AttnBuffers(q=torch.empty(shape, dtype=act_dtype, device=device),
+                       out=torch.empty(shape, dtype=act_dtype, device=device),
+                       lse=torch.empty(shape[:2], dtype=torch.float32, device=device) if keep_lse else None,
+                       ws=attn_prompt_workspace(cfg, B, T, max_len, device))
+
+
+def _heads_of(cfg, qkv):
+    """Queries, keys and values of merged projections [T, (n_heads + 2 n_kv_heads) * D]."""
+    T, hq, hkv, D = qkv.shape[0], cfg.n_heads, cfg.n_kv_heads, cfg.head_dim
+    if qkv.shape != (T, (hq + 2 * hkv) * D):
+        raise ValueError(f"qkv: shape {tuple(qkv.shape)} != {(T, (hq + 2 * hkv) * D)}")
+    rows = qkv.view(T, hq + 2 * hkv, D)
+    return rows[:, :hq], rows[:, hq:hq + hkv], rows[:, hq + hkv:]
+
+
 def attn_layer(cfg: AttnCfg, qkv, positions, slots, cache: KVCache, page_table, seq_lens, max_len: int,
                bufs: AttnBuffers, inv_freq=None, gamma_q=None, gamma_k=None, stream=None):
     """The attention of one decode step between its two projections: qkv
@@ -840,10 +929,17 @@ def attn_layer(cfg: AttnCfg, qkv, positions, slots, cache: KVCache, page_table, 
     included.  The result lands in bufs.out [B,n_heads,D].  Beam's output gate
     is not applied: the caller multiplies it in before the output projection,
     whose result is the m of beam_moe_norm_boundary."""
-    B, hq, hkv, D = qkv.shape[0], cfg.n_heads, cfg.n_kv_heads, cfg.head_dim
-    if qkv.shape != (B, (hq + 2 * hkv) * D):
-        raise ValueError(f"qkv: shape {tuple(qkv.shape)} != {(B, (hq + 2 * hkv) * D)}")
-    rows = qkv.view(B, hq + 2 * hkv, D)
-    beam_moe_qk_norm_rope_cache(cfg, rows[:, :hq], rows[:, hq:hq + hkv], rows[:, hq + hkv:], positions, slots,
-                                bufs.q, cache, inv_freq, gamma_q, gamma_k, stream)
+    q, k, v = _heads_of(cfg, qkv)
+    beam_moe_qk_norm_rope_cache(cfg, q, k, v, positions, slots, bufs.q, cache, inv_freq, gamma_q, gamma_k, stream)
     beam_moe_attn_decode(cfg, bufs.q, cache, page_table, seq_lens, max_len, bufs.out, bufs.ws, bufs.lse, stream)
+
+
+def attn_prompt_layer(cfg: AttnCfg, qkv, positions, slots, cache: KVCache, page_table, q_offsets, seq_lens,
+                      max_len: int, bufs: AttnBuffers, inv_freq=None, gamma_q=None, gamma_k=None, stream=None):
+    """The same for any number of new tokens per sequence: rows q_offsets[b] ..
+    q_offsets[b+1]-1 of qkv [T, (n_heads + 2 n_kv_heads) * D] are the newest
+    of the seq_lens[b] tokens of sequence b.  bufs from attn_prompt_buffers."""
+    q, k, v = _heads_of(cfg, qkv)
+    beam_moe_qk_norm_rope_cache(cfg, q, k, v, positions, slots, bufs.q, cache, inv_freq, gamma_q, gamma_k, stream)
+    beam_moe_attn_prompt(cfg, bufs.q, cache, page_table, q_offsets, seq_lens, max_len, bufs.out, bufs.ws, bufs.lse,
+                         stream)

@@ -21,7 +21,9 @@ BUILD_DIR = os.path.join(ROOT, "_build")
 LIB_PATH = os.path.join(HERE, "libbeam_moe.so")
 BIND_PATH = os.path.join(HERE, "_bind.so")
 SOURCES = ["beam_moe.hip", "route.hip", "permute.hip", "experts.hip", "combine_norm.hip", "pack.hip", "mx.hip",
-           "beam_attn.hip", "attn_prep.hip", "attn_decode.hip"]
+           "beam_attn.hip", "attn_prep.hip", "attn_decode.hip", "attn_decode_sinks.hip", "attn_decode_fp4.hip",
+           "attn_prompt.hip", "attn_prompt_f32.hip", "attn_prompt_bf16.hip", "attn_prompt_fp8.hip",
+           "attn_prompt_fp4.hip"]
 
 ARCH = "gfx950"
 HIP_FLAGS = [

@@ -1,6 +1,6 @@
 // What goes into the attention: per-head RMSNorm of queries and keys, the
 // position rotation, the queries' position factor, and the paged key-value
-// cache (written in bf16, fp32 or e4m3, and read back).
+// cache (written in bf16, fp32, e4m3 or 4 bits, and read back).
 // (TokenSpeed x Reflection Beam blog, "Architecture", and vLLM Beam summary,
 //  kernel list: QK norm + rotation or position factor in one kernel with the
 //  cache write.)
@@ -8,8 +8,7 @@
 // A head row is spread over D/8 lanes of 8 consecutive elements, so a wave
 // holds 512/D heads, a row's sums take log2(D/8) lane exchanges and every
 // access is 16 bytes of bf16 per lane.
-#include "common.h"
-#include "kernels.h"
+#include "attn_common.h"
 
 namespace beam {
 
@@ -120,10 +119,30 @@ BEAM_DEV float inv_sqrt(float s) {
 }
 
 // Stores a head row's 8 elements of this lane at row `row` of one cache
-// side.  e4m3: the scale and codes that quantize_row_e4m3_wave gives a row.
+// side.  e4m3: the scale and codes that quantize_row_e4m3_wave gives a row.  4
+// bits: per block of 32 elements, four lanes', the E8M0 byte of floor(log2 amax)
+// - 2 (at least 0; the exponent field of amax less 2) and E2M1 codes: what
+// beam_quantize_mx_rows gives a finite block.  A NaN counts as 0 in amax and is
+// stored as +-6 times the scale, an infinite element likewise with the largest
+// scale there is, 2^126: it reads back as infinite.
 template <int CK, int D>
-BEAM_DEV void store_cache(void* side, float* scales, size_t row, int e0, float (&x)[8], bool live) {
-    if constexpr (CK == A_FP8) {
+BEAM_DEV void store_cache(void* side, void* scales, size_t row, int e0, float (&x)[8], bool live) {
+    if constexpr (CK == A_FP4) {
+        float amax = 0.f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(x[j]));
+        amax = fmaxf(amax, dpp<kXor1>(amax));   // every lane takes part
+        amax = fmaxf(amax, dpp<kXor2>(amax));
+        const int byte = max((int)(__float_as_uint(amax) >> 23) - 2, 0);
+        const float s = e8m0((uint32_t)byte);
+        if (!live) return;
+        uint32_t c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(0u, x[0], x[1], s, 0);
+        c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, x[2], x[3], s, 1);
+        c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, x[4], x[5], s, 2);
+        c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, x[6], x[7], s, 3);
+        *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(side) + row * (D / 2) + e0 / 2) = c;
+        if (e0 % 32 == 0) static_cast<uint8_t*>(scales)[row * (D / 32) + e0 / 32] = (uint8_t)byte;
+    } else if constexpr (CK == A_FP8) {
         float amax = 0.f;
 #pragma unroll
         for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(x[j]));
@@ -134,7 +153,7 @@ BEAM_DEV void store_cache(void* side, float* scales, size_t row, int e0, float (
         if (!live) return;
         *reinterpret_cast<uint2*>(static_cast<uint8_t*>(side) + row * D + e0) =
             make_uint2(e4m3x4(x[0], x[1], x[2], x[3]), e4m3x4(x[4], x[5], x[6], x[7]));
-        if (e0 == 0) scales[row] = s;
+        if (e0 == 0) static_cast<float*>(scales)[row] = s;
     } else {
         if (live) st8<CK == A_BF16>(side, row * D + e0, x);
     }
@@ -331,6 +350,7 @@ static hipError_t launch_prep_c(const AttnPrepArgs& a, hipStream_t st) {
     if (a.k_out) return launch_prep_d<BF, -1>(a, st);
     if (a.c.kind == A_F32) return launch_prep_d<BF, A_F32>(a, st);
     if (a.c.kind == A_BF16) return launch_prep_d<BF, A_BF16>(a, st);
+    if (a.c.kind == A_FP4) return launch_prep_d<BF, A_FP4>(a, st);
     return launch_prep_d<BF, A_FP8>(a, st);
 }
 
@@ -351,21 +371,34 @@ template <int CK> struct RawC8;                       // 8 cache elements as sto
 template <> struct RawC8<A_BF16> { Raw8<true> v; };
 template <> struct RawC8<A_F32> { Raw8<false> v; };
 template <> struct RawC8<A_FP8> { uint2 v; float s; };
-template <int CK> BEAM_DEV RawC8<CK> ld_cache8(const void* side, const float* scales, size_t row, int D, int e0) {
+template <> struct RawC8<A_FP4> { uint32_t v; uint32_t s; };
+template <int CK> BEAM_DEV RawC8<CK> ld_cache8(const void* side, const void* scales, size_t row, int D, int e0) {
     RawC8<CK> r;
-    if constexpr (CK == A_FP8) {
+    if constexpr (CK == A_FP4) {
+        r.v = __builtin_nontemporal_load(
+            reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(side) + row * (D / 2) + e0 / 2));   // read once
+        r.s = static_cast<const uint8_t*>(scales)[row * (D / 32) + e0 / 32];
+    } else if constexpr (CK == A_FP8) {
         typedef uint32_t u32x2v __attribute__((ext_vector_type(2)));
         const u32x2v w = __builtin_nontemporal_load(
             reinterpret_cast<const u32x2v*>(static_cast<const uint8_t*>(side) + row * D + e0));   // read once
         r.v = make_uint2(w.x, w.y);
-        r.s = scales[row];
+        r.s = static_cast<const float*>(scales)[row];
     } else {
         r.v = ld8<CK == A_BF16>(side, row * D + e0);
     }
     return r;
 }
 template <int CK> BEAM_DEV void wid_cache8(const RawC8<CK>& r, float (&x)[8]) {
-    if constexpr (CK == A_FP8) {
+    if constexpr (CK == A_FP4) {
+        const float s = e8m0(r.s);   // exact in bf16, so in fp32 too
+        const uint32_t w[4] = {e2m1_pair<0>(r.v, s), e2m1_pair<1>(r.v, s), e2m1_pair<2>(r.v, s), e2m1_pair<3>(r.v, s)};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            x[2 * j] = __uint_as_float(w[j] << 16);
+            x[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+        }
+    } else if constexpr (CK == A_FP8) {
         typedef float f32x2v __attribute__((ext_vector_type(2)));
         const uint32_t w[2] = {r.v.x, r.v.y};
 #pragma unroll
@@ -464,6 +497,7 @@ template <bool BF>
 static hipError_t launch_read_c(const KvReadArgs& a, hipStream_t st) {
     if (a.c.kind == A_F32) return launch_read_d<BF, A_F32>(a, st);
     if (a.c.kind == A_BF16) return launch_read_d<BF, A_BF16>(a, st);
+    if (a.c.kind == A_FP4) return launch_read_d<BF, A_FP4>(a, st);
     return launch_read_d<BF, A_FP8>(a, st);
 }
 

@@ -1,0 +1,50 @@
+// How the attention of new tokens cuts blocks into parts, and its launch.
+#include "attn_prompt.h"
+
+namespace beam {
+
+// Parts of the blocks' spans.  Few blocks (together fewer than kWantWG
+// workgroups): each may be cut, so that the chip has work.  Many: only a
+// sequence that is one block is, where it would run on long after the others.
+constexpr int kWantWG = 512, kMostWG = 2048, kLongPart = 1024;
+PromptSplit attn_prompt_split(int B, int T, int Hq, int Hkv, int max_len, int window, int sinks) {
+    PromptSplit p;
+    const int64_t G = Hq / Hkv;
+    p.nseq = (uint32_t)B;
+    p.blocks = (uint32_t)((int64_t)T * G / kPromptRows + B);
+    // what a block's rows see at most: a window, its tokens' breadth and sinks
+    int64_t span = max_len;
+    if (window > 0) {
+        const int64_t seen = (int64_t)window + kPromptRows / G + 32 + (((int64_t)sinks + 15) & ~(int64_t)15);
+        span = seen < span ? seen : span;
+    }
+    const int64_t wg = (int64_t)p.blocks * Hkv;
+    p.every = wg < kWantWG;
+    int64_t s, most;
+    if (p.every) {
+        s = (kWantWG + wg - 1) / wg;
+        most = (span + kPromptMinPart - 1) / kPromptMinPart;
+    } else {
+        // some sequence may be one block only if there are several
+        s = B > 1 ? kMostWG / ((int64_t)B * Hkv) : 1;
+        most = (span + kLongPart - 1) / kLongPart;
+    }
+    s = s < most ? s : most;
+    p.S = (uint32_t)(s < 1 ? 1 : s);
+    return p;
+}
+
+size_t attn_prompt_ws_bytes(int Hkv, int D, const PromptSplit& p) {
+    return (size_t)p.slots() * Hkv * kPromptRows * (D + 4) * sizeof(float);
+}
+
+hipError_t launch_attn_prompt(AttnPromptArgs a, void* ws, hipStream_t st) {
+    a.parts = static_cast<float*>(ws);
+    a.ml = reinterpret_cast<float4*>(a.parts + (size_t)a.p.slots() * a.Hkv * kPromptRows * a.D);
+    if (a.c.kind == A_F32) return launch_attn_prompt_f32(a, st);
+    if (a.c.kind == A_BF16) return launch_attn_prompt_bf16(a, st);
+    if (a.c.kind == A_FP8) return launch_attn_prompt_fp8(a, st);
+    return launch_attn_prompt_fp4(a, st);
+}
+
+}  // namespace beam

@@ -12,6 +12,7 @@ namespace {
 constexpr int64_t kMaxT = 1 << 22;          // tokens or sequences per call
 constexpr int64_t kMaxParts = 1 << 23;      // query heads times parts per decode call: a launch of 256-thread
                                             // workgroups holds fewer than 2^32 threads
+constexpr int64_t kMaxGroups = 1 << 24;     // such workgroups
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
@@ -38,9 +39,10 @@ beam_status check_attn_cfg(const beam_moe_attn_cfg* c) {
 
 beam_status check_cache(const beam_moe_attn_cfg* c, const beam_moe_kv_cache* k, beam::KvCache& out) {
     if (!k || !k->k || !k->v || k->n_pages <= 0) return BEAM_ERR_INVALID_ARG;
-    if (k->dtype != BEAM_F32 && k->dtype != BEAM_BF16 && k->dtype != BEAM_FP8_E4M3) return BEAM_ERR_INVALID_ARG;
+    if (k->dtype != BEAM_F32 && k->dtype != BEAM_BF16 && k->dtype != BEAM_FP8_E4M3 && k->dtype != BEAM_MXFP4)
+        return BEAM_ERR_INVALID_ARG;
     if (!aligned16(k->k) || !aligned16(k->v)) return BEAM_ERR_INVALID_ARG;
-    if (k->dtype == BEAM_FP8_E4M3 && (!k->k_scale || !k->v_scale || !aligned16(k->k_scale) || !aligned16(k->v_scale)))
+    if ((k->dtype == BEAM_FP8_E4M3 || k->dtype == BEAM_MXFP4) && (!k->k_scale || !k->v_scale || !aligned16(k->k_scale) || !aligned16(k->v_scale)))
         return BEAM_ERR_INVALID_ARG;
     if ((int64_t)k->n_pages * c->page_size > 0x7FFFFFFF) return BEAM_ERR_UNSUPPORTED;
     int sh = 0;
@@ -51,9 +53,14 @@ beam_status check_cache(const beam_moe_attn_cfg* c, const beam_moe_kv_cache* k, 
     out.vs = k->v_scale;
     out.n_pages = k->n_pages;
     out.pshift = sh;
-    out.kind = k->dtype == BEAM_F32 ? beam::A_F32 : (k->dtype == BEAM_BF16 ? beam::A_BF16 : beam::A_FP8);
+    out.kind = k->dtype == BEAM_F32    ? beam::A_F32
+               : k->dtype == BEAM_BF16 ? beam::A_BF16
+               : k->dtype == BEAM_MXFP4 ? beam::A_FP4
+                                        : beam::A_FP8;
     return BEAM_OK;
 }
+
+bool sinks_ok(int32_t n) { return n >= 0 && n <= beam::kMaxLen; }
 
 bool act_dtype(beam_dtype d) { return d == BEAM_F32 || d == BEAM_BF16; }
 
@@ -219,18 +226,35 @@ beam_status beam_moe_kv_read(const beam_moe_attn_cfg* cfg, int32_t B, int32_t N,
 }
 
 size_t beam_moe_attn_workspace_bytes(const beam_moe_attn_cfg* cfg, int32_t B, int32_t max_len) {
-    if (check_attn_cfg(cfg) != BEAM_OK || B <= 0 || B > kMaxT || max_len < 0 || max_len > beam::kMaxLen) return 0;
+    return beam_moe_attn_decode_sinks_workspace_bytes(cfg, 0, B, max_len);
+}
+
+size_t beam_moe_attn_decode_sinks_workspace_bytes(const beam_moe_attn_cfg* cfg, int32_t n_sinks, int32_t B,
+                                                  int32_t max_len) {
+    if (check_attn_cfg(cfg) != BEAM_OK || B <= 0 || B > kMaxT || max_len < 0 || max_len > beam::kMaxLen ||
+        !sinks_ok(n_sinks))
+        return 0;
     return beam::attn_decode_ws_bytes(B, cfg->n_heads, cfg->head_dim,
-                                      beam::attn_decode_split(B, cfg->n_kv_heads, max_len, cfg->window));
+                                      beam::attn_decode_split(B, cfg->n_kv_heads, max_len, cfg->window, n_sinks));
 }
 
 beam_status beam_moe_attn_decode(const beam_moe_attn_cfg* cfg, int32_t B, const void* q, int64_t q_stride,
                                  beam_dtype dtype, const beam_moe_kv_cache* cache, const int32_t* page_table,
                                  int32_t max_pages, const int32_t* seq_lens, int32_t max_len, void* out, float* lse,
                                  void* ws, size_t ws_bytes, void* stream) {
+    return beam_moe_attn_decode_sinks(cfg, 0, B, q, q_stride, dtype, cache, page_table, max_pages, seq_lens, max_len,
+                                      out, lse, ws, ws_bytes, stream);
+}
+
+beam_status beam_moe_attn_decode_sinks(const beam_moe_attn_cfg* cfg, int32_t n_sinks, int32_t B, const void* q,
+                                       int64_t q_stride, beam_dtype dtype, const beam_moe_kv_cache* cache,
+                                       const int32_t* page_table, int32_t max_pages, const int32_t* seq_lens,
+                                       int32_t max_len, void* out, float* lse, void* ws, size_t ws_bytes,
+                                       void* stream) {
     beam_status st = check_attn_cfg(cfg);
     if (st != BEAM_OK) return st;
-    if (B < 0 || B > kMaxT || max_pages < 0 || max_len < 0 || max_len > beam::kMaxLen || !act_dtype(dtype))
+    if (B < 0 || B > kMaxT || max_pages < 0 || max_len < 0 || max_len > beam::kMaxLen || !act_dtype(dtype) ||
+        !sinks_ok(n_sinks))
         return BEAM_ERR_INVALID_ARG;
     if (B == 0) return BEAM_OK;
     const int64_t qw = (int64_t)cfg->n_heads * cfg->head_dim;
@@ -243,7 +267,7 @@ beam_status beam_moe_attn_decode(const beam_moe_attn_cfg* cfg, int32_t B, const 
     if ((a.c.kind == beam::A_F32) != (dtype == BEAM_F32)) return BEAM_ERR_UNSUPPORTED;
     const size_t es = dtype == BEAM_BF16 ? 2 : 4;
     if (overlap(out, (size_t)B * qw * es, q, span_bytes(B, q_stride, qw, es))) return BEAM_ERR_INVALID_ARG;
-    a.p = beam::attn_decode_split(B, cfg->n_kv_heads, max_len, cfg->window);
+    a.p = beam::attn_decode_split(B, cfg->n_kv_heads, max_len, cfg->window, n_sinks);
     if ((int64_t)a.p.rows * cfg->n_heads > kMaxParts) return BEAM_ERR_UNSUPPORTED;
     const size_t need = beam::attn_decode_ws_bytes(B, cfg->n_heads, cfg->head_dim, a.p);
     if (need > 0 && (!ws || ws_bytes < need || !aligned16(ws))) return BEAM_ERR_WORKSPACE;
@@ -254,6 +278,7 @@ beam_status beam_moe_attn_decode(const beam_moe_attn_cfg* cfg, int32_t B, const 
     a.D = cfg->head_dim;
     a.max_pages = max_pages;
     a.window = cfg->window;
+    a.sinks = cfg->window > 0 ? n_sinks : 0;
     a.scale = cfg->softmax_scale;
     a.q = q;
     a.qs = (size_t)q_stride;
@@ -262,6 +287,62 @@ beam_status beam_moe_attn_decode(const beam_moe_attn_cfg* cfg, int32_t B, const 
     a.out = out;
     a.lse = lse;
     return ran(beam::launch_attn_decode(a, ws, static_cast<hipStream_t>(stream)));
+}
+
+size_t beam_moe_attn_prompt_workspace_bytes(const beam_moe_attn_cfg* cfg, int32_t n_sinks, int32_t B, int32_t T,
+                                            int32_t max_len) {
+    if (check_attn_cfg(cfg) != BEAM_OK || B <= 0 || B > kMaxT || T <= 0 || T > kMaxT || max_len < 0 ||
+        max_len > beam::kMaxLen || !sinks_ok(n_sinks))
+        return 0;
+    return beam::attn_prompt_ws_bytes(cfg->n_kv_heads, cfg->head_dim,
+                                      beam::attn_prompt_split(B, T, cfg->n_heads, cfg->n_kv_heads, max_len,
+                                                              cfg->window, n_sinks));
+}
+
+beam_status beam_moe_attn_prompt(const beam_moe_attn_cfg* cfg, int32_t n_sinks, int32_t B, int32_t T, const void* q,
+                                 int64_t q_stride, beam_dtype dtype, const beam_moe_kv_cache* cache,
+                                 const int32_t* page_table, int32_t max_pages, const int32_t* q_offsets,
+                                 const int32_t* seq_lens, int32_t max_len, void* out, float* lse, void* ws,
+                                 size_t ws_bytes, void* stream) {
+    beam_status st = check_attn_cfg(cfg);
+    if (st != BEAM_OK) return st;
+    if (B < 0 || B > kMaxT || T < 0 || T > kMaxT || max_pages < 0 || max_len < 0 || max_len > beam::kMaxLen ||
+        !act_dtype(dtype) || !sinks_ok(n_sinks))
+        return BEAM_ERR_INVALID_ARG;
+    if (B == 0 || T == 0) return BEAM_OK;
+    const int64_t qw = (int64_t)cfg->n_heads * cfg->head_dim;
+    if (!rows_ok(q, q_stride, qw) || !out || !aligned16(out) || !seq_lens || !aligned4(seq_lens) || !q_offsets ||
+        !aligned4(q_offsets) || !aligned4(lse))
+        return BEAM_ERR_INVALID_ARG;
+    if (max_pages > 0 && (!page_table || !aligned4(page_table))) return BEAM_ERR_INVALID_ARG;
+    beam::AttnPromptArgs a{};
+    st = check_cache(cfg, cache, a.c);
+    if (st != BEAM_OK) return st;
+    if ((a.c.kind == beam::A_F32) != (dtype == BEAM_F32)) return BEAM_ERR_UNSUPPORTED;
+    const size_t es = dtype == BEAM_BF16 ? 2 : 4;
+    if (overlap(out, (size_t)T * qw * es, q, span_bytes(T, q_stride, qw, es))) return BEAM_ERR_INVALID_ARG;
+    a.p = beam::attn_prompt_split(B, T, cfg->n_heads, cfg->n_kv_heads, max_len, cfg->window, n_sinks);
+    if (a.p.groups(cfg->n_kv_heads) >= kMaxGroups) return BEAM_ERR_UNSUPPORTED;
+    const size_t need = beam::attn_prompt_ws_bytes(cfg->n_kv_heads, cfg->head_dim, a.p);
+    if (need > 0 && (!ws || ws_bytes < need || !aligned16(ws))) return BEAM_ERR_WORKSPACE;
+    a.B = B;
+    a.T = T;
+    a.Hq = cfg->n_heads;
+    a.Hkv = cfg->n_kv_heads;
+    a.G = a.Hq / a.Hkv;
+    a.D = cfg->head_dim;
+    a.max_pages = max_pages;
+    a.window = cfg->window;
+    a.sinks = cfg->window > 0 ? n_sinks : 0;
+    a.scale = cfg->softmax_scale;
+    a.q = q;
+    a.qs = (size_t)q_stride;
+    a.table = page_table;
+    a.offsets = q_offsets;
+    a.lens = seq_lens;
+    a.out = out;
+    a.lse = lse;
+    return ran(beam::launch_attn_prompt(a, ws, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

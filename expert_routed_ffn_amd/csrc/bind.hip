@@ -31,6 +31,8 @@ decltype(&beam_moe_qk_norm_rope_cache) g_norm_rope_cache = nullptr;
 decltype(&beam_moe_kv_write) g_kv_write = nullptr;
 decltype(&beam_moe_kv_read) g_kv_read = nullptr;
 decltype(&beam_moe_attn_decode) g_decode = nullptr;
+decltype(&beam_moe_attn_decode_sinks) g_decode_sinks = nullptr;
+decltype(&beam_moe_attn_prompt) g_prompt = nullptr;
 
 constexpr DLDataType kF32{kDLFloat, 32, 1}, kBF16{kDLBfloat, 16, 1}, kI32{kDLInt, 32, 1}, kU8{kDLUInt, 8, 1};
 
@@ -140,7 +142,7 @@ const beam_moe_kv_cache* cache_of(const Call& c, PyObject* cache, PyObject* k) {
     if (!kv || !view(k, t)) return nullptr;
     if ((int)t.device.device_type != g_gpu_type || t.device.device_id != c.dev || t.ndim != 4 || data(t) != kv->k ||
         t.shape[0] != kv->n_pages || t.shape[1] != c.cfg->n_kv_heads || t.shape[2] != c.cfg->page_size ||
-        t.shape[3] != c.cfg->head_dim)
+        t.shape[3] * (kv->dtype == BEAM_MXFP4 ? 2 : 1) != c.cfg->head_dim)
         return nullptr;
     return kv;
 }
@@ -255,32 +257,85 @@ PyObject* kv_read(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return outcome("beam_moe_kv_read", st);
 }
 
+// cfg, q, cache, cache.k, page_table, seq_lens, max_len, out, ws, lse: what the
+// attention calls have in common, for B sequences (-1: q's rows)
+struct Attend {
+    const beam_moe_kv_cache* kv;
+    void *q, *table, *lens, *out, *lse, *ws;
+    int64_t B, qs, width, wn;
+    int32_t max_len;
+};
+bool attend(Call& c, PyObject* const* a, int64_t B, Attend& p) {
+    DLTensor t, w;
+    if (!view(a[1], t) || !open_call(a[0], t, c)) return false;
+    const int64_t h = c.cfg->n_heads, D = c.cfg->head_dim, shape[3] = {c.T, h, D}, ls[2] = {c.T, h};
+    p.B = B < 0 ? c.T : B;
+    p.kv = cache_of(c, a[2], a[3]);
+    const long long max_len = PyLong_AsLongLong(a[6]);
+    if (max_len == -1 && PyErr_Occurred()) PyErr_Clear();
+    if (!p.kv || max_len < 0 || max_len > INT32_MAX || !heads(t, c.dev, c.dt, c.T, h, D, &p.q, &p.qs) ||
+        !page_table(a[4], c.dev, &p.B, &p.width, &p.table) || !dense1(a[5], c.dev, kI32, p.B, &p.lens) ||
+        !dense(a[7], c.dev, c.dt, 3, shape, &p.out))
+        return false;
+    p.max_len = (int32_t)max_len;
+    p.lse = p.ws = nullptr;
+    p.wn = 0;
+    if (a[9] != Py_None && !dense(a[9], c.dev, kF32, 2, ls, &p.lse)) return false;
+    if (a[8] != Py_None) {
+        if (!view(a[8], w) || w.ndim != 1 || !fits(w, c.dev, kU8, 1, w.shape) || !contiguous(w)) return false;
+        p.ws = data(w);
+        p.wn = w.shape[0];
+    }
+    return true;
+}
+
 // (cfg, q, cache, cache.k, page_table, seq_lens, max_len, out, ws, lse)
 PyObject* attn_decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
     Call c;
-    DLTensor t, w;
-    void *q, *table, *lens, *out, *lse = nullptr, *ws = nullptr;
-    int64_t qs, width, wn = 0;
-    if (n != 10 || !g_decode || !view(a[1], t) || !open_call(a[0], t, c)) return does_not_fit();
-    const int64_t h = c.cfg->n_heads, D = c.cfg->head_dim, shape[3] = {c.T, h, D}, ls[2] = {c.T, h};
-    int64_t B = c.T;
-    const beam_moe_kv_cache* kv = cache_of(c, a[2], a[3]);
-    const long long max_len = PyLong_AsLongLong(a[6]);
-    if (max_len == -1 && PyErr_Occurred()) PyErr_Clear();
-    if (!kv || max_len < 0 || max_len > INT32_MAX || !heads(t, c.dev, c.dt, B, h, D, &q, &qs) ||
-        !page_table(a[4], c.dev, &B, &width, &table) || !dense1(a[5], c.dev, kI32, B, &lens) ||
-        !dense(a[7], c.dev, c.dt, 3, shape, &out))
-        return does_not_fit();
-    if (a[9] != Py_None && !dense(a[9], c.dev, kF32, 2, ls, &lse)) return does_not_fit();
-    if (a[8] != Py_None) {
-        if (!view(a[8], w) || w.ndim != 1 || !fits(w, c.dev, kU8, 1, w.shape) || !contiguous(w)) return does_not_fit();
-        ws = data(w);
-        wn = w.shape[0];
-    }
-    const beam_status st = g_decode(c.cfg, (int32_t)B, q, qs, c.code, kv, static_cast<const int32_t*>(table),
-                                    (int32_t)width, static_cast<const int32_t*>(lens), (int32_t)max_len, out,
-                                    static_cast<float*>(lse), ws, (size_t)wn, c.stream);
+    Attend p;
+    if (n != 10 || !g_decode || !attend(c, a, -1, p)) return does_not_fit();
+    const beam_status st = g_decode(c.cfg, (int32_t)p.B, p.q, p.qs, c.code, p.kv, static_cast<const int32_t*>(p.table),
+                                    (int32_t)p.width, static_cast<const int32_t*>(p.lens), p.max_len, p.out,
+                                    static_cast<float*>(p.lse), p.ws, (size_t)p.wn, c.stream);
     return outcome("beam_moe_attn_decode", st);
+}
+
+bool sinks_of(PyObject* o, int32_t* n) {
+    const long long v = PyLong_AsLongLong(o);
+    if (v == -1 && PyErr_Occurred()) PyErr_Clear();
+    *n = (int32_t)v;
+    return v >= 0 && v <= INT32_MAX;
+}
+
+// (.., lse, sinks)
+PyObject* attn_decode_sinks(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    Call c;
+    Attend p;
+    int32_t sinks;
+    if (n != 11 || !g_decode_sinks || !sinks_of(a[10], &sinks) || !attend(c, a, -1, p)) return does_not_fit();
+    const beam_status st =
+        g_decode_sinks(c.cfg, sinks, (int32_t)p.B, p.q, p.qs, c.code, p.kv, static_cast<const int32_t*>(p.table),
+                       (int32_t)p.width, static_cast<const int32_t*>(p.lens), p.max_len, p.out,
+                       static_cast<float*>(p.lse), p.ws, (size_t)p.wn, c.stream);
+    return outcome("beam_moe_attn_decode_sinks", st);
+}
+
+// (.., lse, sinks, q_offsets)
+PyObject* attn_prompt(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    Call c;
+    Attend p;
+    DLTensor t;
+    int32_t sinks;
+    void* offsets;
+    if (n != 12 || !g_prompt || !sinks_of(a[10], &sinks) || !view(a[4], t) || t.ndim != 2 ||
+        !attend(c, a, t.shape[0], p) || !dense1(a[11], c.dev, kI32, p.B + 1, &offsets))
+        return does_not_fit();
+    const beam_status st =
+        g_prompt(c.cfg, sinks, (int32_t)p.B, (int32_t)c.T, p.q, p.qs, c.code, p.kv,
+                 static_cast<const int32_t*>(p.table), (int32_t)p.width, static_cast<const int32_t*>(offsets),
+                 static_cast<const int32_t*>(p.lens), p.max_len, p.out, static_cast<float*>(p.lse), p.ws,
+                 (size_t)p.wn, c.stream);
+    return outcome("beam_moe_attn_prompt", st);
 }
 
 // bind(exchange capsule, gpu device type, addresses of the five entry points[,
@@ -314,6 +369,15 @@ PyObject* bind(PyObject*, PyObject* args) {
     Py_RETURN_NONE;
 }
 
+// bind_more(addresses of attn_decode_sinks and attn_prompt)
+PyObject* bind_more(PyObject*, PyObject* args) {
+    unsigned long long f[2];
+    if (!PyArg_ParseTuple(args, "KK", &f[0], &f[1])) return nullptr;
+    g_decode_sinks = reinterpret_cast<decltype(g_decode_sinks)>(f[0]);
+    g_prompt = reinterpret_cast<decltype(g_prompt)>(f[1]);
+    Py_RETURN_NONE;
+}
+
 template <typename F> PyMethodDef fast(const char* name, F f) {
     return {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)), METH_FASTCALL, nullptr};
 }
@@ -323,6 +387,9 @@ PyMethodDef methods[] = {fast("qk_norm_rope", qk_norm_rope),
                          fast("kv_write", kv_write),
                          fast("kv_read", kv_read),
                          fast("attn_decode", attn_decode),
+                         fast("attn_decode_sinks", attn_decode_sinks),
+                         fast("attn_prompt", attn_prompt),
+                         {"bind_more", bind_more, METH_VARARGS, nullptr},
                          {"bind", bind, METH_VARARGS, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_bind", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

@@ -129,14 +129,14 @@ hipError_t launch(void (*kernel)(P...), dim3 grid, dim3 block, hipStream_t st, c
 }
 
 // Element kinds of the attention sublayer's activations and cache.
-enum AKind { A_F32 = 0, A_BF16 = 1, A_FP8 = 2 };
+enum AKind { A_F32 = 0, A_BF16 = 1, A_FP8 = 2, A_FP4 = 3 };
 
 // A paged key-value cache: [n_pages, Hkv, 2^pshift, D] per side.
 struct KvCache {
     void* k;
     void* v;
-    float* ks;              // FP8: [n_pages, Hkv, 2^pshift]
-    float* vs;
+    void* ks;               // FP8: fp32 [n_pages, Hkv, 2^pshift]; FP4: E8M0 bytes [n_pages, Hkv, 2^pshift, D/32]
+    void* vs;
     int n_pages;
     int pshift;             // log2 of the tokens per page
     AKind kind;
@@ -187,6 +187,7 @@ struct AttnSplit {
 
 struct AttnDecodeArgs {
     int B, Hq, Hkv, G, D, max_pages, window;   // G = Hq / Hkv
+    int sinks;              // first tokens that a window leaves visible
     float scale;
     const void* q;
     size_t qs;
@@ -202,8 +203,47 @@ struct AttnDecodeArgs {
     int4* lists;            // [joins], listed parts only: sequence, first row, number of parts
 };
 constexpr int kMaxLen = 1 << 30;   // longest sequence attn_decode counts
-AttnSplit attn_decode_split(int B, int Hkv, int max_len, int window);
+AttnSplit attn_decode_split(int B, int Hkv, int max_len, int window, int sinks);
 size_t attn_decode_ws_bytes(int B, int Hq, int D, const AttnSplit& p);
 hipError_t launch_attn_decode(AttnDecodeArgs a, void* ws, hipStream_t st);
+hipError_t launch_attn_decode_sinks(const AttnDecodeArgs& a, hipStream_t st);   // workspace set
+hipError_t launch_attn_decode_fp4(const AttnDecodeArgs& a, hipStream_t st);
+
+// How attn_prompt cuts the blocks' spans of tokens into parts (attn_prompt_split).
+constexpr int kPromptRows = 128;    // rows (query token, head of the group) of a block
+struct PromptSplit {
+    uint32_t blocks;        // most blocks there can be, all sequences together
+    uint32_t S;             // most parts of a block; 1: no workspace
+    bool every;             // every block may be cut; else those that are their sequence's only one
+    uint32_t nseq;
+    uint32_t slots() const { return S > 1 ? (every ? blocks : nseq) * S : 0; }   // parts' places in the workspace
+    int64_t groups(int Hkv) const {   // workgroups of a launch
+        return (int64_t)Hkv * (every ? (int64_t)blocks * S : blocks + (int64_t)nseq * (S - 1));
+    }
+};
+
+struct AttnPromptArgs {
+    int B, T, Hq, Hkv, G, D, max_pages, window, sinks;   // G = Hq / Hkv
+    float scale;
+    const void* q;
+    size_t qs;
+    const int32_t* table;
+    const int32_t* offsets;
+    const int32_t* lens;
+    PromptSplit p;
+    KvCache c;
+    void* out;
+    float* lse;
+    // workspace (attn_prompt_ws_bytes):
+    float* parts;           // [slots, Hkv, kPromptRows, D] sums
+    float4* ml;             // [slots, Hkv, kPromptRows] (max, sum, sum before rounding, -)
+};
+PromptSplit attn_prompt_split(int B, int T, int Hq, int Hkv, int max_len, int window, int sinks);
+size_t attn_prompt_ws_bytes(int Hkv, int D, const PromptSplit& p);
+hipError_t launch_attn_prompt(AttnPromptArgs a, void* ws, hipStream_t st);
+hipError_t launch_attn_prompt_f32(const AttnPromptArgs& a, hipStream_t st);   // workspace set
+hipError_t launch_attn_prompt_bf16(const AttnPromptArgs& a, hipStream_t st);
+hipError_t launch_attn_prompt_fp8(const AttnPromptArgs& a, hipStream_t st);
+hipError_t launch_attn_prompt_fp4(const AttnPromptArgs& a, hipStream_t st);
 
 }  // namespace beam

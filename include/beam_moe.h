@@ -16,10 +16,11 @@
  *                depth-scaled residual h <- sqrt((n-1)/n) h + p / sqrt(n),
  *                next pre-RMSNorm
  * and the operators of the attention sublayer between two such boundaries,
- * for decode serving (second half of this file):
+ * for serving (second half of this file):
  *   qk_norm_rope  per-head norm of queries and keys with the rotation
- *   kv_write/read paged key-value cache, bf16, fp32 or e4m3
+ *   kv_write/read paged key-value cache, bf16, fp32, e4m3 or 4 bits (MXFP4)
  *   attn_decode   attention of one new token per sequence over that cache
+ *   attn_prompt   attention of any number of new tokens per sequence over it
  *
  * Conventions for every entry point:
  *   - All tensor pointers are DEVICE pointers, row-major, densely packed,
@@ -380,7 +381,8 @@ size_t beam_moe_workspace_bytes(const beam_moe_cfg* cfg, int32_t T, beam_dtype w
 
 /* ---------------------------------------------------------------------------
  * Attention sublayer: per-head query/key norms with the position rotation, a
- * paged key-value cache, and the attention of one new token over it.
+ * paged key-value cache, and the attention of new tokens over it: one for each
+ * sequence (decode) or any number (prompts, chunks of them, drafted tokens).
  * (TokenSpeed x Reflection Beam blog, "Architecture"; vLLM Beam summary,
  *  attention section: 48 query heads over 8 key-value heads of 128, a
  *  per-head RMSNorm of queries and keys, sliding windows of 512 with rotary
@@ -414,9 +416,12 @@ typedef struct beam_moe_attn_cfg {
  * the page.  Read by the host during a call only; the arrays are device
  * memory, 16-byte aligned:
  *   k, v             [n_pages, n_kv_heads, page_size, D] of dtype
- *                    (F32, BF16 or FP8_E4M3)
- *   k_scale, v_scale [n_pages, n_kv_heads, page_size] fp32, FP8_E4M3 only:
- *                    an element is code * scale, one scale per head row
+ *                    (F32, BF16, FP8_E4M3 or MXFP4: D/2 bytes per head row)
+ *   k_scale, v_scale FP8_E4M3: [n_pages, n_kv_heads, page_size] fp32, an
+ *                    element is code * scale, one scale per head row;
+ *                    MXFP4: [n_pages, n_kv_heads, page_size, D/32] uint8 (cast
+ *                    to the member's type), E8M0 codes of blocks of 32 (255,
+ *                    which is never written, makes a block NaN)
  * n_pages * page_size is at most 2^31 - 1.
  */
 typedef struct beam_moe_kv_cache {
@@ -456,7 +461,10 @@ beam_status beam_moe_qk_norm_rope(const beam_moe_attn_cfg* cfg, int32_t T,
  * What is stored is the fp32 result rounded once to the cache's dtype; for
  * FP8_E4M3, scale = amax/448 of the head row in fp32 (1 where that is 0) and
  * code = e4m3(value / scale), rounded to nearest even, as
- * beam_moe_quantize_fp8 does per token.
+ * beam_moe_quantize_fp8 does per token; for MXFP4, the codes and scales of
+ * beam_moe_quantize_mx, per 32 elements of the head row (an infinite element
+ * gives its block the scale 2^126 and reads back as infinite; there is no 4-bit
+ * NaN: one is stored as 6 times its block's scale).
  *   slots [T] int32: a row whose slot is outside [0, n_pages * page_size)
  *         (-1 for padding) is not stored; its q_out row is written all the
  *         same.  The slots in range must differ: two rows for one slot
@@ -506,14 +514,14 @@ beam_status beam_moe_kv_read(const beam_moe_attn_cfg* cfg, int32_t B, int32_t N,
  *   z_j = softmax_scale * q . k_j for the tokens j in
  *         [max(0, len - window), len) (window 0: [0, len)), len = seq_lens[b]
  *   out = sum_j softmax(z)_j v_j,   lse = log sum_j exp(z_j)
- * Sums, maxima and the join of the parts are fp32; with a BF16 or FP8_E4M3
- * cache a probability (times the value row's scale) enters the matrix cores as
+ * Sums, maxima and the join of the parts are fp32; with a BF16, FP8_E4M3 or
+ * MXFP4 cache a probability (times the value row's scale) enters the matrix cores as
  * two bf16 parts, off by 2^-15 of it at most.  Values are summed before the
  * division by the probabilities' sum: magnitudes beyond 2^96 may overflow
  * there.
  *   q      [B, n_heads, D] dtype, rows q_stride apart; out [B, n_heads, D]
- *          dtype, dense, must not overlap q.  dtype is BF16 for a BF16 or
- *          FP8_E4M3 cache and F32 for an F32 one.
+ *          dtype, dense, must not overlap q.  dtype is BF16 for a BF16,
+ *          FP8_E4M3 or MXFP4 cache and F32 for an F32 one.
  *   lse    [B, n_heads] fp32 out, nullable (natural logarithm)
  *   page_table as in beam_moe_kv_read; seq_lens [B] int32.  A length below 0
  *          counts as 0 and one beyond the table as the table's
@@ -541,6 +549,65 @@ beam_status beam_moe_attn_decode(const beam_moe_attn_cfg* cfg, int32_t B, const 
 /* Workspace bytes of beam_moe_attn_decode for B sequences of at most max_len
  * tokens (0 for invalid input, and where none is needed). */
 size_t beam_moe_attn_workspace_bytes(const beam_moe_attn_cfg* cfg, int32_t B, int32_t max_len);
+
+/*
+ * beam_moe_attn_decode_sinks -- the same with sinks beside the window: the
+ * first n_sinks tokens of a sequence (0 .. 2^30; 0 is beam_moe_attn_decode)
+ * stay visible when the window has left them behind, so that the tokens j are
+ * those of [max(0, len - window), len) and of [0, min(n_sinks, len)), each
+ * once.  Without a window (0) every token is visible and n_sinks says nothing.
+ */
+beam_status beam_moe_attn_decode_sinks(const beam_moe_attn_cfg* cfg, int32_t n_sinks, int32_t B, const void* q,
+                                       int64_t q_stride, beam_dtype dtype, const beam_moe_kv_cache* cache,
+                                       const int32_t* page_table, int32_t max_pages, const int32_t* seq_lens,
+                                       int32_t max_len, void* out, float* lse,
+                                       void* ws, size_t ws_bytes, void* stream);
+
+/* Workspace bytes of beam_moe_attn_decode_sinks. */
+size_t beam_moe_attn_decode_sinks_workspace_bytes(const beam_moe_attn_cfg* cfg, int32_t n_sinks, int32_t B,
+                                                  int32_t max_len);
+
+/*
+ * beam_moe_attn_prompt -- attention of any number of new tokens per sequence
+ * over its cached tokens (the new tokens' own keys and values are in the cache
+ * already): a prompt, a chunk of one behind a cached prefix, drafted tokens,
+ * single tokens, all in one call.  The new tokens of sequence b are the rows
+ * q_offsets[b] .. q_offsets[b+1] - 1 of q, and the last ones of its
+ * len = seq_lens[b] cached tokens: the i-th of n stands at p = len - n + i and
+ * sees the tokens j <= p with j > p - window, or j < n_sinks, or window 0.
+ * Scores, softmax, out and lse as in beam_moe_attn_decode; here a probability
+ * (with an FP8_E4M3 cache, times the value row's scale) enters the matrix cores
+ * as one rounded bf16 where the cache is not fp32.
+ *   n_sinks   as in beam_moe_attn_decode_sinks
+ *   q         [T, n_heads, D] dtype, rows q_stride apart; out [T, n_heads, D]
+ *             dtype, dense, must not overlap q; dtype as in
+ *             beam_moe_attn_decode
+ *   lse       [T, n_heads] fp32 out, nullable
+ *   q_offsets [B+1] int32, ascending from 0 to at most T.  Rows of out and lse
+ *             at and behind q_offsets[B] are left as they were.
+ *   seq_lens  [B] int32, bounded as in beam_moe_attn_decode.  A row that sees
+ *             no token (one with p < 0 where n > len, too) gets out = 0 and
+ *             lse = -inf.  Tokens on a page outside [0, n_pages) are skipped.
+ *             A token that a row does not see does not reach its result,
+ *             whatever is cached there.
+ *   max_len   the longest length to expect, as in beam_moe_attn_decode: few
+ *             rows over long sequences are split over it
+ *   ws        beam_moe_attn_prompt_workspace_bytes(cfg, n_sinks, B, T, max_len)
+ *             bytes for this B, T and max_len, 16-byte aligned (may be null
+ *             where that is 0); no initialisation; calls that overlap in time
+ *             must not share it.
+ * (T * n_heads / 128 + B * n_kv_heads below 2^24, BEAM_ERR_UNSUPPORTED.)
+ */
+beam_status beam_moe_attn_prompt(const beam_moe_attn_cfg* cfg, int32_t n_sinks, int32_t B, int32_t T, const void* q,
+                                 int64_t q_stride, beam_dtype dtype, const beam_moe_kv_cache* cache,
+                                 const int32_t* page_table, int32_t max_pages, const int32_t* q_offsets,
+                                 const int32_t* seq_lens, int32_t max_len, void* out, float* lse,
+                                 void* ws, size_t ws_bytes, void* stream);
+
+/* Workspace bytes of beam_moe_attn_prompt (0 for invalid input, and where none
+ * is needed). */
+size_t beam_moe_attn_prompt_workspace_bytes(const beam_moe_attn_cfg* cfg, int32_t n_sinks, int32_t B, int32_t T,
+                                            int32_t max_len);
 
 /* Static, human-readable name of a status code. */
 const char* beam_moe_status_string(beam_status status);

@@ -63,3 +63,31 @@ def decode_attention(q, k, v, scale):
         w = e / e.sum(1, keepdims=True)
         out[i], mag[i] = w @ v[:, i], w @ np.abs(v[:, i])
     return out, lse, mag
+
+
+def seen(n, length, window, sinks):
+    """[n, length] truth values: the i-th of n new tokens, at p = length - n + i,
+    sees the tokens j <= p with j > p - window, or j < sinks, or window 0."""
+    p = length - n + np.arange(n)[:, None]
+    j = np.arange(length)[None, :]
+    return (j <= p) & ((j > p - window) | (j < sinks) | (window == 0))
+
+
+def masked_attention(q, k, v, mask, scale):
+    """q [n, h, G, D] over keys and values [L, h, D] where mask [n, L]: (out
+    [n, h, G, D], lse [n, h, G], sum of probabilities times |v|); a row that
+    sees nothing gives 0 and -inf."""
+    n, h, G, D = q.shape
+    out, mag, lse = np.zeros(q.shape), np.zeros(q.shape), np.full((n, h, G), -np.inf)
+    some = mask.any(1)
+    if not some.any():
+        return out, lse, mag
+    m = mask[some][:, None, :]
+    for i in range(h):
+        z = np.where(m, scale * (q[some, i] @ k[:, i].T), -np.inf)     # [rows, G, L]
+        top = z.max(2, keepdims=True)
+        e = np.exp(z - top)
+        lse[some, i] = top[..., 0] + np.log(e.sum(2))
+        w = e / e.sum(2, keepdims=True)
+        out[some, i], mag[some, i] = w @ v[:, i], w @ np.abs(v[:, i])
+    return out, lse, mag

@@ -55,3 +55,28 @@ def test_cached_rows_follow_the_table():
     assert list(there) == [True, False, True, False]
     assert np.array_equal(rows[0], cache[2, :, 0]) and np.array_equal(rows[2], cache[0, :, 3])
     assert not rows[1].any() and not rows[3].any()
+
+
+@pytest.mark.parametrize("n,length,window,sinks", [(5, 5, 0, 0), (4, 20, 6, 0), (9, 30, 5, 3), (30, 30, 7, 2),
+                                                   (3, 2, 0, 0), (1, 40, 8, 100)])
+def test_masked_attention_is_one_query_at_a_time(n, length, window, sinks):
+    g = np.random.default_rng(n * 100 + length)
+    q, k, v = g.standard_normal((n, 2, 3, 16)), g.standard_normal((length, 2, 16)), g.standard_normal((length, 2, 16))
+    mask = oracle.seen(n, length, window, sinks)
+    out, lse, mag = oracle.masked_attention(q, k, v, mask, 0.25)
+    for i in range(n):
+        p = length - n + i
+        j = [t for t in range(p + 1) if not window or p - t < window or t < sinks]
+        assert list(np.nonzero(mask[i])[0]) == j
+        o, l, a = oracle.decode_attention(q[i], k[j], v[j], 0.25)
+        assert np.allclose(out[i], o, atol=1e-13) and np.allclose(lse[i], l) and np.allclose(mag[i], a, atol=1e-13)
+
+
+def test_masked_attention_against_torch():
+    g = np.random.default_rng(3)
+    q, k, v = (g.standard_normal((1, 12, 32)) for _ in range(3))
+    mask = oracle.seen(12, 12, 5, 2)
+    want = torch.nn.functional.scaled_dot_product_attention(*(torch.tensor(x) for x in (q, k, v)),
+                                                            attn_mask=torch.tensor(mask), scale=0.3)[0].numpy()
+    out, _, _ = oracle.masked_attention(q[0][:, None, None], k[0][:, None], v[0][:, None], mask, 0.3)
+    assert np.allclose(out[:, 0, 0], want, atol=1e-13)
