@@ -131,23 +131,13 @@ template <int KIND, int D> struct Lds {
     }
 };
 
-// Zeros, 16 bytes for each lane: what a token that no row sees is read from
-__device__ const uint4 kZeros[64] = {};
+// As many zeros as the rows that a wave stages: what a 16-token block past the
+// end or on a bad page is read from.
+__device__ const uint4 kZeros[512] = {};
 
 BEAM_DEV void to_lds(const void* src, void* dst) {   // dst: the wave's, lane i's 16 bytes at 16 i
     __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) uint32_t*)src,
                                      (__attribute__((address_space(3))) uint32_t*)dst, 16, 0, 0);
-}
-
-BEAM_DEV bool not_finite(uint4 v, bool f32) {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    bool bad = false;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        if (f32) bad |= (w[i] & 0x7F800000u) == 0x7F800000u;
-        else bad |= (w[i] & 0x7F800000u) == 0x7F800000u || (w[i] & 0x7F80u) == 0x7F80u;
-    }
-    return bad;
 }
 
 // A step's keys or values on their way to LDS: what a wave's lanes load of its
@@ -161,7 +151,7 @@ template <int KIND, int D> struct Stage {
     uint4 w[DIRECT ? 1 : N];
     uint32_t s[KIND == A_FP4 ? N : 1];   // FP4: scale bytes
 
-    // rows at `src` (null: zeros) to rows row0 .. of the LDS tile
+    // rows at `src` (the same for the wave) to rows row0 .. of the LDS tile
     template <bool IS_V> BEAM_DEV void load(const uint8_t* src, const uint8_t* scales, uint8_t* tile, int row0) {
         const int lane = threadIdx.x & 63;
         if constexpr (DIRECT) {
@@ -169,16 +159,12 @@ template <int KIND, int D> struct Stage {
             for (int i = 0; i < N; ++i) {
                 const int p = i * 64 + lane, row = row0 + p / L::NP;
                 const int piece = IS_V ? L::vslot(row, p % L::NP) : L::kslot(row, p % L::NP);
-                const void* from = src ? static_cast<const void*>(src + (p / L::NP) * CB + piece * 16) : kZeros + lane;
-                to_lds(from, tile + row0 * L::RB + i * 1024);
+                to_lds(src + (uint32_t)((p / L::NP) * CB + piece * 16), tile + row0 * L::RB + i * 1024);
             }
         } else {
 #pragma unroll
             for (int i = 0; i < N; ++i) {
-                const int p = i * 64 + lane;
-                w[i] = make_uint4(0, 0, 0, 0);
-                if constexpr (KIND == A_FP4) s[i] = 127;
-                if (!src || p >= ROWS * CB / 16) continue;
+                const uint32_t p = min(i * 64 + lane, ROWS * CB / 16 - 1);
                 w[i] = *reinterpret_cast<const uint4*>(src + p * 16);
                 if constexpr (KIND == A_FP4) s[i] = scales[p];   // 16 bytes are a block of 32
             }
@@ -240,8 +226,10 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void beam_attn_prompt(AttnPr
     constexpr int ND = D / 32;
     constexpr int ROWS = Stage<KIND, D>::ROWS;
     constexpr bool SC = KIND == A_FP8;
-    __shared__ __attribute__((aligned(16))) uint8_t sK[2][L::BYTES], sV[2][L::BYTES];
-    __shared__ float sKs[2][SC ? TILE : 1], sVs[2][SC ? TILE : 1];
+    // two buffers of a step's keys and values, variables of their own: so the
+    // compiler sees that reads of one need not wait for loads into the other
+    __shared__ __attribute__((aligned(16))) uint8_t sK0[L::BYTES], sV0[L::BYTES], sK1[L::BYTES], sV1[L::BYTES];
+    __shared__ __attribute__((aligned(16))) float sKs[2][SC ? TILE : 4], sVs[2][SC ? TILE : 4];
     __shared__ int sBad;
 
     const int lane = threadIdx.x & 63;
@@ -300,46 +288,47 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void beam_attn_prompt(AttnPr
 #pragma unroll
     for (int t = 0; t < ND; ++t) o[t] = zeros16();
 
-    const int32_t* table = a.table + (size_t)k.b * a.max_pages;
+    // The pages of a step's 16-token blocks, through the scalar cache; they are
+    // looked up two steps ahead.  Blocks past the end look up the last one.
+    typedef const __attribute__((address_space(4))) int32_t* scalar_ints;
+    const scalar_ints table = (scalar_ints)(uintptr_t)(a.table + (size_t)k.b * a.max_pages);
     const auto token = [&](int place) { return place < k.skip ? place : place + k.gap; };   // of a 16-token block
-    // page of the 16-token block at a place; -1 past the end and where there is none
-    const auto page_of = [&](int place) {
-        if (place >= v1) return -1;
-        const int pg = table[token(place) >> a.c.pshift];
-        return (uint32_t)pg < (uint32_t)a.c.n_pages ? pg : -1;
+    const int last16 = (v1 - 1) & ~15;
+    const auto pages_of = [&](int v, int (&pg)[NB]) {
+#pragma unroll
+        for (int u = 0; u < NB; ++u) pg[u] = table[token(min(v + 16 * u, last16)) >> a.c.pshift];
     };
+    const auto in_cache = [&](int pg) { return (uint32_t)pg < (uint32_t)a.c.n_pages; };
 
     Stage<KIND, D> ck, cv;
     float ksc = 0.f, vsc = 0.f;
-    // the loads of the step at place v, into buffer `buf`
-    const auto load = [&](int v, int buf) {
-        const int place = v + wave * ROWS;
-        const int pg = __builtin_amdgcn_readfirstlane(page_of(place & ~15));
-        const uint8_t *kp = nullptr, *vp = nullptr, *kss = nullptr, *vss = nullptr;
-        size_t at_row = 0;
-        if (pg >= 0) {
-            at_row = (((size_t)pg * a.Hkv + head) << a.c.pshift) +
-                     ((token(place & ~15) + (place & 15)) & ((1 << a.c.pshift) - 1));
+    // the loads of the step at place v, into one of the buffers
+    const auto load = [&](int v, const int (&pg)[NB], uint8_t* sK, uint8_t* sV) {
+        const int row = wave * ROWS, place = v + (row & ~15);
+        int page = 0;
+#pragma unroll
+        for (int u = 0; u < NB; ++u) page |= pg[u] & -(int)(row / 16 == u);
+        const uint8_t *kp, *vp, *kss, *vss;
+        kp = vp = kss = vss = reinterpret_cast<const uint8_t*>(kZeros);
+        if (place < v1 && in_cache(page)) {
+            const size_t at_row = (((size_t)page * a.Hkv + head) << a.c.pshift) +
+                                  ((token(place) + (row & 15)) & ((1 << a.c.pshift) - 1));
             kp = static_cast<const uint8_t*>(a.c.k) + at_row * Stage<KIND, D>::CB;
             vp = static_cast<const uint8_t*>(a.c.v) + at_row * Stage<KIND, D>::CB;
-            if constexpr (KIND == A_FP4) {
-                kss = static_cast<const uint8_t*>(a.c.ks) + at_row * (D / 32);
-                vss = static_cast<const uint8_t*>(a.c.vs) + at_row * (D / 32);
-            }
+            constexpr int SB = KIND == A_FP4 ? D / 32 : 4;   // scale bytes per row
+            kss = static_cast<const uint8_t*>(a.c.ks) + at_row * SB;
+            vss = static_cast<const uint8_t*>(a.c.vs) + at_row * SB;
         }
-        ck.template load<false>(kp, kss, sK[buf], wave * ROWS);
-        cv.template load<true>(vp, vss, sV[buf], wave * ROWS);
+        ck.template load<false>(kp, kss, sK, row);
+        cv.template load<true>(vp, vss, sV, row);
         if constexpr (SC) {
-            ksc = vsc = 0.f;
-            if (pg >= 0 && lane < ROWS) {
-                ksc = static_cast<const float*>(a.c.ks)[at_row + lane];
-                vsc = static_cast<const float*>(a.c.vs)[at_row + lane];
-            }
+            ksc = reinterpret_cast<const float*>(kss)[lane % ROWS];
+            vsc = reinterpret_cast<const float*>(vss)[lane % ROWS];
         }
     };
-    const auto store = [&](int buf) {
-        ck.template store<false>(sK[buf], wave * ROWS);
-        cv.template store<true>(sV[buf], wave * ROWS);
+    const auto store = [&](uint8_t* sK, uint8_t* sV, int buf) {
+        ck.template store<false>(sK, wave * ROWS);
+        cv.template store<true>(sV, wave * ROWS);
         if constexpr (SC) {
             if (lane < ROWS) {
                 sKs[buf][wave * ROWS + lane] = ksc;
@@ -349,38 +338,96 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void beam_attn_prompt(AttnPr
     };
 
     if (threadIdx.x == 0) sBad = -1;
-    load(v0, 0);
-    store(0);
-    int buf = 0;
-    for (int v = v0; v < v1; v += TILE, buf ^= 1) {
+    int pg[NB], next[NB];
+    if (v0 < v1) {
+        pages_of(v0, pg);
+        load(v0, pg, sK0, sV0);
+        pages_of(v0 + TILE, next);
+        store(sK0, sV0, 0);
+    }
+    // one step: buffer `buf` (sK, sV) is worked on while the other (oK, oV) fills
+    const auto step = [&](int v, int buf, uint8_t* sK, uint8_t* sV, uint8_t* oK, uint8_t* oV) {
         __builtin_amdgcn_s_waitcnt(0);   // this wave's loads to LDS have landed
         __syncthreads();                 // everyone's, and no one reads the other buffer any more
         const bool more = v + TILE < v1;
-        if (more) load(v + TILE, buf ^ 1);
-
         // whether every row of the block, and of the wave, sees all of the step's tokens
-        bool all = true, mine = true;
-        uint32_t there = 0;              // 16-token blocks that are in the cache
+        const int t0 = token(v), t1 = t0 + TILE - 1;
+        bool ok = v + TILE <= v1 && (v >= k.skip || v + TILE <= k.skip);
 #pragma unroll
-        for (int u = 0; u < NB; ++u) {
-            const int place = v + 16 * u, t = token(place);
-            const bool ok = page_of(place) >= 0;
-            there |= ok ? 1u << u : 0u;
-            all &= ok && t + 15 <= k.p0 && (a.window == 0 || t > k.p1 - a.window || t + 15 < a.sinks);
-            mine &= ok && t + 15 <= wlo && (a.window == 0 || t > whi - a.window || t + 15 < a.sinks);
+        for (int u = 0; u < NB; ++u) ok = ok && in_cache(pg[u]);
+        const bool all = ok && t1 <= k.p0 && (a.window == 0 || t0 > k.p1 - a.window || t1 < a.sinks);
+        const bool mine = ok && t1 <= wlo && (a.window == 0 || t0 > whi - a.window || t1 < a.sinks);
+        uint32_t there = 0;              // 16-token blocks that there are
+#pragma unroll
+        for (int u = 0; u < NB; ++u) there |= v + 16 * u < v1 && in_cache(pg[u]) ? 1u << u : 0u;
+        if (more) {
+            load(v + TILE, next, oK, oV);
+#pragma unroll
+            for (int u = 0; u < NB; ++u) pg[u] = next[u];
+            pages_of(v + 2 * TILE, next);
         }
+        const auto sees = [&](int u, int x) {   // whether this lane's row sees token x of the step's 16-token block u
+            const int tok = token(v + 16 * u) + x;
+            return (there >> u & 1) && tok <= pos && (a.window == 0 || tok > pos - a.window || tok < a.sinks);
+        };
         // A value that is not finite must not reach rows that do not see it: 0
         // times it is NaN.  Where rows differ in what they see, the step's values
-        // are looked through first.
-        bool bad = false;
+        // are looked through first.  If one is not finite, it is added to the
+        // rows that see it, with any weight, and is 0 in LDS from there on.
         if (!all) {
-            bool mine_bad = false;
-            const uint8_t* p = sV[buf] + wave * ROWS * L::RB;
-            for (int i = lane; i < ROWS * L::NP; i += 64)
-                mine_bad |= not_finite(*reinterpret_cast<const uint4*>(p + i * 16), KIND == A_F32);
-            if (__any(mine_bad) && lane == 0) sBad = v;
+            const auto mend = [&](bool set) {
+                bool bad = false;
+                uint8_t* p = sV + wave * ROWS * L::RB;
+                for (int i = lane; i < ROWS * L::NP; i += 64) {
+                    uint4* w = reinterpret_cast<uint4*>(p + i * 16);
+                    uint32_t x[4] = {w->x, w->y, w->z, w->w};
+                    bool here = false;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        if ((x[e] & 0x7F800000u) == 0x7F800000u) {
+                            x[e] &= KIND == A_F32 ? 0u : 0x0000FFFFu;
+                            here = true;
+                        }
+                        if (KIND != A_F32 && (x[e] & 0x7F80u) == 0x7F80u) {
+                            x[e] &= 0xFFFF0000u;
+                            here = true;
+                        }
+                    }
+                    if (set && here) *w = make_uint4(x[0], x[1], x[2], x[3]);
+                    bad |= here;
+                }
+                return bad;
+            };
+            if (__any(mend(false)) && lane == 0) sBad = v;
             __syncthreads();
-            bad = sBad == v;
+            if (sBad == v) {
+#pragma unroll 1
+                for (int y = 0; y < TILE; ++y) {
+                    const bool add = sees(y / 16, y % 16);
+#pragma unroll
+                    for (int t = 0; t < ND; ++t)
+#pragma unroll
+                        for (int i = 0; i < 16; i += 4) {
+                            const int e = 32 * t + 2 * i + 4 * h;
+                            const uint8_t* w = sV + y * L::RB + L::vslot(y, e * L::ES / 16) * 16 + e * L::ES % 16;
+                            float x[4];
+                            if constexpr (KIND == A_F32) {
+                                const float4 f = *reinterpret_cast<const float4*>(w);
+                                x[0] = f.x; x[1] = f.y; x[2] = f.z; x[3] = f.w;
+                            } else {
+                                const uint2 f = *reinterpret_cast<const uint2*>(w);
+                                x[0] = __uint_as_float(f.x << 16); x[1] = __uint_as_float(f.x & 0xFFFF0000u);
+                                x[2] = __uint_as_float(f.y << 16); x[3] = __uint_as_float(f.y & 0xFFFF0000u);
+                            }
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)   // x - x: 0, or NaN
+                                o[t][i + j] += (add & (x[j] - x[j] != 0.f)) ? x[j] : 0.f;
+                        }
+                }
+                __syncthreads();
+                mend(true);
+                __syncthreads();
+            }
         }
 
         // scores: lane (r, h) gets row r, tokens 32 t + 8 (i / 4) + 4 h + i % 4
@@ -391,7 +438,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void beam_attn_prompt(AttnPr
 #pragma unroll
             for (int c = 0; c < NQ; ++c) {
                 const int kr = 32 * t + r;
-                const uint4 kf = *reinterpret_cast<const uint4*>(sK[buf] + kr * L::RB + L::kslot(kr, 2 * c + h) * 16);
+                const uint4 kf = *reinterpret_cast<const uint4*>(sK + kr * L::RB + L::kslot(kr, 2 * c + h) * 16);
                 if constexpr (KIND == A_F32) {
                     const uint32_t kw[4] = {kf.x, kf.y, kf.z, kf.w}, qw[4] = {qf[c].x, qf[c].y, qf[c].z, qf[c].w};
 #pragma unroll
@@ -415,13 +462,8 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void beam_attn_prompt(AttnPr
 #pragma unroll
             for (int t = 0; t < NT; ++t)
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const int u = 2 * t + i / 8;
-                    const int tok = token(v + 16 * u) + 8 * (i / 4 % 2) + 4 * h + i % 4;
-                    const bool live = (there >> u & 1) && tok <= pos &&
-                                      (a.window == 0 || tok > pos - a.window || tok < a.sinks);
-                    z[t][i] = live ? z[t][i] : -INFINITY;
-                }
+                for (int i = 0; i < 16; ++i)
+                    z[t][i] = sees(2 * t + i / 8, 8 * (i / 4 % 2) + 4 * h + i % 4) ? z[t][i] : -INFINITY;
         }
         // The reference moves (and what was summed is rescaled) only when a
         // score exceeds it by 8 powers of two.
@@ -490,7 +532,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void beam_attn_prompt(AttnPr
                 // i / 4 and elements 4 (i % 4) .. + 3, and get element i of each
                 const int i = lane & 15, vr = 16 * s + 8 * y + 4 * h + i / 4;
                 const int e = 32 * t + (lane & 16) + 4 * (i % 4);
-                const uint8_t* p = sV[buf] + vr * L::RB + L::vslot(vr, e / 8) * 16 + (e % 8) * 2;
+                const uint8_t* p = sV + vr * L::RB + L::vslot(vr, e / 8) * 16 + (e % 8) * 2;
                 const uint2 x = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
                                                               (__attribute__((address_space(3))) s16x4*)p));
                 w[2 * y] = x.x;
@@ -501,64 +543,28 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void beam_attn_prompt(AttnPr
         };
         const auto vword = [&](int t, int i) {   // fp32: element 32 t + lane % 32 of token 8 (i / 4) + 4 h + i % 4
             const int vr = 8 * (i / 4) + 4 * h + i % 4, e = 32 * t + r;
-            return *reinterpret_cast<const float*>(sV[buf] + vr * L::RB + L::vslot(vr, e / 4) * 16 + (e % 4) * 4);
+            return *reinterpret_cast<const float*>(sV + vr * L::RB + L::vslot(vr, e / 4) * 16 + (e % 4) * 4);
         };
-        if (!bad) {
 #pragma unroll
-            for (int t = 0; t < ND; ++t) {
-                if constexpr (KIND == A_F32) {
+        for (int t = 0; t < ND; ++t) {
+            if constexpr (KIND == A_F32) {
 #pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        o[t] = __builtin_amdgcn_mfma_f32_32x32x2f32(vword(t, i), z[0][i], o[t], 0, 0, 0);
-                } else {
+                for (int i = 0; i < 16; ++i)
+                    o[t] = __builtin_amdgcn_mfma_f32_32x32x2f32(vword(t, i), z[0][i], o[t], 0, 0, 0);
+            } else {
 #pragma unroll
-                    for (int s = 0; s < NB; ++s)
-                        o[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-                            __builtin_bit_cast(bf16x8, vfrag(t, s)),
-                            __builtin_bit_cast(bf16x8, make_uint4(pb[4 * s], pb[4 * s + 1], pb[4 * s + 2], pb[4 * s + 3])),
-                            o[t], 0, 0, 0);
-                }
-            }
-        } else {
-            // once per position of the wave, with the values that it does not see
-            // as zeros; a lane keeps its own position's sums
-#pragma unroll
-            for (int t = 0; t < ND; ++t) {
-                f32x16 mine_o = o[t];
-                for (int pq = wlo; pq <= whi; ++pq) {
-                    const auto sees = [&](int u, int x) {   // token x of 16-token block u
-                        const int tok = token(v + 16 * u) + x;
-                        return (there >> u & 1) && tok <= pq && (a.window == 0 || tok > pq - a.window || tok < a.sinks);
-                    };
-                    f32x16 acc = o[t];
-                    if constexpr (KIND == A_F32) {
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            const float x = sees(i / 8, 8 * (i / 4 % 2) + 4 * h + i % 4) ? vword(t, i) : 0.f;
-                            acc = __builtin_amdgcn_mfma_f32_32x32x2f32(x, z[0][i], acc, 0, 0, 0);
-                        }
-                    } else {
-#pragma unroll
-                        for (int s = 0; s < NB; ++s) {
-                            const uint4 f = vfrag(t, s);
-                            uint32_t w[4] = {f.x, f.y, f.z, f.w};
-#pragma unroll
-                            for (int j = 0; j < 8; ++j)
-                                if (!sees(s, 8 * (j / 4) + 4 * h + j % 4)) w[j / 2] &= j % 2 ? 0x0000FFFFu : 0xFFFF0000u;
-                            acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-                                __builtin_bit_cast(bf16x8, make_uint4(w[0], w[1], w[2], w[3])),
-                                __builtin_bit_cast(bf16x8,
-                                                   make_uint4(pb[4 * s], pb[4 * s + 1], pb[4 * s + 2], pb[4 * s + 3])),
-                                acc, 0, 0, 0);
-                        }
-                    }
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) mine_o[i] = pos == pq ? acc[i] : mine_o[i];
-                }
-                o[t] = mine_o;
+                for (int s = 0; s < NB; ++s)
+                    o[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+                        __builtin_bit_cast(bf16x8, vfrag(t, s)),
+                        __builtin_bit_cast(bf16x8, make_uint4(pb[4 * s], pb[4 * s + 1], pb[4 * s + 2], pb[4 * s + 3])),
+                        o[t], 0, 0, 0);
             }
         }
-        if (more) store(buf ^ 1);
+        if (more) store(oK, oV, buf ^ 1);
+    };
+    for (int v = v0; v < v1; v += 2 * TILE) {
+        step(v, 0, sK0, sV0, sK1, sV1);
+        if (v + TILE < v1) step(v + TILE, 1, sK1, sV1, sK0, sV0);
     }
 
     // o[t][i] of lane (r, h) is row r, element 32 t + 8 (i / 4) + 4 h + i % 4

@@ -157,7 +157,7 @@ def check_prompt(cfg, kind, q, c, vals, table, off, lens, max_len, name, lse=Tru
         assert (gl[T:] == 9).all()
         gl = gl[:T]
         assert np.array_equal(np.isneginf(gl), inf), name
-        worst = np.max((np.abs(gl - rl) - el)[~inf], initial=-1)
+        worst = np.max(np.abs(gl[~inf] - rl[~inf]) - el[~inf], initial=-1)
         say(f"  {name}: lse over the bound by {worst:.2e}")
         assert worst <= 0, name
     return out, ls
@@ -685,7 +685,8 @@ def test_every_four_bit_code_and_scale_reads_back():
     ko, vo = (torch.empty((256, 1, 64), device=DEV) for _ in range(2))
     beam.beam_moe_kv_read(cfg, c, i32([[0]]), i32([0, 256]), ko, vo)
     for got, t, sc in ((ko, c.k, c.k_scale), (vo, c.v, c.v_scale)):
-        want = mx_values(t, sc)[0, 0].astype(np.float32)
+        with np.errstate(over="ignore"):
+            want = mx_values(t, sc)[0, 0].astype(np.float32)
         g = got.cpu().numpy()[:, 0]
         assert np.array_equal(np.isnan(want), np.isnan(g))
         assert np.array_equal(want[~np.isnan(want)], g[~np.isnan(want)])
