@@ -43,6 +43,9 @@ struct Block {
 };
 
 BEAM_DEV int prompt_offset(const AttnPromptArgs& a, int b) { return min(max(a.offsets[b], 0), a.T); }
+BEAM_DEV int first_block_at(const AttnPromptArgs& a, int b, int offset) {
+    return (int)((int64_t)offset * a.G / kPromptRows) + b;
+}
 
 // places that the rows of positions p0 .. p1 see
 BEAM_DEV void block_span(const AttnPromptArgs& a, Block& k) {
@@ -117,7 +120,7 @@ BEAM_DEV int sequence_of(const AttnPromptArgs& a, int idx) {
 // time in one column of pieces, values four rows at a time in four.
 template <int KIND, int D> struct Lds {
     static constexpr int ES = KIND == A_F32 ? 4 : 2;
-    static constexpr int TILE = KIND == A_F32 ? 32 : 64;
+    static constexpr int TILE = KIND == A_F32 || D == 256 ? 32 : 64;
     static constexpr int RB = D * ES, NP = RB / 16;
     static constexpr int BYTES = TILE * RB;
     static BEAM_DEV int kslot(int row, int piece) {
@@ -345,6 +348,13 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void beam_attn_prompt(AttnPr
         pages_of(v0 + TILE, next);
         store(sK0, sV0, 0);
     }
+    // Byte places in LDS of this lane's key piece 2 c + h of row 32 t + r, and of
+    // its four value elements for a transposing read: the exchange of pieces is an
+    // exclusive or, so piece and block enter by one.
+    const int i16 = lane & 15;
+    int kat = r * L::RB + L::kslot(r, h) * 16;                    // ^ 32 c, + 32 t RB
+    int vat = (4 * h + i16 / 4) * L::RB +
+              L::vslot(4 * h + i16 / 4, (lane & 16) / 8 + i16 % 4 / 2) * 16 + i16 % 2 * 8;   // ^ (64 t + 32 y), + (16 s + 8 y) RB
     // one step: buffer `buf` (sK, sV) is worked on while the other (oK, oV) fills
     const auto step = [&](int v, int buf, uint8_t* sK, uint8_t* sV, uint8_t* oK, uint8_t* oV) {
         __builtin_amdgcn_s_waitcnt(0);   // this wave's loads to LDS have landed
@@ -430,6 +440,9 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void beam_attn_prompt(AttnPr
             }
         }
 
+        // the registers that 256 elements leave hold no sixteen places
+        if constexpr (D == 256) asm volatile("" : "+v"(kat), "+v"(vat));
+
         // scores: lane (r, h) gets row r, tokens 32 t + 8 (i / 4) + 4 h + i % 4
         f32x16 z[NT];
 #pragma unroll
@@ -437,8 +450,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void beam_attn_prompt(AttnPr
             z[t] = zeros16();
 #pragma unroll
             for (int c = 0; c < NQ; ++c) {
-                const int kr = 32 * t + r;
-                const uint4 kf = *reinterpret_cast<const uint4*>(sK + kr * L::RB + L::kslot(kr, 2 * c + h) * 16);
+                const uint4 kf = *reinterpret_cast<const uint4*>(sK + (kat ^ (32 * c)) + 32 * t * L::RB);
                 if constexpr (KIND == A_F32) {
                     const uint32_t kw[4] = {kf.x, kf.y, kf.z, kf.w}, qw[4] = {qf[c].x, qf[c].y, qf[c].z, qf[c].w};
 #pragma unroll
@@ -530,9 +542,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void beam_attn_prompt(AttnPr
             for (int y = 0; y < 2; ++y) {
                 // the 16 lanes of a group read four rows of 16 elements, lane i row
                 // i / 4 and elements 4 (i % 4) .. + 3, and get element i of each
-                const int i = lane & 15, vr = 16 * s + 8 * y + 4 * h + i / 4;
-                const int e = 32 * t + (lane & 16) + 4 * (i % 4);
-                const uint8_t* p = sV + vr * L::RB + L::vslot(vr, e / 8) * 16 + (e % 8) * 2;
+                const uint8_t* p = sV + (vat ^ (64 * t + 32 * y)) + (16 * s + 8 * y) * L::RB;
                 const uint2 x = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
                                                               (__attribute__((address_space(3))) s16x4*)p));
                 w[2 * y] = x.x;
