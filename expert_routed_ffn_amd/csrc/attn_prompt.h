@@ -120,7 +120,7 @@ BEAM_DEV int sequence_of(const AttnPromptArgs& a, int idx) {
 // time in one column of pieces, values four rows at a time in four.
 template <int KIND, int D> struct Lds {
     static constexpr int ES = KIND == A_F32 ? 4 : 2;
-    static constexpr int TILE = KIND == A_F32 || D == 256 ? 32 : 64;
+    static constexpr int TILE = KIND == A_F32 ? 32 : 64;
     static constexpr int RB = D * ES, NP = RB / 16;
     static constexpr int BYTES = TILE * RB;
     static BEAM_DEV int kslot(int row, int piece) {
@@ -203,7 +203,7 @@ template <int KIND, int D> struct Stage {
     }
 };
 
-// ---------------------------------------------------------------- the kernel
+// ---------------------------------------------------------------- rows
 
 BEAM_DEV float max_halves(float v) {
     const auto q = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
@@ -220,409 +220,166 @@ BEAM_DEV f32x16 zeros16() {
     return z;
 }
 
-template <int KIND, int D>
-__global__ __launch_bounds__(256, D == 256 ? 1 : 2) void beam_attn_prompt(AttnPromptArgs a) {
-    using L = Lds<KIND, D>;
-    constexpr int TILE = L::TILE, NT = TILE / 32;    // 32-token blocks of a step
-    constexpr int NB = TILE / 16;                    // 16-token blocks of a step
-    constexpr int NQ = KIND == A_F32 ? D / 8 : D / 16;   // 16-byte query pieces per lane
-    constexpr int ND = D / 32;
-    constexpr int ROWS = Stage<KIND, D>::ROWS;
-    constexpr bool SC = KIND == A_FP8;
-    // two buffers of a step's keys and values, variables of their own: so the
-    // compiler sees that reads of one need not wait for loads into the other
-    __shared__ __attribute__((aligned(16))) uint8_t sK0[L::BYTES], sV0[L::BYTES], sK1[L::BYTES], sV1[L::BYTES];
-    __shared__ __attribute__((aligned(16))) float sKs[2][SC ? TILE : 4], sVs[2][SC ? TILE : 4];
-    __shared__ int sBad;
 
-    const int lane = threadIdx.x & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int r = lane & 31, h = lane >> 5;
-    const int head = blockIdx.x % a.Hkv, G = a.G;
-    const int at = blockIdx.x / a.Hkv;
+// A wave's 32 rows, one to a lane: lanes r and r + 32 hold row r.  Rows past the
+// block's last repeat it.
+struct Rows {
+    int qi, qg, pos;         // query token and head of this lane's row, its position
+    int lo, hi;              // the wave's first and last position
+    bool live;
+};
+BEAM_DEV Rows rows_of(const AttnPromptArgs& a, const Block& k, int wave) {
+    const int r = threadIdx.x & 31, w0 = k.row0 + wave * 32, end = k.row1 - 1;
+    Rows x;
+    const int row = min(w0 + r, end);
+    x.qi = row / a.G;
+    x.qg = row - x.qi * a.G;
+    x.pos = k.len - k.n + x.qi;
+    x.lo = k.len - k.n + min(w0, end) / a.G;
+    x.hi = k.len - k.n + min(w0 + 31, end) / a.G;
+    x.live = w0 + r < k.row1;
+    return x;
+}
 
-    // the block and the part: parts 1 .. of the sequences in one block come first,
-    // then the blocks, a sequence's last ones, which see most, first
-    Block k;
-    int part = 0, slot;
+// The workgroup's block, its part of it and that part's place in the workspace;
+// false: there is none.  Parts 1 .. of the sequences in one block come first, then
+// the blocks, a sequence's last ones, which see most, first.
+BEAM_DEV bool block_part(const AttnPromptArgs& a, Block& k, int* part, size_t* slot) {
+    const int at = blockIdx.x / a.Hkv, S = (int)a.p.S;
+    int idx = (int)a.p.blocks - 1 - at, s = 0;
     if (a.p.every) {
-        const int idx = (int)a.p.blocks - 1 - at;
-        const int b = sequence_of(a, idx);
-        if (!block_of(a, b, idx - first_block(a, b), k)) return;
-        part = blockIdx.y;
-        slot = idx * (int)a.p.S + part;
+        s = blockIdx.y;
     } else {
-        const int extra = a.B * ((int)a.p.S - 1);
+        const int extra = a.B * (S - 1);
         if (at < extra) {
-            const int b = at / ((int)a.p.S - 1);
-            part = 1 + at % ((int)a.p.S - 1);
-            if (!block_of(a, b, 0, k)) return;
-        } else {
-            const int idx = (int)a.p.blocks - 1 - (at - extra);
-            const int b = sequence_of(a, idx);
-            if (!block_of(a, b, idx - first_block(a, b), k)) return;
+            s = 1 + at % (S - 1);
+            *part = s;
+            *slot = (size_t)(at / (S - 1)) * S + s;
+            return block_of(a, at / (S - 1), 0, k) && s < k.np;
         }
-        slot = k.b * (int)a.p.S + part;
+        idx += extra;
     }
-    if (part >= k.np) return;
-    const int v0 = k.base + part * k.part;
-    const int v1 = part + 1 < k.np ? v0 + k.part : k.end;
+    const int b = sequence_of(a, idx);
+    if (!block_of(a, b, idx - first_block(a, b), k)) return false;
+    *part = s;
+    *slot = (size_t)(a.p.every ? idx : b) * S + s;
+    return s < k.np;
+}
 
-    // this lane's row and query; rows past the block's last repeat it
-    const int row = min(k.row0 + wave * 32 + r, k.row1 - 1);
-    const int qi = row / G, qg = row - qi * G;
-    const int pos = k.len - k.n + qi;
-    const int wlo = k.len - k.n + min(k.row0 + wave * 32, k.row1 - 1) / G;        // the wave's first and last position
-    const int whi = k.len - k.n + min(k.row0 + wave * 32 + 31, k.row1 - 1) / G;
-    uint4 qf[NQ];
-    {
-        const size_t off = (size_t)(k.first + qi) * a.qs + (size_t)(head * G + qg) * D;
-        const uint4* q = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.q) + off * L::ES);
+// The value rows of a wave in LDS, rows row0 .. of a tile: whether an element is
+// not finite; SET: 0 in its place.
+template <int KIND, int D, bool SET> BEAM_DEV bool find_not_finite(uint8_t* tile, int row0) {
+    using L = Lds<KIND, D>;
+    bool bad = false;
+    for (int i = threadIdx.x & 63; i < L::TILE / kPromptWaves * L::NP; i += 64) {
+        uint4* w = reinterpret_cast<uint4*>(tile + row0 * L::RB + i * 16);
+        uint32_t x[4] = {w->x, w->y, w->z, w->w};
+        bool here = false;
 #pragma unroll
-        for (int c = 0; c < NQ; ++c) qf[c] = q[2 * c + h];
-    }
-
-    const float zs = a.scale * kLog2e;
-    // reference that the probabilities are relative to, this lane's share of
-    // their sum, and (BF) of their sum before they were rounded, which lse needs
-    constexpr bool BF = KIND == A_BF16 || KIND == A_FP4;
-    float m = -INFINITY, l = 0.f, lx = 0.f;
-    f32x16 o[ND];
-#pragma unroll
-    for (int t = 0; t < ND; ++t) o[t] = zeros16();
-
-    // The pages of a step's 16-token blocks, through the scalar cache; they are
-    // looked up two steps ahead.  Blocks past the end look up the last one.
-    typedef const __attribute__((address_space(4))) int32_t* scalar_ints;
-    const scalar_ints table = (scalar_ints)(uintptr_t)(a.table + (size_t)k.b * a.max_pages);
-    const auto token = [&](int place) { return place < k.skip ? place : place + k.gap; };   // of a 16-token block
-    const int last16 = (v1 - 1) & ~15;
-    const auto pages_of = [&](int v, int (&pg)[NB]) {
-#pragma unroll
-        for (int u = 0; u < NB; ++u) pg[u] = table[token(min(v + 16 * u, last16)) >> a.c.pshift];
-    };
-    const auto in_cache = [&](int pg) { return (uint32_t)pg < (uint32_t)a.c.n_pages; };
-
-    Stage<KIND, D> ck, cv;
-    float ksc = 0.f, vsc = 0.f;
-    // the loads of the step at place v, into one of the buffers
-    const auto load = [&](int v, const int (&pg)[NB], uint8_t* sK, uint8_t* sV) {
-        const int row = wave * ROWS, place = v + (row & ~15);
-        int page = 0;
-#pragma unroll
-        for (int u = 0; u < NB; ++u) page |= pg[u] & -(int)(row / 16 == u);
-        const uint8_t *kp, *vp, *kss, *vss;
-        kp = vp = kss = vss = reinterpret_cast<const uint8_t*>(kZeros);
-        if (place < v1 && in_cache(page)) {
-            const size_t at_row = (((size_t)page * a.Hkv + head) << a.c.pshift) +
-                                  ((token(place) + (row & 15)) & ((1 << a.c.pshift) - 1));
-            kp = static_cast<const uint8_t*>(a.c.k) + at_row * Stage<KIND, D>::CB;
-            vp = static_cast<const uint8_t*>(a.c.v) + at_row * Stage<KIND, D>::CB;
-            constexpr int SB = KIND == A_FP4 ? D / 32 : 4;   // scale bytes per row
-            kss = static_cast<const uint8_t*>(a.c.ks) + at_row * SB;
-            vss = static_cast<const uint8_t*>(a.c.vs) + at_row * SB;
-        }
-        ck.template load<false>(kp, kss, sK, row);
-        cv.template load<true>(vp, vss, sV, row);
-        if constexpr (SC) {
-            ksc = reinterpret_cast<const float*>(kss)[lane % ROWS];
-            vsc = reinterpret_cast<const float*>(vss)[lane % ROWS];
-        }
-    };
-    const auto store = [&](uint8_t* sK, uint8_t* sV, int buf) {
-        ck.template store<false>(sK, wave * ROWS);
-        cv.template store<true>(sV, wave * ROWS);
-        if constexpr (SC) {
-            if (lane < ROWS) {
-                sKs[buf][wave * ROWS + lane] = ksc;
-                sVs[buf][wave * ROWS + lane] = vsc;
+        for (int e = 0; e < 4; ++e) {
+            if ((x[e] & 0x7F800000u) == 0x7F800000u) {
+                x[e] &= KIND == A_F32 ? 0u : 0x0000FFFFu;
+                here = true;
+            }
+            if (KIND != A_F32 && (x[e] & 0x7F80u) == 0x7F80u) {
+                x[e] &= 0xFFFF0000u;
+                here = true;
             }
         }
-    };
-
-    if (threadIdx.x == 0) sBad = -1;
-    int pg[NB], next[NB];
-    if (v0 < v1) {
-        pages_of(v0, pg);
-        load(v0, pg, sK0, sV0);
-        pages_of(v0 + TILE, next);
-        store(sK0, sV0, 0);
+        if (SET && here) *w = make_uint4(x[0], x[1], x[2], x[3]);
+        bad |= here;
     }
-    // Byte places in LDS of this lane's key piece 2 c + h of row 32 t + r, and of
-    // its four value elements for a transposing read: the exchange of pieces is an
-    // exclusive or, so piece and block enter by one.
-    const int i16 = lane & 15;
-    int kat = r * L::RB + L::kslot(r, h) * 16;                    // ^ 32 c, + 32 t RB
-    int vat = (4 * h + i16 / 4) * L::RB +
-              L::vslot(4 * h + i16 / 4, (lane & 16) / 8 + i16 % 4 / 2) * 16 + i16 % 2 * 8;   // ^ (64 t + 32 y), + (16 s + 8 y) RB
-    // one step: buffer `buf` (sK, sV) is worked on while the other (oK, oV) fills
-    const auto step = [&](int v, int buf, uint8_t* sK, uint8_t* sV, uint8_t* oK, uint8_t* oV) {
-        __builtin_amdgcn_s_waitcnt(0);   // this wave's loads to LDS have landed
-        __syncthreads();                 // everyone's, and no one reads the other buffer any more
-        const bool more = v + TILE < v1;
-        // whether every row of the block, and of the wave, sees all of the step's tokens
-        const int t0 = token(v), t1 = t0 + TILE - 1;
-        bool ok = v + TILE <= v1 && (v >= k.skip || v + TILE <= k.skip);
-#pragma unroll
-        for (int u = 0; u < NB; ++u) ok = ok && in_cache(pg[u]);
-        const bool all = ok && t1 <= k.p0 && (a.window == 0 || t0 > k.p1 - a.window || t1 < a.sinks);
-        const bool mine = ok && t1 <= wlo && (a.window == 0 || t0 > whi - a.window || t1 < a.sinks);
-        uint32_t there = 0;              // 16-token blocks that there are
-#pragma unroll
-        for (int u = 0; u < NB; ++u) there |= v + 16 * u < v1 && in_cache(pg[u]) ? 1u << u : 0u;
-        if (more) {
-            load(v + TILE, next, oK, oV);
-#pragma unroll
-            for (int u = 0; u < NB; ++u) pg[u] = next[u];
-            pages_of(v + 2 * TILE, next);
-        }
-        const auto sees = [&](int u, int x) {   // whether this lane's row sees token x of the step's 16-token block u
-            const int tok = token(v + 16 * u) + x;
-            return (there >> u & 1) && tok <= pos && (a.window == 0 || tok > pos - a.window || tok < a.sinks);
-        };
-        // A value that is not finite must not reach rows that do not see it: 0
-        // times it is NaN.  Where rows differ in what they see, the step's values
-        // are looked through first.  If one is not finite, it is added to the
-        // rows that see it, with any weight, and is 0 in LDS from there on.
-        if (!all) {
-            const auto mend = [&](bool set) {
-                bool bad = false;
-                uint8_t* p = sV + wave * ROWS * L::RB;
-                for (int i = lane; i < ROWS * L::NP; i += 64) {
-                    uint4* w = reinterpret_cast<uint4*>(p + i * 16);
-                    uint32_t x[4] = {w->x, w->y, w->z, w->w};
-                    bool here = false;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        if ((x[e] & 0x7F800000u) == 0x7F800000u) {
-                            x[e] &= KIND == A_F32 ? 0u : 0x0000FFFFu;
-                            here = true;
-                        }
-                        if (KIND != A_F32 && (x[e] & 0x7F80u) == 0x7F80u) {
-                            x[e] &= 0xFFFF0000u;
-                            here = true;
-                        }
-                    }
-                    if (set && here) *w = make_uint4(x[0], x[1], x[2], x[3]);
-                    bad |= here;
-                }
-                return bad;
-            };
-            if (__any(mend(false)) && lane == 0) sBad = v;
-            __syncthreads();
-            if (sBad == v) {
+    return bad;
+}
+
+// A value that is not finite must not reach rows that do not see it: 0 times it
+// is NaN.  Where rows differ in what they see of a tile, all waves look its
+// values through first (`tag` tells the tiles apart).  If one is not finite, it
+// is added to the sums of the rows that see it, with any weight, and is 0 in LDS
+// from there on.  sees(x): whether this lane's row sees token x of the tile.
+template <int KIND, int D, typename Sees>
+BEAM_DEV void mend_values(uint8_t* tile, int wave, int tag, int* flag, f32x16 (&o)[D / 32], Sees sees) {
+    using L = Lds<KIND, D>;
+    const int lane = threadIdx.x & 63, h = lane >> 5, row0 = wave * (L::TILE / kPromptWaves);
+    if (__any(find_not_finite<KIND, D, false>(tile, row0)) && lane == 0) *flag = tag;
+    __syncthreads();
+    if (*flag != tag) return;
 #pragma unroll 1
-                for (int y = 0; y < TILE; ++y) {
-                    const bool add = sees(y / 16, y % 16);
+    for (int y = 0; y < L::TILE; ++y) {
+        const bool add = sees(y);
 #pragma unroll
-                    for (int t = 0; t < ND; ++t)
+        for (int t = 0; t < D / 32; ++t)
 #pragma unroll
-                        for (int i = 0; i < 16; i += 4) {
-                            const int e = 32 * t + 2 * i + 4 * h;
-                            const uint8_t* w = sV + y * L::RB + L::vslot(y, e * L::ES / 16) * 16 + e * L::ES % 16;
-                            float x[4];
-                            if constexpr (KIND == A_F32) {
-                                const float4 f = *reinterpret_cast<const float4*>(w);
-                                x[0] = f.x; x[1] = f.y; x[2] = f.z; x[3] = f.w;
-                            } else {
-                                const uint2 f = *reinterpret_cast<const uint2*>(w);
-                                x[0] = __uint_as_float(f.x << 16); x[1] = __uint_as_float(f.x & 0xFFFF0000u);
-                                x[2] = __uint_as_float(f.y << 16); x[3] = __uint_as_float(f.y & 0xFFFF0000u);
-                            }
-#pragma unroll
-                            for (int j = 0; j < 4; ++j)   // x - x: 0, or NaN
-                                o[t][i + j] += (add & (x[j] - x[j] != 0.f)) ? x[j] : 0.f;
-                        }
-                }
-                __syncthreads();
-                mend(true);
-                __syncthreads();
-            }
-        }
-
-        // the registers that 256 elements leave hold no sixteen places
-        if constexpr (D == 256) asm volatile("" : "+v"(kat), "+v"(vat));
-
-        // scores: lane (r, h) gets row r, tokens 32 t + 8 (i / 4) + 4 h + i % 4
-        f32x16 z[NT];
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            z[t] = zeros16();
-#pragma unroll
-            for (int c = 0; c < NQ; ++c) {
-                const uint4 kf = *reinterpret_cast<const uint4*>(sK + (kat ^ (32 * c)) + 32 * t * L::RB);
+            for (int i = 0; i < 16; i += 4) {
+                const int e = 32 * t + 2 * i + 4 * h;
+                const uint8_t* w = tile + y * L::RB + L::vslot(y, e * L::ES / 16) * 16 + e * L::ES % 16;
+                float x[4];
                 if constexpr (KIND == A_F32) {
-                    const uint32_t kw[4] = {kf.x, kf.y, kf.z, kf.w}, qw[4] = {qf[c].x, qf[c].y, qf[c].z, qf[c].w};
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        z[t] = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(kw[e]), __uint_as_float(qw[e]), z[t],
-                                                                    0, 0, 0);
+                    const float4 f = *reinterpret_cast<const float4*>(w);
+                    x[0] = f.x; x[1] = f.y; x[2] = f.z; x[3] = f.w;
                 } else {
-                    z[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, kf),
-                                                                   __builtin_bit_cast(bf16x8, qf[c]), z[t], 0, 0, 0);
+                    const uint2 f = *reinterpret_cast<const uint2*>(w);
+                    x[0] = __uint_as_float(f.x << 16); x[1] = __uint_as_float(f.x & 0xFFFF0000u);
+                    x[2] = __uint_as_float(f.y << 16); x[3] = __uint_as_float(f.y & 0xFFFF0000u);
                 }
+#pragma unroll
+                for (int j = 0; j < 4; ++j)   // x - x: 0, or NaN
+                    o[t][i + j] += (add & (x[j] - x[j] != 0.f)) ? x[j] : 0.f;
             }
-            if constexpr (SC) {
-#pragma unroll
-                for (int i = 0; i < 16; i += 4) {
-                    const float4 f = *reinterpret_cast<const float4*>(&sKs[buf][32 * t + 2 * i + 4 * h]);
-                    z[t][i] *= f.x; z[t][i + 1] *= f.y; z[t][i + 2] *= f.z; z[t][i + 3] *= f.w;
-                }
-            }
-        }
-        if (!mine) {
-#pragma unroll
-            for (int t = 0; t < NT; ++t)
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    z[t][i] = sees(2 * t + i / 8, 8 * (i / 4 % 2) + 4 * h + i % 4) ? z[t][i] : -INFINITY;
-        }
-        // The reference moves (and what was summed is rescaled) only when a
-        // score exceeds it by 8 powers of two.
-        float top = -INFINITY;
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) top = fmaxf(top, z[t][i]);
-        top *= zs;
-        if (__any(top > m + 8.f)) {
-            const float mn = fmaxf(m, max_halves(top));
-            const float alpha = __builtin_amdgcn_exp2f(m - (mn == -INFINITY ? 0.f : mn));
-            m = mn;
-            l *= alpha;
-            lx *= alpha;
-#pragma unroll
-            for (int t = 0; t < ND; ++t)
-#pragma unroll
-                for (int i = 0; i < 16; ++i) o[t][i] *= alpha;
-        }
-        const float ms = m == -INFINITY ? 0.f : m;
-        uint32_t pb[KIND == A_F32 ? 1 : NT * 8];
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) z[t][i] = __builtin_amdgcn_exp2f(fmaf(z[t][i], zs, -ms));
-            if (!BF || a.lse) {
-                float& sum = BF ? lx : l;
-#pragma unroll
-                for (int i = 0; i < 16; i += 4) sum += (z[t][i] + z[t][i + 1]) + (z[t][i + 2] + z[t][i + 3]);
-            }
-            if constexpr (KIND != A_F32) {
-#pragma unroll
-                for (int i = 0; i < 16; i += 4) {
-                    float y[4] = {z[t][i], z[t][i + 1], z[t][i + 2], z[t][i + 3]};
-                    if constexpr (SC) {
-                        const float4 f = *reinterpret_cast<const float4*>(&sVs[buf][32 * t + 2 * i + 4 * h]);
-                        y[0] *= f.x; y[1] *= f.y; y[2] *= f.z; y[3] *= f.w;
-                        if (!mine) {   // a scale that is not finite, of a token that is not seen
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) y[e] = z[t][i + e] == 0.f ? 0.f : y[e];
-                        }
-                    }
-                    pb[8 * t + i / 2] = pack_bf16x2(y[0], y[1]);
-                    pb[8 * t + i / 2 + 1] = pack_bf16x2(y[2], y[3]);
-                    if constexpr (BF) {
-                        // summed as they enter the product, so that their rounding
-                        // cancels: equal values come back as themselves
-                        typedef __bf16 pair __attribute__((ext_vector_type(2)));
-                        const pair one = {(__bf16)1.f, (__bf16)1.f};
-                        l = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(pair, pb[8 * t + i / 2]), one, l, false);
-                        l = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(pair, pb[8 * t + i / 2 + 1]), one, l, false);
-                    }
-                }
-            }
-        }
-
-        // values: V^T fragments of 32 elements by 16 tokens
-        const auto vfrag = [&](int t, int s) {   // elements 32 t + lane % 32, tokens 16 s + 8 (j / 4) + 4 h + j % 4
-            typedef short s16x4 __attribute__((ext_vector_type(4)));
-            uint4 f;
-            uint32_t w[4];
-#pragma unroll
-            for (int y = 0; y < 2; ++y) {
-                // the 16 lanes of a group read four rows of 16 elements, lane i row
-                // i / 4 and elements 4 (i % 4) .. + 3, and get element i of each
-                const uint8_t* p = sV + (vat ^ (64 * t + 32 * y)) + (16 * s + 8 * y) * L::RB;
-                const uint2 x = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                                                              (__attribute__((address_space(3))) s16x4*)p));
-                w[2 * y] = x.x;
-                w[2 * y + 1] = x.y;
-            }
-            f = make_uint4(w[0], w[1], w[2], w[3]);
-            return f;
-        };
-        const auto vword = [&](int t, int i) {   // fp32: element 32 t + lane % 32 of token 8 (i / 4) + 4 h + i % 4
-            const int vr = 8 * (i / 4) + 4 * h + i % 4, e = 32 * t + r;
-            return *reinterpret_cast<const float*>(sV + vr * L::RB + L::vslot(vr, e / 4) * 16 + (e % 4) * 4);
-        };
-#pragma unroll
-        for (int t = 0; t < ND; ++t) {
-            if constexpr (KIND == A_F32) {
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    o[t] = __builtin_amdgcn_mfma_f32_32x32x2f32(vword(t, i), z[0][i], o[t], 0, 0, 0);
-            } else {
-#pragma unroll
-                for (int s = 0; s < NB; ++s)
-                    o[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-                        __builtin_bit_cast(bf16x8, vfrag(t, s)),
-                        __builtin_bit_cast(bf16x8, make_uint4(pb[4 * s], pb[4 * s + 1], pb[4 * s + 2], pb[4 * s + 3])),
-                        o[t], 0, 0, 0);
-            }
-        }
-        if (more) store(oK, oV, buf ^ 1);
-    };
-    for (int v = v0; v < v1; v += 2 * TILE) {
-        step(v, 0, sK0, sV0, sK1, sV1);
-        if (v + TILE < v1) step(v + TILE, 1, sK1, sV1, sK0, sV0);
     }
+    __syncthreads();
+    find_not_finite<KIND, D, true>(tile, row0);
+    __syncthreads();
+}
 
-    // o[t][i] of lane (r, h) is row r, element 32 t + 8 (i / 4) + 4 h + i % 4
+// Writes a wave's rows: results where the block is in one part, else its sums.
+// o[t][i] of lane (r, h) is row r, element 32 t + 8 (i / 4) + 4 h + i % 4; l and lx
+// are halves of the row's.
+template <int KIND, int D>
+BEAM_DEV void write_rows(const AttnPromptArgs& a, const Block& k, const Rows& x, size_t slot, int head, int wave,
+                         f32x16 (&o)[D / 32], float m, float l, float lx) {
+    const int lane = threadIdx.x & 63, h = lane >> 5;
     l = sum_halves(l);
-    lx = BF ? sum_halves(lx) : l;
-    const int my = k.row0 + wave * 32 + r;
+    lx = sum_halves(lx);
     if (k.np > 1) {
-        const size_t at_row = ((size_t)slot * a.Hkv + head) * kPromptRows + wave * 32 + r;
-        if (my < k.row1) {
+        const size_t at = (slot * a.Hkv + head) * kPromptRows + wave * 32 + (lane & 31);
+        if (!x.live) return;
 #pragma unroll
-            for (int t = 0; t < ND; ++t)
+        for (int t = 0; t < D / 32; ++t)
 #pragma unroll
-                for (int i = 0; i < 16; i += 4)
-                    *reinterpret_cast<float4*>(a.parts + at_row * D + 32 * t + 2 * i + 4 * h) =
-                        make_float4(o[t][i], o[t][i + 1], o[t][i + 2], o[t][i + 3]);
-            if (h == 0) a.ml[at_row] = make_float4(m, l, lx, 0.f);
-        }
+            for (int i = 0; i < 16; i += 4)
+                *reinterpret_cast<float4*>(a.parts + at * D + 32 * t + 2 * i + 4 * h) =
+                    make_float4(o[t][i], o[t][i + 1], o[t][i + 2], o[t][i + 3]);
+        if (h == 0) a.ml[at] = make_float4(m, l, lx, 0.f);
         return;
     }
     const float inv = l == 0.f ? 0.f : 1.0f / l;
-    const size_t out = ((size_t)(k.first + qi) * a.Hq + head * G + qg);
-    if constexpr (KIND == A_F32) {
-        if (my < k.row1) {
+    const size_t out = (size_t)(k.first + x.qi) * a.Hq + head * a.G + x.qg;
 #pragma unroll
-            for (int t = 0; t < ND; ++t)
+    for (int t = 0; t < D / 32; ++t) {
+        if constexpr (KIND == A_F32) {
 #pragma unroll
-                for (int i = 0; i < 16; i += 4)
+            for (int i = 0; i < 16; i += 4)
+                if (x.live)
                     *reinterpret_cast<float4*>(static_cast<float*>(a.out) + out * D + 32 * t + 2 * i + 4 * h) =
                         make_float4(o[t][i] * inv, o[t][i + 1] * inv, o[t][i + 2] * inv, o[t][i + 3] * inv);
-        }
-    } else {
-        // halves exchange four elements each, so that a lane stores eight in a row
-#pragma unroll
-        for (int t = 0; t < ND; ++t)
+        } else {
+            // halves exchange four elements each, so that a lane stores eight in a row
 #pragma unroll
             for (int i = 0; i < 16; i += 8) {
                 uint32_t w[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
                     w[e] = pack_bf16x2(o[t][i + 2 * e] * inv, o[t][i + 2 * e + 1] * inv);
-                const auto x = __builtin_amdgcn_permlane32_swap(w[0], w[2], false, false);
-                const auto y = __builtin_amdgcn_permlane32_swap(w[1], w[3], false, false);
-                if (my < k.row1)
+                const auto y = __builtin_amdgcn_permlane32_swap(w[0], w[2], false, false);
+                const auto z = __builtin_amdgcn_permlane32_swap(w[1], w[3], false, false);
+                if (x.live)
                     *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + out * D + 32 * t + 2 * i + 8 * h) =
-                        make_uint4(x[0], y[0], x[1], y[1]);
+                        make_uint4(y[0], z[0], y[1], z[1]);
             }
+        }
     }
-    if (a.lse && h == 0 && my < k.row1) a.lse[out] = lx == 0.f ? -INFINITY : m * kLn2 + logf(lx);
+    if (a.lse && h == 0 && x.live) a.lse[out] = lx == 0.f ? -INFINITY : m * kLn2 + logf(lx);
 }
 
 // Join of a block's parts: a workgroup per (block, key-value head, 256 / (D / 4)
@@ -687,20 +444,14 @@ __global__ __launch_bounds__(256) void beam_attn_prompt_join(AttnPromptArgs a) {
     if (a.lse && d == 0) a.lse[out] = Lx == 0.f ? -INFINITY : M * kLn2 + logf(Lx);
 }
 
-template <int KIND, int D> static hipError_t launch_prompt(const AttnPromptArgs& a, hipStream_t st) {
+template <int KIND, int D, typename K> hipError_t launch_prompt(K kernel, const AttnPromptArgs& a, hipStream_t st) {
     const unsigned more = a.p.every ? 0 : (unsigned)a.B * (a.p.S - 1);
     const dim3 grid((a.p.blocks + more) * a.Hkv, a.p.every ? a.p.S : 1);
-    const hipError_t err = launch(beam_attn_prompt<KIND, D>, grid, dim3(256), st, a);
+    const hipError_t err = launch(kernel, grid, dim3(256), st, a);
     if (err != hipSuccess || a.p.S == 1) return err;
     constexpr unsigned PER = kPromptRows / (256 / (D / 4));
     return launch(beam_attn_prompt_join<KIND, D>, dim3((a.p.every ? a.p.blocks : (unsigned)a.B) * a.Hkv * PER),
                   dim3(256), st, a);
-}
-
-template <int KIND> static hipError_t launch_prompt_d(const AttnPromptArgs& a, hipStream_t st) {
-    if (a.D == 64) return launch_prompt<KIND, 64>(a, st);
-    if (a.D == 128) return launch_prompt<KIND, 128>(a, st);
-    return launch_prompt<KIND, 256>(a, st);
 }
 
 }  // namespace beam

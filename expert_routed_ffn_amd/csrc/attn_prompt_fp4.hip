@@ -1,5 +1,5 @@
 // Attention of new tokens over a 4-bit cache.
-#include "attn_prompt.h"
+#include "attn_prompt_bf16.h"
 
 namespace beam {
 
