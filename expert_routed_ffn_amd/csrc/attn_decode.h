@@ -32,8 +32,13 @@
 
 namespace beam {
 
-// Tokens per wave step, by cache element.
-template <int KIND> constexpr int tile_tokens() { return KIND == A_F32 ? 16 : 32; }
+// Tokens per wave step, by cache element.  4 bits take twice as many, which are
+// as few bytes (64 sequences of 1 .. 32768 tokens: 175 us with 64, 177 with 32; one
+// of 131072: 32.4 and 33.3), but at D = 256, where their registers are too many (64
+// sequences of 8192: 334 and 282).
+template <int KIND, int D> constexpr int tile_tokens() {
+    return KIND == A_F32 ? 16 : KIND == A_FP4 && D < 256 ? 64 : 32;
+}
 
 // Parts of a sequence, chosen on the device from its own length: `want` even
 // ones, of kMinPart to kMaxPart tokens; `want` is what gives kWantWG workgroups
@@ -295,11 +300,14 @@ template <int D, int QT> struct Acc {
 // With 32 queries a wave, or heads of 256, the registers are held to two waves
 // per SIMD (64 queries on one head, e4m3: 61 -> 52 us; D = 256, 253 windows of 128,
 // e4m3: 51 -> 32 us); fp32 would spill there (129 -> 146 us), and else what the
-// compiler takes is best.
+// compiler takes is best.  4 bits are held to three waves (64 sequences of 8192:
+// 119 -> 111 us), since vector instructions bound them.
+template <int KIND, int D, int QT> constexpr int decode_waves() {
+    return KIND == A_FP4 && QT == 1 && D < 256 ? 3 : KIND != A_F32 && (QT == 2 || D == 256) ? 2 : 1;
+}
 template <int KIND, int D, int QT, bool LISTED, bool SINKS>
-__global__ __launch_bounds__(256, KIND != A_F32 && (QT == 2 || D == 256) ? 2 : 1) void beam_attn_decode(AttnDecodeArgs a,
-                                                                                         int qgroups) {
-    constexpr int TILE = tile_tokens<KIND>(), NU = TILE / 16;   // 16-token blocks per step
+__global__ __launch_bounds__(256, (decode_waves<KIND, D, QT>())) void beam_attn_decode(AttnDecodeArgs a, int qgroups) {
+    constexpr int TILE = tile_tokens<KIND, D>(), NU = TILE / 16;   // 16-token blocks per step
     constexpr int STEP = 4 * TILE;                              // tokens per workgroup step
     constexpr int EB = KIND == A_F32 ? 32 : (KIND == A_BF16 ? 16 : (KIND == A_FP8 ? 8 : 4));   // bits per cache element
     constexpr int RB = D * EB / 8;                              // bytes per cache row
@@ -490,7 +498,7 @@ __global__ __launch_bounds__(256, KIND != A_F32 && (QT == 2 || D == 256) ? 2 : 1
                         w[3] = e4m3_hi(key(c, 1));
                     } else {
                         // fragments 4n .. 4n + 3 share a block of 32 (and a quarter, at D = 256, is two)
-                        const float f = e8m0(SB == 8 ? (kb[u] >> (8 * (c / 4))) & 0xFF : kb[u]);
+                        const float f = __uint_as_float(kb[u] << (23 - 8 * (c / 4)));
                         w[0] = e2m1_pair<0>(key(c, 0), f);
                         w[1] = e2m1_pair<1>(key(c, 0), f);
                         w[2] = e2m1_pair<2>(key(c, 0), f);
@@ -521,7 +529,7 @@ __global__ __launch_bounds__(256, KIND != A_F32 && (QT == 2 || D == 256) ? 2 : 1
                     const int blk = r * DL / 32;
                     uint32_t w = vb[u][SB * i / 4];
                     if constexpr (SB == 8) w = blk & 4 ? vb[u][2 * i + 1] : w;
-                    vf[u][i] = e8m0(w >> (8 * (SB * i % 4 + (blk & 3))) & 0xFF);
+                    vf[u][i] = __uint_as_float(__builtin_amdgcn_alignbit(w, w, 9 + 8 * (SB * i % 4 + (blk & 3))));
                 }
         }
         if (!full) {

@@ -18,7 +18,10 @@ h(bf16) (A + |out|) (1 + 2 h(bf16)); over e4m3 caches p_j times the value's scal
 that + (2 e + c) A + h(dtype) |out|, and lse, whose sum is of the probabilities
 as they were, by e + c + u |lse|.
 
-Decode: the bound of tests/test_gpu_attn.py.
+Decode: the bound of tests/test_gpu_attn.py, with a probability as two bf16
+parts (2^-15 off).  Below the least normal number a rounding is not off by a
+share of the value but by half the step there, which adds 2^-134 (bf16, least step
+2^-133) to a result's bound.
 
 4-bit codes: an element's scaling is by a power of two and its rounding the
 definition's, so codes and scales of given rows are equal, byte for byte; of
@@ -494,7 +497,7 @@ def check_decode(cfg, kind, q, c, vals, table, lens, max_len, name):
         Z = cfg.softmax_scale * max((np.abs(qb[h]) @ np.abs(kr[:, h]).T).max() for h in range(hkv)) if len(kr) else 0.0
         e, n = (D / 4 + 8) * U * Z, (len(kr) / 32 + 64) * U
         half_p = 0.0 if kind == "f32" else 2.0 ** -15 + 2 * U
-        bound = (half_p + 2 * e + n) * mag.reshape(hq, D) + HALF[q.dtype] * np.abs(o.reshape(hq, D))
+        bound = (half_p + 2 * e + n) * mag.reshape(hq, D) + HALF[q.dtype] * np.abs(o.reshape(hq, D)) + 2.0 ** -134
         worst = max(worst, (np.abs(got[b] - o.reshape(hq, D)) - bound).max())
         z = z.reshape(hq)
         if not len(kr):
@@ -566,6 +569,30 @@ def test_decode_garbage_where_it_does_not_see(kind, window, sinks):
     t2[0, 2], t2[0, 5], t2[1, :] = -1, n_pages, 1 << 20
     c, vals = filled(cfg, n_pages, kind, 81)
     check_decode(cfg, kind, q[:4], c, vals, t2, lens2, 112, "bad pages")
+
+
+@pytest.mark.parametrize("hq,hkv,D", [(6, 1, 64), (48, 8, 128), (40, 1, 128), (4, 2, 256)])
+def test_decode_of_uneven_queries_over_four_bits(hq, hkv, D):
+    """Queries whose elements span many powers of two, huge and tiny ones, all zeros; and what is not finite."""
+    P, L = 16, 70
+    cfg = beam.AttnCfg(hq, hkv, D, 0, False, 0, P, softmax_scale=1.0)
+    c, vals = filled(cfg, 6, "fp4", 95)
+    table = base.tables([L] * 6, P, 30, 96, 5) % 6
+    g = gen(97)
+    q = torch.randn((6, hq, D), generator=g, device=DEV)
+    q[0] *= torch.exp2(torch.randint(-30, 1, q[0].shape, generator=g, device=DEV).float())
+    q[1] *= 2.0 ** -60
+    q[2, :, ::32] = 100.0
+    q[3] = 0
+    q[4] *= torch.exp2(torch.randint(-140, -100, q[4].shape, generator=g, device=DEV).float())
+    check_decode(cfg, "fp4", q.to(torch.bfloat16), c, vals, table, [L] * 6, L, "uneven queries")
+    q[5, hq - 1, D - 1] = float("nan")
+    out = torch.empty((6, hq, D), dtype=torch.bfloat16, device=DEV)
+    beam.beam_moe_attn_decode(cfg, q.to(torch.bfloat16), c, i32(table), i32([L] * 6), L, out, beam.attn_workspace(cfg, 6, L))
+    want = np.zeros((6, hq), bool)
+    want[5, hq - 1] = True
+    assert np.array_equal(torch.isnan(out).all(-1).cpu().numpy(), want)
+    assert np.array_equal(torch.isnan(out).any(-1).cpu().numpy(), want)
 
 
 def test_sinks_without_a_window_say_nothing():
