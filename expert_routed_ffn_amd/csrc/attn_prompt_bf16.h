@@ -14,7 +14,7 @@ namespace beam {
 // has.  A tile of 64 tokens is two blocks: the workgroup meets once per tile t,
 // when the keys of tile t and the values of tile t - 1 have landed in LDS, and
 // then starts the loads of the keys of tile t + 1 and the values of tile t.
-template <int KIND, int D>
+template <int KIND, int D, bool FEW>
 __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void beam_attn_prompt(AttnPromptArgs a) {
     using L = Lds<KIND, D>;
     using S = Stage<KIND, D>;
@@ -27,6 +27,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void beam_attn_prompt(AttnPr
     // of tile t at t % 4: e4m3 scales, and which waves' rows there are (a byte each)
     __shared__ __attribute__((aligned(16))) float sKs[4][SC ? TILE : 4], sVs[4][SC ? TILE : 4];
     __shared__ uint32_t sThere[4];
+    __shared__ float sJoin[2][3][FEW ? 64 : 1];
     __shared__ int sBad;
 
     const int lane = threadIdx.x & 63;
@@ -40,7 +41,16 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void beam_attn_prompt(AttnPr
     const int v0 = k.base + part * k.part;
     const int v1 = part + 1 < k.np ? v0 + k.part : k.end;
     const int tiles = (v1 - v0 + TILE - 1) / TILE;
-    const Rows row = rows_of(a, k, wave);
+    // FEW: of a block of up to 64 rows waves 0, 1 take the rows with the first 32
+    // tokens of a tile, waves 2, 3 with the others, and are joined at the end.  Half
+    // the waves would be idle else: bf16, 4 sequences of 8 drafted tokens over
+    // 32768, 67.7 -> 56.6 us; 200 single tokens and 4 chunks over e4m3 152 -> 119.
+    // Both loops in one kernel cost long prompts registers (16384 tokens 3.30 ->
+    // 3.37 ms, e4m3 windows 170 -> 197 us), so those have one without.  At D = 256
+    // it gains nothing (35.6 -> 36.0 us at 16 of 64 tokens).
+    const bool halves = FEW && k.row1 - k.row0 <= 64;
+    const int rg = halves ? wave & 1 : wave, ts = halves ? wave >> 1 : 0;
+    const Rows row = rows_of(a, k, rg);
     bf16x8 qf[NM];
     {
         const uint4* q = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) +
@@ -255,20 +265,6 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void beam_attn_prompt(AttnPr
                 }
             }
         }
-#ifdef SGB
-        if constexpr (QK() && SM() && PV()) {
-            constexpr int kMfma = 8, kValu = 2, kDsRead = 0x100;
-#pragma unroll
-            for (int j = 0; j < NM; ++j) {
-                __builtin_amdgcn_sched_group_barrier(kMfma, 1, 0);
-                if (j + 2 < NM) __builtin_amdgcn_sched_group_barrier(kDsRead, 1, 0);
-                __builtin_amdgcn_sched_group_barrier(kValu, SGB / 2, 0);
-                __builtin_amdgcn_sched_group_barrier(kMfma, 1, 0);
-                if (j + 2 < NM) __builtin_amdgcn_sched_group_barrier(kDsRead, 2, 0);
-                __builtin_amdgcn_sched_group_barrier(kValu, SGB - SGB / 2, 0);
-            }
-        }
-#endif
         if constexpr (SM()) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) asm volatile("" : "+v"(po[i]));   // the probabilities are formed here, not where they are used
@@ -297,7 +293,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void beam_attn_prompt(AttnPr
         store_keys(0, sK0);
     }
     // tile t: keys at sK, the values of tile t - 1 at sV; oK and oV fill
-    const auto turn = [&](int t, auto FIRST, auto LAST, uint8_t* sK, uint8_t* sV, uint8_t* oK,
+    const auto turn = [&](int t, auto HALVES, auto FIRST, auto LAST, uint8_t* sK, uint8_t* sV, uint8_t* oK,
                           uint8_t* oV) __attribute__((always_inline)) {
         __builtin_amdgcn_s_waitcnt(0);   // this wave's loads to LDS have landed
         __syncthreads();                 // everyone's, and no one reads the other buffers any more
@@ -316,7 +312,16 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void beam_attn_prompt(AttnPr
                 mend_values<KIND, D>(sV, wave, t, &sBad, o, [&](int y) {
                     return (seen16(before, y / 16) >> (y & 15) & 1) != 0;
                 });
-        if constexpr (FIRST()) {
+        if constexpr (HALVES()) {
+            const uint8_t *kh = sK + ts * 32 * L::RB, *vh = sV + ts * 32 * L::RB;
+            if constexpr (LAST()) {
+                step(no, no, yes, kh, vh, zB, zA, pA, pB, before, t - 1, 0);
+            } else {
+                if constexpr (FIRST()) step(yes, no, no, kh, vh, zB, zA, pA, pB, before, t - 1, 0);
+                else step(yes, no, yes, kh, vh, zB, zA, pA, pB, before, t - 1, 0);
+                step(no, yes, no, kh, vh, zA, zB, pB, pA, now, t, ts);
+            }
+        } else if constexpr (FIRST()) {
             step(yes, no, no, sK, sV, zB, zA, pA, pB, before, t - 1, 1);
             step(yes, yes, no, sK + 32 * L::RB, sV, zA, zB, pB, pA, now, t, 0);
         } else if constexpr (LAST()) {
@@ -334,27 +339,72 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void beam_attn_prompt(AttnPr
     };
     // tile t's keys are in buffer t % 2, its values too: they are loaded in turn t
     // and used in turn t + 1
-    if (tiles > 0) {
-        turn(0, yes, no, sK0, sV1, sK1, sV0);
+    if (FEW && halves && tiles > 0) {
+        if constexpr (FEW) {
+        turn(0, yes, yes, no, sK0, sV1, sK1, sV0);
         int t = 1;
         for (; t + 1 < tiles; t += 2) {
-            turn(t, no, no, sK1, sV0, sK0, sV1);
-            turn(t + 1, no, no, sK0, sV1, sK1, sV0);
+            turn(t, yes, no, no, sK1, sV0, sK0, sV1);
+            turn(t + 1, yes, no, no, sK0, sV1, sK1, sV0);
         }
         if (t < tiles) {
-            turn(t, no, no, sK1, sV0, sK0, sV1);
-            turn(t + 1, no, yes, sK0, sV1, sK1, sV0);
+            turn(t, yes, no, no, sK1, sV0, sK0, sV1);
+            turn(t + 1, yes, no, yes, sK0, sV1, sK1, sV0);
         } else {
-            turn(t, no, yes, sK1, sV0, sK0, sV1);
+            turn(t, yes, no, yes, sK1, sV0, sK0, sV1);
+        }
+        }
+    } else if (tiles > 0) {
+        turn(0, no, yes, no, sK0, sV1, sK1, sV0);
+        int t = 1;
+        for (; t + 1 < tiles; t += 2) {
+            turn(t, no, no, no, sK1, sV0, sK0, sV1);
+            turn(t + 1, no, no, no, sK0, sV1, sK1, sV0);
+        }
+        if (t < tiles) {
+            turn(t, no, no, no, sK1, sV0, sK0, sV1);
+            turn(t + 1, no, no, yes, sK0, sV1, sK1, sV0);
+        } else {
+            turn(t, no, no, yes, sK1, sV0, sK0, sV1);
         }
     }
-    write_rows<KIND, D>(a, k, row, slot, head, wave, o, m, l, BF ? lx : l);
+    if (halves) {
+        // waves 2 and 3 hand over what they have, lane by lane, in the tiles' memory
+        static_assert(L::BYTES == 32 * D * sizeof(float), "a wave's sums fit a tile");
+        float* mem = reinterpret_cast<float*>(rg ? sV0 : sK0) + lane;
+        __syncthreads();
+        if (ts) {
+#pragma unroll
+            for (int e = 0; e < ND; ++e)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) mem[(16 * e + i) * 64] = o[e][i];
+            sJoin[rg][0][lane] = m;
+            sJoin[rg][1][lane] = l;
+            sJoin[rg][2][lane] = lx;
+        }
+        __syncthreads();
+        if (ts) return;
+        const float m1 = sJoin[rg][0][lane], mn = fmaxf(m, m1), ms = mn == -INFINITY ? 0.f : mn;
+        const float f0 = __builtin_amdgcn_exp2f(m - ms), f1 = __builtin_amdgcn_exp2f(m1 - ms);
+        m = mn;
+        l = fmaf(f1, sJoin[rg][1][lane], f0 * l);
+        lx = fmaf(f1, sJoin[rg][2][lane], f0 * lx);
+#pragma unroll
+        for (int e = 0; e < ND; ++e)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[e][i] = fmaf(f1, mem[(16 * e + i) * 64], f0 * o[e][i]);
+    }
+    write_rows<KIND, D>(a, k, row, slot, head, rg, o, m, l, BF ? lx : l);
 }
 
 template <int KIND> hipError_t launch_prompt_d(const AttnPromptArgs& a, hipStream_t st) {
-    if (a.D == 64) return launch_prompt<KIND, 64>(beam_attn_prompt<KIND, 64>, a, st);
-    if (a.D == 128) return launch_prompt<KIND, 128>(beam_attn_prompt<KIND, 128>, a, st);
-    return launch_prompt<KIND, 256>(beam_attn_prompt<KIND, 256>, a, st);
+    if (a.D == 64)
+        return launch_prompt<KIND, 64>(a.p.few ? beam_attn_prompt<KIND, 64, true> : beam_attn_prompt<KIND, 64, false>,
+                                       a, st);
+    if (a.D == 128)
+        return launch_prompt<KIND, 128>(
+            a.p.few ? beam_attn_prompt<KIND, 128, true> : beam_attn_prompt<KIND, 128, false>, a, st);
+    return launch_prompt<KIND, 256>(beam_attn_prompt<KIND, 256, false>, a, st);
 }
 
 }  // namespace beam

@@ -215,6 +215,7 @@ struct PromptSplit {
     uint32_t blocks;        // most blocks there can be, all sequences together
     uint32_t S;             // most parts of a block; 1: no workspace
     bool every;             // every block may be cut; else those that are their sequence's only one
+    bool few;               // some blocks may have few rows
     uint32_t nseq;
     uint32_t slots() const { return S > 1 ? (every ? blocks : nseq) * S : 0; }   // parts' places in the workspace
     int64_t groups(int Hkv) const {   // workgroups of a launch
