@@ -332,7 +332,7 @@ beam_status beam_moe_attn_prompt(const beam_moe_attn_cfg* cfg, int32_t n_sinks, 
     a.G = a.Hq / a.Hkv;
     a.D = cfg->head_dim;
     a.max_pages = max_pages;
-    a.window = cfg->window;
+    a.window = cfg->window < beam::kMaxLen ? cfg->window : beam::kMaxLen;   // as far as any; differences of 32 bits hold it
     a.sinks = cfg->window > 0 ? n_sinks : 0;
     a.scale = cfg->softmax_scale;
     a.q = q;

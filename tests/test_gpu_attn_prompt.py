@@ -430,6 +430,25 @@ def test_prompt_over_cache_offsets_beyond_32_bits(kind):
     del c
 
 
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("window", [4096, 1 << 30, (1 << 31) - 1])
+def test_a_window_beyond_every_token_is_none(kind, window):
+    """Also where a sequence has more new tokens than it is long, whose first
+    queries stand before it: a query's position less such a window, counted in
+    32 bits, would come out at their other end."""
+    new, lens = [300, 1, 40, 0, 200], [300, 700, 1000, 5, 70]
+    c0 = beam.AttnCfg(12, 2, 128, 0, False, 0, 16)
+    n_pages = sum(-(-n // 16) for n in lens) + 2
+    c, _ = filled(c0, n_pages, kind, 3)
+    table, off = sequences(new, lens, 16, n_pages, 4)
+    q = torch.randn((int(off[-1]), 12, 128), generator=gen(5), device=DEV).to(act_of(kind))
+    want, wl = run_prompt(c0, q, c, table, off, lens, max(lens))
+    for sinks in (0, 5, 1 << 30):
+        cfg = beam.AttnCfg(12, 2, 128, 0, False, window, 16, sinks=sinks)
+        got, gl = run_prompt(cfg, q, c, table, off, lens, max(lens))
+        assert torch.equal(got, want) and torch.equal(gl, wl), sinks
+
+
 @pytest.mark.parametrize("kind", ["bf16", "fp8", "fp4"])
 def test_prompt_in_a_graph_and_on_two_streams(kind):
     """Captured, replayed with other lengths, offsets and queries, with eager work between; two at once."""
