@@ -43,9 +43,6 @@ struct Block {
 };
 
 BEAM_DEV int prompt_offset(const AttnPromptArgs& a, int b) { return min(max(a.offsets[b], 0), a.T); }
-BEAM_DEV int first_block_at(const AttnPromptArgs& a, int b, int offset) {
-    return (int)((int64_t)offset * a.G / kPromptRows) + b;
-}
 
 // places that the rows of positions p0 .. p1 see
 BEAM_DEV void block_span(const AttnPromptArgs& a, Block& k) {
@@ -156,7 +153,12 @@ template <int KIND, int D> struct Stage {
 
     // rows at `src` (the same for the wave) to rows row0 .. of the LDS tile
     template <bool IS_V> BEAM_DEV void load(const uint8_t* src, const uint8_t* scales, uint8_t* tile, int row0) {
-        const int lane = threadIdx.x & 63;
+        int lane = threadIdx.x & 63;
+        // D = 256: places are formed anew for each tile, not held in registers: those
+        // that spilled waited for the loads in flight (4096 tokens, 32 heads over 4,
+        // bf16 489 -> 371 us, 4 bits 491 -> 444, e4m3 562 -> 547; at D = 128, where
+        // nothing spills in the loop, it costs 3 to 5 %)
+        if constexpr (D == 256) asm volatile("" : "+v"(lane));
         if constexpr (DIRECT) {
 #pragma unroll
             for (int i = 0; i < N; ++i) {
@@ -178,7 +180,8 @@ template <int KIND, int D> struct Stage {
         if constexpr (!DIRECT) {
             constexpr int PR = CB / 16;                    // loads per row
             constexpr int EP = KIND == A_FP8 ? 2 : 4;      // LDS pieces per load
-            const int lane = threadIdx.x & 63;
+            int lane = threadIdx.x & 63;
+            if constexpr (D == 256) asm volatile("" : "+v"(lane));   // places are formed anew, not held
 #pragma unroll
             for (int i = 0; i < N; ++i) {
                 const int p = i * 64 + lane;
@@ -219,7 +222,6 @@ BEAM_DEV f32x16 zeros16() {
     for (int i = 0; i < 16; ++i) z[i] = 0.f;
     return z;
 }
-
 
 // A wave's 32 rows, one to a lane: lanes r and r + 32 hold row r.  Rows past the
 // block's last repeat it.
