@@ -20,7 +20,8 @@
 // HBM bounds it: 2 flops per byte and query at most (e4m3) are far below what
 // the matrix cores give, with the padding of G to 16 columns and the second
 // product's two operands too.  64 sequences of 8192 tokens, 48 heads over 8 of
-// 128: bf16 340 us, 6.3 TB/s; e4m3 181 us, 6.1 TB/s; fp32 670 us, 6.4 TB/s; one
+// 128: bf16 340 us, 6.3 TB/s; e4m3 181 us, 6.1 TB/s; fp32 670 us, 6.4 TB/s; 4 bits
+// 112 us, 5.2 TB/s, with the vector unit, which widens the codes, as busy; one
 // sequence of 131071, bf16: 87 us, 6.1 TB/s (a read-only stream on this card
 // reaches 6.3 with plain loads, 7.0 with non-temporal ones; a copy 4.7).  Small
 // calls are latency: 8 sequences of up to 2048 tokens take 9 us for a chain of

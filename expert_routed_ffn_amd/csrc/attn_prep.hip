@@ -169,7 +169,8 @@ BEAM_DEV void store_cache(void* side, void* scales, size_t row, int e0, float (&
 // the position factor: the rotation R is linear, so both factors wait until
 // after it.  Bound by HBM where there are many tokens (16384 of 48 + 8 + 8 heads
 // of 128, bf16 into e4m3: 97 us, 5.2 TB/s; values and keys alone: 22.7 us, 4.5
-// TB/s; a copy reaches 4.7), by latency where there are few (64: 3.8 us).
+// TB/s; a copy reaches 4.7), by latency where there are few (64: 3.8 us).  Into 4
+// bits: values and keys of 16384 tokens, and back, 40 us in two launches.
 // ---------------------------------------------------------------------------
 template <bool BF, int CK, int D>
 __global__ __launch_bounds__(256) void beam_attn_prep(AttnPrepArgs a, int units, int wpt, int gpw) {
@@ -363,7 +364,8 @@ hipError_t launch_attn_prep(const AttnPrepArgs& a, hipStream_t st) {
 // output rows: each lane finds one row's place in the cache, then groups of
 // D/8 lanes copy one head row of one side at a time, kReadBatch of them with
 // all their loads in flight.  Bound by HBM (91500 rows of 8 heads of 128, e4m3
-// to bf16: 110 us, 5.2 TB/s; one row per workgroup: 137 us; 4 rows and loads
+// to bf16: 110 us, 5.2 TB/s; 4 bits to bf16, 474 MB: 103 us, 4.6 TB/s, most of it
+// the rows written; one row per workgroup: 137 us; 4 rows and loads
 // at a time: 119 us; one head of 128 instead of 8: 17.6 us with the 64 rows it
 // gets, 50 with 8).
 // ---------------------------------------------------------------------------
