@@ -228,7 +228,8 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void beam_attn_prompt(AttnPr
             moved = __any(top > m + 8.f);
             if (__builtin_expect(moved, 0)) {
                 const float mn = fmaxf(m, max_halves(top));
-                alpha = __builtin_amdgcn_exp2f(m - (mn == -INFINITY ? 0.f : mn));
+                // before the first score the sums are 0, or infinite by mend_values
+                alpha = m == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(m - mn);
                 m = mn;
                 l *= alpha;
                 lx *= alpha;
@@ -320,6 +321,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void beam_attn_prompt(AttnPr
         if constexpr (!FIRST())
             if (__builtin_expect(!before.all, 0))
                 mend_values<KIND, D>(sV, wave, t, &sBad, o, [&](int y) {
+                    if (HALVES() && y / 32 != ts) return false;
                     return (seen16(before, y / 16) >> (y & 15) & 1) != 0;
                 });
         if constexpr (HALVES()) {

@@ -118,7 +118,8 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void beam_attn_prompt_f32(At
         top *= zs;
         if (__any(top > m + 8.f)) {
             const float mn = fmaxf(m, max_halves(top));
-            const float alpha = __builtin_amdgcn_exp2f(m - (mn == -INFINITY ? 0.f : mn));
+            // before the first score the sums are 0, or infinite by mend_values
+            const float alpha = m == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(m - mn);
             m = mn;
             l *= alpha;
 #pragma unroll

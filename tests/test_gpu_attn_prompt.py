@@ -281,6 +281,32 @@ def test_values_that_are_not_finite_reach_who_sees_them(kind, hq, hkv, D, window
             assert np.array_equal(a[sees][:, :G, :D - 1], b[sees][:, :G, :D - 1])
 
 
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("hq,hkv,D", [(12, 2, 128), (4, 4, 64), (6, 1, 256)])
+@pytest.mark.parametrize("n,L", [(1, 20), (1, 150), (7, 100), (90, 150), (1, 3000), (200, 200)])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (40, 3), (7, 0)])
+def test_infinite_values_stay_infinite(kind, hq, hkv, D, n, L, window, sinks):
+    """A weight above 0 times an infinite value: also where it is the first
+    token that a row sees, and in one of the halves that pairs of waves take.
+    Scores differ by far less than what makes a weight 0."""
+    P = 16
+    cfg = beam.AttnCfg(hq, hkv, D, 0, False, window, P, softmax_scale=D ** -0.5, sinks=sinks)
+    pages = -(-L // P) + 1
+    c, _ = filled(cfg, pages, kind, 21)
+    table, off = sequences([n], [L], P, pages, 22)
+    q = torch.randn((n, hq, D), generator=gen(23), device=DEV).to(act_of(kind))
+    clean, _ = run_prompt(cfg, q, c, table, off, [L], L)
+    mask = oracle.seen(n, L, window, sinks)
+    for t in sorted({0, L - 1, L - 2, L - 7, max(L - 40, 0), max(L - 41, 0), L // 2}):
+        w, _ = filled(cfg, pages, kind, 21)
+        w.v[table[0, t // P], 0, t % P, 5] = float("-inf" if t % 2 else "inf")
+        got, lse = run_prompt(cfg, q, w, table, off, [L], L)
+        want = f64(clean).copy()
+        rows = np.nonzero(mask[:, t])[0]
+        want[rows, :hq // hkv, 5] = -np.inf if t % 2 else np.inf
+        assert np.array_equal(f64(got), want), t
+
+
 @pytest.mark.parametrize("kind", KINDS)
 def test_prompt_bad_pages_and_lengths(kind):
     say(f"prompt bad pages {kind}")
