@@ -4,8 +4,19 @@
 namespace beam {
 
 // Parts of the blocks' spans.  Few blocks (together fewer than kWantWG
-// workgroups): each may be cut, so that the chip has work.  Many: only a
-// sequence that is one block is, where it would run on long after the others.
+// workgroups, what the chip holds at once at D <= 128): each may be cut, so that
+// the chip has work.  Many: only a sequence that is one block is, where it would
+// run on long after the others, into parts of kLongPart at least and kMostWG
+// workgroups.  (48 heads over 8 of 128, with kWantWG 256, 512, 1024: 4 x 8 tokens
+// over 32768 84, 58, 61 us, 128 over 8192 58, 46, 56.  kMostWG 1024, 2048, 4096: 64
+// single tokens over 8192 and a chunk of 2048 257, 227, 221, 200 of 2000 and 4
+// chunks, e4m3, 120, 119, 143.  kLongPart 512, 1024, 4096: 8 single tokens and 4
+// chunks, 4 bits, 65, 62, 95.)
+//   With more than half of kWantWG, parts are two or three, and cost a join: none
+// where they would be short (one prompt of 700 tokens 30 us in two parts, 22 in
+// one; 1300: 56 and 39; but 1000 over 16384: 463 and 505, 8 of up to 128 over
+// 8192, e4m3, 74 and 97), and single blocks are cut as among many (40 of up to 8
+// tokens over 8192: 121 us with each block cut, 107).
 constexpr int kWantWG = 512, kMostWG = 2048, kLongPart = 1024;
 // Sequences of this many rows in the mean, or fewer, may be single tokens beside a
 // few chunks, whose blocks share their rows between half the waves (64 tokens and 8
@@ -23,12 +34,13 @@ PromptSplit attn_prompt_split(int B, int T, int Hq, int Hkv, int max_len, int wi
         span = seen < span ? seen : span;
     }
     const int64_t wg = (int64_t)p.blocks * Hkv;
-    p.every = wg < kWantWG;
+    const bool half = 2 * wg > kWantWG;
+    p.every = wg < kWantWG && !(half && T * G <= (int64_t)kPromptRows / 2 * B);
     p.few = T * G <= (int64_t)kFewRows * B;
     int64_t s, most;
     if (p.every) {
         s = (kWantWG + wg - 1) / wg;
-        most = (span + kPromptMinPart - 1) / kPromptMinPart;
+        most = half ? span / kLongPart : (span + kPromptMinPart - 1) / kPromptMinPart;
     } else {
         // some sequence may be one block only if there are several
         s = B > 1 ? kMostWG / ((int64_t)B * Hkv) : 1;
