@@ -289,14 +289,19 @@ beam_status beam_moe_attn_decode_sinks(const beam_moe_attn_cfg* cfg, int32_t n_s
     return ran(beam::launch_attn_decode(a, ws, static_cast<hipStream_t>(stream)));
 }
 
+// max_len counts in whole pages: so a workspace for the longest length serves a
+// call that expects what its table holds
+static beam::PromptSplit prompt_split(const beam_moe_attn_cfg& cfg, int32_t n_sinks, int32_t B, int32_t T,
+                                      int32_t max_len) {
+    const int32_t pages = (max_len + cfg.page_size - 1) & -cfg.page_size;   // at most kMaxLen, as max_len is
+    return beam::attn_prompt_split(B, T, cfg.n_heads, cfg.n_kv_heads, pages, cfg.window, n_sinks);
+}
 size_t beam_moe_attn_prompt_workspace_bytes(const beam_moe_attn_cfg* cfg, int32_t n_sinks, int32_t B, int32_t T,
                                             int32_t max_len) {
     if (check_attn_cfg(cfg) != BEAM_OK || B <= 0 || B > kMaxT || T <= 0 || T > kMaxT || max_len < 0 ||
         max_len > beam::kMaxLen || !sinks_ok(n_sinks))
         return 0;
-    return beam::attn_prompt_ws_bytes(cfg->n_kv_heads, cfg->head_dim,
-                                      beam::attn_prompt_split(B, T, cfg->n_heads, cfg->n_kv_heads, max_len,
-                                                              cfg->window, n_sinks));
+    return beam::attn_prompt_ws_bytes(cfg->n_kv_heads, cfg->head_dim, prompt_split(*cfg, n_sinks, B, T, max_len));
 }
 
 beam_status beam_moe_attn_prompt(const beam_moe_attn_cfg* cfg, int32_t n_sinks, int32_t B, int32_t T, const void* q,
@@ -321,7 +326,7 @@ beam_status beam_moe_attn_prompt(const beam_moe_attn_cfg* cfg, int32_t n_sinks, 
     if ((a.c.kind == beam::A_F32) != (dtype == BEAM_F32)) return BEAM_ERR_UNSUPPORTED;
     const size_t es = dtype == BEAM_BF16 ? 2 : 4;
     if (overlap(out, (size_t)T * qw * es, q, span_bytes(T, q_stride, qw, es))) return BEAM_ERR_INVALID_ARG;
-    a.p = beam::attn_prompt_split(B, T, cfg->n_heads, cfg->n_kv_heads, max_len, cfg->window, n_sinks);
+    a.p = prompt_split(*cfg, n_sinks, B, T, max_len);
     if (a.p.groups(cfg->n_kv_heads) >= kMaxGroups) return BEAM_ERR_UNSUPPORTED;
     const size_t need = beam::attn_prompt_ws_bytes(cfg->n_kv_heads, cfg->head_dim, a.p);
     if (need > 0 && (!ws || ws_bytes < need || !aligned16(ws))) return BEAM_ERR_WORKSPACE;

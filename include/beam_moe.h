@@ -590,12 +590,12 @@ size_t beam_moe_attn_decode_sinks_workspace_bytes(const beam_moe_attn_cfg* cfg, 
  *             lse = -inf.  Tokens on a page outside [0, n_pages) are skipped.
  *             A token that a row does not see does not reach its result,
  *             whatever is cached there.
- *   max_len   the longest length to expect, as in beam_moe_attn_decode: few
- *             rows over long sequences are split over it
+ *   max_len   the longest length to expect, as in beam_moe_attn_decode, in
+ *             whole pages: few rows over long sequences are split over it
  *   ws        beam_moe_attn_prompt_workspace_bytes(cfg, n_sinks, B, T, max_len)
- *             bytes for this B, T and max_len, 16-byte aligned (may be null
- *             where that is 0); no initialisation; calls that overlap in time
- *             must not share it.
+ *             bytes for this B, T and max_len (in whole pages), 16-byte aligned
+ *             (may be null where that is 0); no initialisation; calls that
+ *             overlap in time must not share it.
  * (T * n_heads / 128 + B * n_kv_heads below 2^24, BEAM_ERR_UNSUPPORTED.)
  */
 beam_status beam_moe_attn_prompt(const beam_moe_attn_cfg* cfg, int32_t n_sinks, int32_t B, int32_t T, const void* q,

@@ -125,6 +125,18 @@ def test_workspaces(L):
     assert p(65, 2112, 10240) > 0                            # some sequence may be one long block
 
 
+@pytest.mark.parametrize("page", [16, 64, 1024])
+@pytest.mark.parametrize("B,T", [(1, 1), (1, 32), (1, 300), (3, 17), (30, 30), (40, 320)])
+def test_a_workspace_for_the_longest_serves_the_table(L, page, B, T):
+    """max_len counts in whole pages, in the workspace and in the call."""
+    for n in (1, 255, 256, 257, 1000, 1024, 1025, 5000, (1 << 30) - 1):
+        c, whole = cfg(page_size=page), -(-n // page) * page
+        need = L.beam_moe_attn_prompt_workspace_bytes(c.c(), 0, B, T, n)
+        assert need == L.beam_moe_attn_prompt_workspace_bytes(c.c(), 0, B, T, whole)
+        if need:
+            assert prompt(L, c, B=B, T=T, ml=whole, ws=A * 6, wsb=need - 1) == 3
+
+
 @pytest.mark.parametrize("hq,hkv", [(48, 8), (64, 1), (1, 1), (256, 256), (16384, 256)])
 @pytest.mark.parametrize("B,T", [(1, 1), (1, 1 << 22), (7, 5), (300, 300), (1 << 22, 1 << 22), (1 << 22, 1), (4096, 70000)])
 @pytest.mark.parametrize("n,window,sinks", [(0, 0, 0), (1 << 30, 0, 0), (1 << 30, 1 << 20, 1 << 30), (1 << 30, 1, 1),
