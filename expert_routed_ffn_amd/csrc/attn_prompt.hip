@@ -12,6 +12,11 @@ namespace beam {
 // single tokens over 8192 and a chunk of 2048 257, 227, 221, 200 of 2000 and 4
 // chunks, e4m3, 120, 119, 143.  kLongPart 512, 1024, 4096: 8 single tokens and 4
 // chunks, 4 bits, 65, 62, 95.)
+//   A part is kPromptMinPart tokens at least, of what a block sees in the mean:
+// among a prompt's own tokens half of them (one prompt of 300 tokens 17.1 us in two
+// parts, 12.8 in one; 512: 23.1 and 17.2; but 128 tokens over 500 17.1 in three, 20.1
+// in one).  From a quarter of kWantWG on no part is shorter (2 x 256 tokens, window
+// 512: 25.6 us in three, 20.2 in one).
 //   With more than half of kWantWG, parts are two or three, and cost a join: none
 // where they would be short (one prompt of 700 tokens 30 us in two parts, 22 in
 // one; 1300: 56 and 39; but 1000 over 16384: 463 and 505, 8 of up to 128 over
@@ -40,7 +45,9 @@ PromptSplit attn_prompt_split(int B, int T, int Hq, int Hkv, int max_len, int wi
     int64_t s, most;
     if (p.every) {
         s = (kWantWG + wg - 1) / wg;
-        most = half ? span / kLongPart : (span + kPromptMinPart - 1) / kPromptMinPart;
+        const int64_t n = T / B, mean = span - (n < span ? n : span) / 2;
+        const int64_t up = 4 * wg > kWantWG ? 0 : kPromptMinPart - 1;
+        most = half ? span / kLongPart : (mean + up) / kPromptMinPart;
     } else {
         // some sequence may be one block only if there are several
         s = B > 1 ? kMostWG / ((int64_t)B * Hkv) : 1;
