@@ -5,9 +5,14 @@
 namespace beam {
 
 AttnSplit attn_decode_split(int B, int Hkv, int max_len, int window, int sinks) {
-    // a window's tokens begin inside a 16-token block, and its sinks end in one
-    const int64_t span =
-        window > 0 && window < max_len ? (int64_t)window + 15 + (((int64_t)sinks + 15) & ~(int64_t)15) : max_len;
+    // a window's tokens begin inside a 16-token block, and its sinks end in one;
+    // together no more than there are (64 sequences of up to 1000 tokens in windows
+    // of 512 with 100000 sinks need no workspace, as without a window)
+    int64_t span = window > 0 && window < max_len ? (int64_t)window + 15 : max_len;
+    if (window > 0 && window < max_len && sinks > 0) {
+        span += ((int64_t)sinks + 15) & ~(int64_t)15;
+        span = span < max_len ? span : max_len;
+    }
     const int64_t heads = (int64_t)B * Hkv;
     const auto at_least_1 = [](int64_t v) { return v < 1 ? 1 : v; };
     const auto parts = [&](int of) { return at_least_1((span + of - 1) / of); };
