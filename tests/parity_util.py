@@ -184,3 +184,15 @@ def sample_tokens(T, n, seed=0):
     rng = np.random.default_rng(seed)
     mid = rng.choice(np.arange(1, T - 1), n - 2, replace=False)
     return sorted({0, T - 1, *[int(v) for v in mid]})
+
+
+def over_bound(got, ref, bound):
+    """By how much `got` exceeds `ref` +- `bound` anywhere (at most 0: nowhere);
+    infinite where an element is not finite, or is not to be compared."""
+    got, ref, bound = np.broadcast_arrays(*(np.asarray(x, np.float64) for x in (got, ref, bound)))
+    if got.size == 0:
+        return -math.inf
+    d = np.full(got.shape, math.inf)
+    ok = np.isfinite(got) & np.isfinite(ref) & np.isfinite(bound)
+    d[ok] = np.abs(got[ok] - ref[ok]) - bound[ok]
+    return float(d.max())
