@@ -818,6 +818,9 @@ def attn_workspace(cfg: AttnCfg, B: int, max_len: int, device="cuda") -> torch.T
 
 
 def attn_prompt_workspace(cfg: AttnCfg, B: int, T: int, max_len: int, device="cuda") -> torch.Tensor:
+    """Scratch of a call with this B and T.  Fewer tokens may need more (a few
+    rows are split over the cache, many are not): for calls of several T take
+    the largest."""
     return _bytes(lib().beam_moe_attn_prompt_workspace_bytes(cfg.c(), cfg.sinks, _i32(B, "B"), _i32(T, "T"),
                                                              _i32(max_len, "max_len")), device)
 

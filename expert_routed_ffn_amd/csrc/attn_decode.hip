@@ -33,7 +33,6 @@ size_t attn_decode_ws_bytes(int B, int Hq, int D, const AttnSplit& p) {
     return p.S > 1 ? p.rows * Hq * (D + 2) * sizeof(float) : 0;
 }
 
-
 hipError_t launch_attn_decode(AttnDecodeArgs a, void* ws, hipStream_t st) {
     a.parts = static_cast<float*>(ws);
     if (a.p.extra) {

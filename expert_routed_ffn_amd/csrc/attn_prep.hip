@@ -170,7 +170,8 @@ BEAM_DEV void store_cache(void* side, void* scales, size_t row, int e0, float (&
 // after it.  Bound by HBM where there are many tokens (16384 of 48 + 8 + 8 heads
 // of 128, bf16 into e4m3: 97 us, 5.2 TB/s; values and keys alone: 22.7 us, 4.5
 // TB/s; a copy reaches 4.7), by latency where there are few (64: 3.8 us).  Into 4
-// bits: values and keys of 16384 tokens, and back, 40 us in two launches.
+// bits: 92 us with norm and rotation (e4m3 96, bf16 100); values and keys alone, and
+// back, 40 us in two launches.
 // ---------------------------------------------------------------------------
 template <bool BF, int CK, int D>
 __global__ __launch_bounds__(256) void beam_attn_prep(AttnPrepArgs a, int units, int wpt, int gpw) {

@@ -21,10 +21,12 @@
 // 4 D flops per row and visible token over keys and values that 128 rows share:
 // the matrix cores bound it where prompts are long, with the vector unit beside
 // them (softmax, LDS and staging), HBM where few rows meet a long cache, latency
-// where there is little of both.  48 heads over 8 of 128, bf16: 16384 tokens 3.28
-// ms, 1005 TFLOP/s (a large product reaches 1343); 2048 tokens 66 to 77 us, where
-// workgroups of 1 to 32 tiles do not fill the chip evenly; 4 x 8 tokens over 32768
-// 57 us, 4.4 TB/s; 37 tokens 7 us.  e4m3, 4096 tokens: 252 us, 4 bits 240, bf16 228.
+// where there is little of both.  48 heads over 8 of 128, bf16: 16384 tokens 3.28 to
+// 3.38 ms, 976 to 1005 TFLOP/s (a large product reaches 1343); 2048 tokens 66 to 77
+// us, where workgroups of 1 to 32 tiles do not fill the chip evenly; 4 x 8 tokens
+// over up to 32768 72 us, 3.5 TB/s (253 MB, from HBM; 56 us from the last-level cache, which
+// holds them), on 416 of the 512 workgroups that the chip holds; 37 tokens 7 us.
+// e4m3, 4096 tokens: 252 us, 4 bits 240, bf16 228.
 #pragma once
 
 #include "attn_common.h"

@@ -7,8 +7,8 @@ namespace beam {
 // workgroups, what the chip holds at once at D <= 128): each may be cut, so that
 // the chip has work.  Many: only a sequence that is one block is, where it would
 // run on long after the others, into parts of kLongPart at least and kMostWG
-// workgroups.  (48 heads over 8 of 128, with kWantWG 256, 512, 1024: 4 x 8 tokens
-// over 32768 84, 58, 61 us, 128 over 8192 58, 46, 56.  kMostWG 1024, 2048, 4096: 64
+// workgroups.  (48 heads over 8 of 128, inputs in the last-level cache, with kWantWG
+// 256, 512, 1024: 4 x 8 tokens over 32768 84, 58, 61 us, 128 over 8192 58, 46, 56.  kMostWG 1024, 2048, 4096: 64
 // single tokens over 8192 and a chunk of 2048 257, 227, 221, 200 of 2000 and 4
 // chunks, e4m3, 120, 119, 143.  kLongPart 512, 1024, 4096: 8 single tokens and 4
 // chunks, 4 bits, 65, 62, 95.)
@@ -17,6 +17,12 @@ namespace beam {
 // parts, 12.8 in one; 512: 23.1 and 17.2; but 128 tokens over 500 17.1 in three, 20.1
 // in one).  From a quarter of kWantWG on no part is shorter (2 x 256 tokens, window
 // 512: 25.6 us in three, 20.2 in one).
+//   So among 1024 / Hkv sequences and more a single block is not cut, and a longer
+// one among many never: one token behind 131072 among 63, 127, 128 of 500 (8
+// key-value heads) takes 583, 1142, 2173 us, where decode, which lists parts by the
+// lengths there are, takes 108, 132, 133; 1400 tokens over 32768 are 528 workgroups,
+// hence two rounds of uncut ones: 680 TFLOP/s, where 1000 in parts reach 910 and 2048
+// 962.
 //   With more than half of kWantWG, parts are two or three, and cost a join: none
 // where they would be short (one prompt of 700 tokens 30 us in two parts, 22 in
 // one; 1300: 56 and 39; but 1000 over 16384: 463 and 505, 8 of up to 128 over

@@ -14,7 +14,7 @@ namespace beam {
 // has.  A tile of 64 tokens is two blocks: the workgroup meets once per tile t,
 // when the keys of tile t and the values of tile t - 1 have landed in LDS, and
 // then starts the loads of the keys of tile t + 1 and the values of tile t.
-// (One stage after the other, 16384 tokens: 3.47 ms, so 3.28; e4m3, 4096 tokens:
+// (One stage after the other, 16384 tokens: 3.47 ms, so 3.28 then; e4m3, 4096 tokens:
 // 368 and 253 us.  Two workgroups per CU hold 64 KB of LDS each at D = 128, of two
 // waves per SIMD; at D = 256 a workgroup has 128 KB and the CU to itself.  Blocks
 // of 256 rows on eight waves are 1 to 7 % faster at 16384 tokens and slower below.)
@@ -54,7 +54,8 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void beam_attn_prompt(AttnPr
     // FEW: of a block of up to 64 rows waves 0, 1 take the rows with the first 32
     // tokens of a tile, waves 2, 3 with the others, and are joined at the end.  Half
     // the waves would be idle else: bf16, 4 sequences of 8 drafted tokens over
-    // 32768, 67.7 -> 56.6 us; 200 single tokens and 4 chunks over e4m3 152 -> 119.
+    // 32768 in the last-level cache, 67.7 -> 56.6 us; 200 single tokens and 4 chunks
+    // over e4m3 152 -> 119.
     // Both loops in one kernel cost long prompts registers (16384 tokens 3.30 ->
     // 3.37 ms, e4m3 windows 170 -> 197 us), so those have one without.  At D = 256
     // it gains nothing (35.6 -> 36.0 us at 16 of 64 tokens).
@@ -353,18 +354,18 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void beam_attn_prompt(AttnPr
     // and used in turn t + 1
     if (FEW && halves && tiles > 0) {
         if constexpr (FEW) {
-        turn(0, yes, yes, no, sK0, sV1, sK1, sV0);
-        int t = 1;
-        for (; t + 1 < tiles; t += 2) {
-            turn(t, yes, no, no, sK1, sV0, sK0, sV1);
-            turn(t + 1, yes, no, no, sK0, sV1, sK1, sV0);
-        }
-        if (t < tiles) {
-            turn(t, yes, no, no, sK1, sV0, sK0, sV1);
-            turn(t + 1, yes, no, yes, sK0, sV1, sK1, sV0);
-        } else {
-            turn(t, yes, no, yes, sK1, sV0, sK0, sV1);
-        }
+            turn(0, yes, yes, no, sK0, sV1, sK1, sV0);
+            int t = 1;
+            for (; t + 1 < tiles; t += 2) {
+                turn(t, yes, no, no, sK1, sV0, sK0, sV1);
+                turn(t + 1, yes, no, no, sK0, sV1, sK1, sV0);
+            }
+            if (t < tiles) {
+                turn(t, yes, no, no, sK1, sV0, sK0, sV1);
+                turn(t + 1, yes, no, yes, sK0, sV1, sK1, sV0);
+            } else {
+                turn(t, yes, no, yes, sK1, sV0, sK0, sV1);
+            }
         }
     } else if (tiles > 0) {
         turn(0, no, yes, no, sK0, sV1, sK1, sV0);

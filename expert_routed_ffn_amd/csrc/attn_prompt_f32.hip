@@ -1,6 +1,8 @@
 // Attention of new tokens over an fp32 cache: both products on the fp32 matrix
 // instructions, which bound it (one prompt of 4096 tokens, 48 heads over 8 of 128:
-// 114 TFLOP/s of the 154 that a large fp32 product reaches).
+// 114 TFLOP/s of the 154 that a large fp32 product reaches; 2048: 118).  Blocks of up
+// to 64 rows leave two of the four waves idle: 4 x 8 tokens over up to 32768, 505 MB, take
+// 418 us, 1.2 TB/s.
 #include "attn_prompt.h"
 
 namespace beam {

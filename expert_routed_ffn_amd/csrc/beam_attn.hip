@@ -42,7 +42,8 @@ beam_status check_cache(const beam_moe_attn_cfg* c, const beam_moe_kv_cache* k, 
     if (k->dtype != BEAM_F32 && k->dtype != BEAM_BF16 && k->dtype != BEAM_FP8_E4M3 && k->dtype != BEAM_MXFP4)
         return BEAM_ERR_INVALID_ARG;
     if (!aligned16(k->k) || !aligned16(k->v)) return BEAM_ERR_INVALID_ARG;
-    if ((k->dtype == BEAM_FP8_E4M3 || k->dtype == BEAM_MXFP4) && (!k->k_scale || !k->v_scale || !aligned16(k->k_scale) || !aligned16(k->v_scale)))
+    if ((k->dtype == BEAM_FP8_E4M3 || k->dtype == BEAM_MXFP4) &&
+        (!k->k_scale || !k->v_scale || !aligned16(k->k_scale) || !aligned16(k->v_scale)))
         return BEAM_ERR_INVALID_ARG;
     if ((int64_t)k->n_pages * c->page_size > 0x7FFFFFFF) return BEAM_ERR_UNSUPPORTED;
     int sh = 0;

@@ -595,7 +595,17 @@ size_t beam_moe_attn_decode_sinks_workspace_bytes(const beam_moe_attn_cfg* cfg, 
  *   ws        beam_moe_attn_prompt_workspace_bytes(cfg, n_sinks, B, T, max_len)
  *             bytes for this B, T and max_len (in whole pages), 16-byte aligned
  *             (may be null where that is 0); no initialisation; calls that
- *             overlap in time must not share it.
+ *             overlap in time must not share it.  Fewer tokens may need more:
+ *             a few rows are split over the cache, many are not (one sequence of
+ *             32768, 48 heads over 8 of 128: 33 MiB at T = 1, 65 at 1343, none
+ *             from 1344 on), so a buffer for calls of several T is the largest
+ *             of their sizes, and one too small is BEAM_ERR_WORKSPACE
+ * Single tokens only are beam_moe_attn_decode's: it splits every sequence by its
+ * length.  Here, in calls that fill the device, a sequence of up to 128 rows
+ * (tokens times n_heads / n_kv_heads) is split into 2048 / (B * n_kv_heads) parts
+ * at most, and one of more rows not at all: a token behind a very long cache among
+ * 1024 / n_kv_heads sequences and more is walked through in one part (131072 tokens:
+ * 2.2 ms, in decode 0.13).
  * (T * n_heads / 128 + B * n_kv_heads below 2^24, BEAM_ERR_UNSUPPORTED.)
  */
 beam_status beam_moe_attn_prompt(const beam_moe_attn_cfg* cfg, int32_t n_sinks, int32_t B, int32_t T, const void* q,
